@@ -315,6 +315,124 @@ moe_status moe_route_static(const void *x_bf16, int32_t T, int32_t hidden, const
                             int32_t renormalize, int32_t *topk_ids, float *topk_w, int32_t *expert_offsets,
                             int32_t *sorted_rows, void *stream);
 
+/* ======================================================================
+ * The token path around the experts' products, for callers whose products are
+ * their own (8-bit or bf16 products, training): the layer's norm, the sort of
+ * the (token, slot) pairs by expert, rows to expert order and back, and the
+ * gradients.  These entry points need no plan, allocate nothing, keep nothing
+ * between calls and replay from CUDA graphs.  Rows (x, residual, sum, y, q,
+ * their gradients, weight) are 16-byte aligned, every other array is aligned to
+ * its element.  Row counts, row offsets and strides may pass 32 bits in bytes.
+ * ====================================================================== */
+
+/* Element type of activations and of a norm's weight. */
+typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2 } moe_dtype;
+
+/* 8-bit output of moe_rms_norm.  Codes are E4M3 bytes q[T][H]; a group's scale
+ * is what its codes are multiplied by.
+ *   NONE:     no 8-bit output.
+ *   E4M3_128: groups of 128 consecutive values, fp32 scales [T][ceil(H/128)].
+ *   E4M3_ROW: one group a row, fp32 scales [T].
+ *             For both: a = max(amax of the group, 2^-100), scale = a / 448,
+ *             code = E4M3_rne_sat(n * (448 / a)).  A NaN makes its group NaN.
+ *   MXFP8:    groups of 32, E8M0 scales uint8[T][ceil(H/32)]: byte =
+ *             clamp(floor(log2(amax)) - 8 + 127, 0, 254) (0 for an all-zero
+ *             group), code = E4M3_rne_sat(n * 2^(127 - byte)); a group whose
+ *             amax is not finite gets byte 255 and NaN codes.
+ * The last group of a row is shorter where H is not a multiple of the group. */
+typedef enum {
+    MOE_QUANT_NONE = 0, MOE_QUANT_E4M3_128 = 1, MOE_QUANT_E4M3_ROW = 2, MOE_QUANT_MXFP8 = 3
+} moe_quant8;
+
+/* Residual addition and root-mean-square norm of T rows of H values:
+ *   s = round(x + residual)  (s = x without a residual),
+ *   rstd = 1 / sqrt(mean(s^2) + eps),  n = (s * rstd) * weight  in fp32,
+ *   y = round(n), and/or n in 8 bits (moe_quant8).
+ * The statistic is that of the stored (rounded) sum, summed in fp32: a row
+ * whose sum of squares leaves fp32's range has rstd 0.
+ *   x        [T] rows of H, x_stride elements apart
+ *   residual NULL, or [T] rows of H, residual_stride elements apart
+ *   weight   [H], in `dtype` as x, residual, sum and y are
+ *   sum      NULL, or [T][H] (only with a residual).  May be x's or residual's
+ *            own memory where that one's stride is H.
+ *   y        [T][H]; may be NULL when quant is not MOE_QUANT_NONE
+ *   q, scales  as moe_quant8 says; NULL for MOE_QUANT_NONE
+ *   rstd     NULL, or [T] fp32 (for the backward pass)
+ * H: a multiple of 8 up to 16384; strides: multiples of 8, at least H;
+ * eps > 0 and finite.  T = 0 is a no-op. */
+moe_status moe_rms_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                        const void *weight, int32_t T, int32_t H, int32_t dtype, float eps, int32_t quant,
+                        void *sum, void *y, uint8_t *q, void *scales, float *rstd, void *stream);
+
+/* Gradients of moe_rms_norm's y (and of its sum) for one shared input: with
+ * n = sum * rstd and g = grad_y * weight,
+ *   grad_in = rstd * (g - n * mean(g * n)) + grad_sum   (x's and residual's)
+ *   grad_w  = sum over rows of grad_y * n               (fp32)
+ * grad_y, sum, grad_sum (NULL: none), grad_in: [T][H] of `dtype`; grad_in may
+ * be grad_y's or grad_sum's memory.  weight [H] of `dtype`, rstd [T], grad_w
+ * [H] fp32 (written, not added to).  workspace: device memory of at least
+ * moe_rms_norm_backward_workspace(T, H) bytes, 16-byte aligned, used during
+ * the call only.  Rows are added in a fixed order: the same inputs on the same
+ * device give the same bits.  T = 0 writes grad_w = 0. */
+size_t moe_rms_norm_backward_workspace(int32_t T, int32_t H);
+moe_status moe_rms_norm_backward(const void *grad_y, const void *sum, const void *weight, const float *rstd,
+                                 const void *grad_sum, int32_t T, int32_t H, int32_t dtype, void *grad_in,
+                                 float *grad_w, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Rows of the sorted layout of `pairs` pairs: enough for any routing when
+ * every expert's segment is padded to a multiple of `align` rows, that is
+ * floor((pairs + min(E, pairs) * (align - 1)) / align) * align.  -1 for
+ * arguments moe_sort_pairs refuses. */
+int64_t moe_sorted_rows(int64_t pairs, int32_t num_experts, int32_t align);
+
+/* Stable sort of the pairs p = t*k + j by expert, from any router's ids.
+ *   topk_ids       [T][k] int32; a pair whose id is outside [0, E) is dropped
+ *   expert_offsets [E+1] int32: the first row of every expert's segment; each
+ *                  segment holds its pairs in increasing p, then padding up to
+ *                  a multiple of `align` rows (none for align = 1)
+ *   sorted_rows    [rows] int32: the pair at a row, -1 where there is none
+ *   pair_rows      [T][k] int32: the row of a pair, -1 where it is dropped
+ * rows = moe_sorted_rows(T*k, E, align), at most 2^31 - 1; align a power of
+ * two up to 256; k up to 32; E up to 1024.  With align = 1 and no pair dropped,
+ * expert_offsets and sorted_rows are moe_route's.  T = 0 writes zero offsets. */
+moe_status moe_sort_pairs(const int32_t *topk_ids, int32_t T, int32_t k, int32_t num_experts, int32_t align,
+                          int64_t rows, int32_t *expert_offsets, int32_t *sorted_rows, int32_t *pair_rows,
+                          void *stream);
+
+/* Token rows into expert order: row r of out is token sorted_rows[r] / k's row
+ * of x, and zeros where sorted_rows[r] is -1.  Rows are copied as bytes, so x
+ * is of any type; scales (NULL: none) are rows that go with them, such as
+ * moe_rms_norm's.  Its gradient is moe_combine without weights.
+ *   x      [T] rows of row_bytes, x_stride_bytes apart (multiples of 16)
+ *   scales [T][scale_bytes], out_scales [rows][scale_bytes]
+ *   out    [rows][row_bytes]
+ * sorted_rows and pair_rows are moe_sort_pairs' of the same T, k and rows; an
+ * entry out of range counts as -1. */
+moe_status moe_dispatch(const void *x, int64_t x_stride_bytes, int64_t row_bytes, const void *scales,
+                        int32_t scale_bytes, int32_t T, int32_t k, const int32_t *sorted_rows,
+                        const int32_t *pair_rows, int64_t rows, void *out, void *out_scales, void *stream);
+
+/* Expert rows back into token order:
+ *   out[t] = round(sum over j of weights[t][j] * y[pair_rows[t][j]] + base[t])
+ * in fp32, in increasing j, base last.  Dropped pairs add nothing and rows of
+ * padding are not read; a token without pairs gets base (0 without one).
+ *   y [rows][H], base (NULL: none) and out [T][H] of `dtype`; weights [T][k]
+ *   fp32 or NULL for 1 (the gradient of moe_dispatch).  out may be base's
+ *   memory.  H: a multiple of 8. */
+moe_status moe_combine(const void *y, int32_t dtype, int32_t T, int32_t k, int32_t H, const int32_t *pair_rows,
+                       int64_t rows, const float *weights, const void *base, void *out, void *stream);
+
+/* Gradients of moe_combine (base's is grad_out itself):
+ *   grad_y[r] = round(weights[p] * grad_out[p / k]) for p = sorted_rows[r],
+ *               zeros where that is -1
+ *   grad_weights[t][j] = dot(grad_out[t], y[pair_rows[t][j]]) fp32, 0 where
+ *               the pair is dropped
+ * grad_out [T][H], y and grad_y [rows][H] of `dtype`; grad_y may be y's
+ * memory.  weights, grad_weights [T][k] fp32. */
+moe_status moe_combine_backward(const void *grad_out, const void *y, int32_t dtype, int32_t T, int32_t k, int32_t H,
+                                const int32_t *sorted_rows, const int32_t *pair_rows, int64_t rows,
+                                const float *weights, void *grad_y, float *grad_weights, void *stream);
+
 /* Text of a status code (static storage). */
 const char *moe_status_string(moe_status s);
 

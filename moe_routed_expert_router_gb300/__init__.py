@@ -31,8 +31,11 @@ EXPORTS = ["moe_plan_create", "moe_plan_destroy", "moe_route", "moe_forward", "m
            "moe_quantize_act", "moe_quantize_nvfp4", "moe_plan_sync_status", "moe_plan_debug_buffer",
            "moe_plan_set_profiling", "moe_plan_read_profile", "moe_plan_set_path", "moe_plan_check_timeout",
            "moe_route_static", "moe_convert_f32", "moe_quantize_mxfp4", "moe_plan_keep_h", "moe_status_string",
-           "moe_version"]
+           "moe_version", "moe_rms_norm", "moe_rms_norm_backward", "moe_rms_norm_backward_workspace",
+           "moe_sorted_rows", "moe_sort_pairs", "moe_dispatch", "moe_combine", "moe_combine_backward"]
 FMT_E4M3, FMT_E2M1 = 0, 1
+DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
+QUANT_NONE, QUANT_E4M3_128, QUANT_E4M3_ROW, QUANT_MXFP8 = 0, 1, 2, 3
 PATH_AUTO, PATH_CUDA_CORE, PATH_TENSOR_CORE, PATH_WARP_MMA = 0, 1, 2, 3
 STAGES = ["route", "group", "quant_x", "permute", "gate_up", "quant_h", "down", "finalize"]
 
@@ -67,7 +70,7 @@ def lib():
         if not os.path.exists(LIB_PATH) or not _build.up_to_date():
             _build.build()
         L = ctypes.CDLL(LIB_PATH)
-        P, I32 = ctypes.c_void_p, ctypes.c_int32
+        P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         L.moe_plan_create.argtypes = [ctypes.POINTER(Config), ctypes.POINTER(P)]
         L.moe_plan_destroy.argtypes = [P]
         L.moe_route.argtypes = [P, P, I32, P, P, P, P, P, P, P]
@@ -85,12 +88,22 @@ def lib():
         L.moe_plan_read_profile.argtypes = [P, P, P, P]
         L.moe_convert_f32.argtypes = [P, ctypes.c_int64, I32, P, P]
         L.moe_quantize_mxfp4.argtypes = [P, ctypes.c_int64, I32, P, P, P]
+        L.moe_rms_norm.argtypes = [P, I64, P, I64, P, I32, I32, I32, ctypes.c_float, I32, P, P, P, P, P, P]
+        L.moe_rms_norm_backward.argtypes = [P, P, P, P, P, I32, I32, I32, P, P, P, SZ, P]
+        L.moe_rms_norm_backward_workspace.argtypes = [I32, I32]
+        L.moe_sorted_rows.argtypes = [I64, I32, I32]
+        L.moe_sort_pairs.argtypes = [P, I32, I32, I32, I32, I64, P, P, P, P]
+        L.moe_dispatch.argtypes = [P, I64, I64, P, I32, I32, I32, P, P, I64, P, P, P]
+        L.moe_combine.argtypes = [P, I32, I32, I32, I32, P, I64, P, P, P, P]
+        L.moe_combine_backward.argtypes = [P, P, I32, I32, I32, I32, P, P, I64, P, P, P, P]
         L.moe_status_string.argtypes = [I32]
         L.moe_status_string.restype = ctypes.c_char_p
         L.moe_version.restype = ctypes.c_char_p
         for n in EXPORTS:
             if n not in ("moe_status_string", "moe_version"):
                 getattr(L, n).restype = I32
+        L.moe_rms_norm_backward_workspace.restype = SZ
+        L.moe_sorted_rows.restype = I64
         _lib = L
     return _lib
 
@@ -168,6 +181,252 @@ def convert_f32(src: torch.Tensor, fmt: int, out: torch.Tensor | None = None, st
     if out is None:
         out = torch.empty(src.shape, dtype=torch.uint8, device=src.device)
     _check(lib().moe_convert_f32(_ptr(src), src.numel(), fmt, _ptr(out), _stream(stream)), "moe_convert_f32")
+    return out
+
+
+# ------------------------------------------------ the token path around the experts' products
+
+_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+_GROUP = {QUANT_E4M3_128: 128, QUANT_MXFP8: 32}
+
+
+def _refuse(where: str, what: str, status: int = ERR_INVALID_ARG):
+    raise MoeError(status, f"{where} ({what})")
+
+
+def _dtype(t, where):
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        _refuse(where, f"{t.dtype} rows; float32, bfloat16 or float16 expected")
+    return d
+
+
+def _want(t, where, name, shape, dtype, device, strided=False):
+    """A tensor argument is where and what the kernels take it to be: contiguous (strided: rows of contiguous values)."""
+    if t.device != device or not t.is_cuda:
+        _refuse(where, f"{name} on {t.device}; every tensor is on one CUDA device")
+    if t.dtype != dtype or t.shape != shape:
+        _refuse(where, f"{name} {t.dtype}{list(t.shape)}; {dtype}{list(shape)} expected")
+    if not t.is_contiguous() and not (strided and t.dim() == 2 and t.stride(1) == 1):
+        _refuse(where, f"{name} is not contiguous")
+    return t
+
+
+def _new(shape, dtype, device, stream):
+    """Memory that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _row_stride(t):
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def rms_norm(x, weight, residual=None, eps=1e-6, quant=QUANT_NONE, out=None, stream=None):
+    """Residual addition and root-mean-square norm of x [T][H] (rows may be strided).
+
+    Returns a dict of what `out` holds, or of new tensors: "rstd" [T] fp32; "sum" (x + residual) with a residual;
+    "y" for QUANT_NONE, else "q" float8_e4m3fn [T][H] and its "scales" (fp32 [T][ceil(H/128)] or [T][1],
+    float8_e8m0fnu [T][ceil(H/32)] for QUANT_MXFP8).  An `out` may hold "y" beside "q", leave out "sum" or "rstd"
+    (not written then), and give x or residual themselves as "sum"."""
+    where = "moe_rms_norm"
+    if x.dim() != 2:
+        _refuse(where, "x is not [T][H]")
+    T, H = x.shape
+    dev, dt = x.device, x.dtype
+    code = _dtype(x, where)
+    _want(x, where, "x", (T, H), dt, dev, strided=True)
+    _want(weight, where, "weight", (H,), dt, dev)
+    if residual is not None:
+        _want(residual, where, "residual", (T, H), dt, dev, strided=True)
+    if quant not in (QUANT_NONE, QUANT_E4M3_128, QUANT_E4M3_ROW, QUANT_MXFP8):
+        _refuse(where, f"quant {quant}")
+    sc_dtype = torch.float8_e8m0fnu if quant == QUANT_MXFP8 else torch.float32
+    sc_shape = (T, 1) if quant == QUANT_E4M3_ROW else (T, -(-H // _GROUP.get(quant, 1)))
+    if out is None:
+        out = {"rstd": _new((T,), torch.float32, dev, stream)}
+        if residual is not None:
+            out["sum"] = _new((T, H), dt, dev, stream)
+        if quant == QUANT_NONE:
+            out["y"] = _new((T, H), dt, dev, stream)
+        else:
+            out["q"] = _new((T, H), torch.float8_e4m3fn, dev, stream)
+            out["scales"] = _new(sc_shape, sc_dtype, dev, stream)
+    else:
+        for name, t in out.items():
+            if name in ("sum", "y"):
+                _want(t, where, name, (T, H), dt, dev)
+            elif name == "rstd":
+                _want(t, where, name, (T,), torch.float32, dev)
+            elif name == "q" and quant != QUANT_NONE:
+                _want(t, where, name, (T, H), torch.float8_e4m3fn, dev)
+            elif name == "scales" and quant != QUANT_NONE:
+                _want(t, where, name, sc_shape, sc_dtype, dev)
+            else:
+                _refuse(where, f"no output {name!r}")
+    _check(lib().moe_rms_norm(_ptr(x), _row_stride(x), _ptr(residual), 0 if residual is None else _row_stride(residual),
+                              _ptr(weight), T, H, code, eps, quant, _ptr(out.get("sum")), _ptr(out.get("y")),
+                              _ptr(out.get("q")), _ptr(out.get("scales")), _ptr(out.get("rstd")), _stream(stream)), where)
+    return out
+
+
+def rms_norm_backward(grad_y, sum, weight, rstd, grad_sum=None, out=None, stream=None):
+    """Gradients of rms_norm: {"grad_sum": [T][H], x's and residual's; "grad_w": [H] fp32}.
+
+    `sum` is rms_norm's "sum" (x itself without a residual), `rstd` its "rstd"; `grad_sum` the gradient that reaches
+    the sum on its other way (the residual stream)."""
+    where = "moe_rms_norm_backward"
+    if sum.dim() != 2:
+        _refuse(where, "sum is not [T][H]")
+    T, H = sum.shape
+    dev, dt = sum.device, sum.dtype
+    code = _dtype(sum, where)
+    _want(sum, where, "sum", (T, H), dt, dev)
+    _want(grad_y, where, "grad_y", (T, H), dt, dev)
+    _want(weight, where, "weight", (H,), dt, dev)
+    _want(rstd, where, "rstd", (T,), torch.float32, dev)
+    if grad_sum is not None:
+        _want(grad_sum, where, "grad_sum", (T, H), dt, dev)
+    if out is None:
+        out = {"grad_sum": _new((T, H), dt, dev, stream), "grad_w": _new((H,), torch.float32, dev, stream)}
+    else:
+        _want(out["grad_sum"], where, "out grad_sum", (T, H), dt, dev)
+        _want(out["grad_w"], where, "out grad_w", (H,), torch.float32, dev)
+    n = lib().moe_rms_norm_backward_workspace(T, H)
+    ws = _new((n,), torch.uint8, dev, stream)
+    _check(lib().moe_rms_norm_backward(_ptr(grad_y), _ptr(sum), _ptr(weight), _ptr(rstd), _ptr(grad_sum), T, H, code,
+                                       _ptr(out["grad_sum"]), _ptr(out["grad_w"]), _ptr(ws), n, _stream(stream)), where)
+    return out
+
+
+def sorted_rows(pairs: int, num_experts: int, align: int = 1) -> int:
+    """Rows of the sorted layout, whatever the routing (moe_sorted_rows)."""
+    n = lib().moe_sorted_rows(pairs, num_experts, align)
+    if n < 0:
+        _refuse("moe_sorted_rows", f"{pairs} pairs, {num_experts} experts, align {align}", ERR_UNSUPPORTED_SHAPE)
+    return n
+
+
+def sort_pairs(topk_ids, num_experts, align=1, out=None, stream=None):
+    """Stable sort of the (token, slot) pairs by expert, from ids [T][k] int32 (outside [0, num_experts): dropped).
+
+    Returns {"expert_offsets": [E+1], "sorted_rows": [rows] (pair at a row, -1 none), "pair_rows": [T][k] (row of a
+    pair, -1 dropped)}, int32; every expert's segment is padded to a multiple of `align` rows."""
+    where = "moe_sort_pairs"
+    if topk_ids.dim() != 2:
+        _refuse(where, "topk_ids is not [T][k]")
+    T, k = topk_ids.shape
+    dev = topk_ids.device
+    _want(topk_ids, where, "topk_ids", (T, k), torch.int32, dev)
+    R = sorted_rows(T * k, num_experts, align)
+    if out is None:
+        out = {"expert_offsets": _new((num_experts + 1,), torch.int32, dev, stream),
+               "sorted_rows": _new((R,), torch.int32, dev, stream),
+               "pair_rows": _new((T, k), torch.int32, dev, stream)}
+    else:
+        _want(out["expert_offsets"], where, "out expert_offsets", (num_experts + 1,), torch.int32, dev)
+        _want(out["sorted_rows"], where, "out sorted_rows", (R,), torch.int32, dev)
+        _want(out["pair_rows"], where, "out pair_rows", (T, k), torch.int32, dev)
+    _check(lib().moe_sort_pairs(_ptr(topk_ids), T, k, num_experts, align, R, _ptr(out["expert_offsets"]),
+                                _ptr(out["sorted_rows"]), _ptr(out["pair_rows"]), _stream(stream)), where)
+    return out
+
+
+def _order(order, where, dev):
+    """sort_pairs' result: (sorted_rows, pair_rows, rows, T, k)."""
+    rows, inv = order["sorted_rows"], order["pair_rows"]
+    if inv.dim() != 2 or rows.dim() != 1:
+        _refuse(where, "order is not sort_pairs' result")
+    _want(rows, where, "sorted_rows", rows.shape, torch.int32, dev)
+    _want(inv, where, "pair_rows", inv.shape, torch.int32, dev)
+    return rows, inv, rows.shape[0], inv.shape[0], inv.shape[1]
+
+
+def dispatch(x, order, scales=None, out=None, stream=None):
+    """Token rows x [T][H] (any type; rows may be strided) into sort_pairs' order, zeros where a row holds no pair.
+
+    Returns {"rows": [rows][H]} and, with scales [T][n], {"scales": [rows][n]}."""
+    where = "moe_dispatch"
+    dev = x.device
+    rows, inv, R, T, k = _order(order, where, dev)
+    if x.dim() != 2 or x.shape[0] != T:
+        _refuse(where, f"x is not [{T}][H]")
+    H, es = x.shape[1], x.element_size()
+    _want(x, where, "x", (T, H), x.dtype, dev, strided=True)
+    sb = 0
+    if scales is not None:
+        if scales.dim() != 2:
+            _refuse(where, "scales is not [T][n]")
+        _want(scales, where, "scales", (T, scales.shape[1]), scales.dtype, dev)
+        sb = scales.shape[1] * scales.element_size()
+    if out is None:
+        out = {"rows": _new((R, H), x.dtype, dev, stream)}
+        if scales is not None:
+            out["scales"] = _new((R, scales.shape[1]), scales.dtype, dev, stream)
+    else:
+        _want(out["rows"], where, "out rows", (R, H), x.dtype, dev)
+        if scales is not None:
+            _want(out["scales"], where, "out scales", (R, scales.shape[1]), scales.dtype, dev)
+        elif "scales" in out:
+            _refuse(where, "out scales without scales")
+    _check(lib().moe_dispatch(_ptr(x), _row_stride(x) * es, H * es, _ptr(scales), sb, T, k, _ptr(rows), _ptr(inv), R,
+                              _ptr(out["rows"]), _ptr(out.get("scales")), _stream(stream)), where)
+    return out
+
+
+def combine(y, order, weights=None, base=None, out=None, stream=None):
+    """out[t] = sum_j weights[t][j] * y[row of pair (t, j)] + base[t]: expert rows y [rows][H] back into token order.
+
+    weights [T][k] fp32 (None: 1); base [T][H] is added where given.  Rows of y that hold no pair are not read."""
+    where = "moe_combine"
+    dev = y.device
+    rows, inv, R, T, k = _order(order, where, dev)
+    if y.dim() != 2:
+        _refuse(where, "y is not [rows][H]")
+    H = y.shape[1]
+    code = _dtype(y, where)
+    _want(y, where, "y", (R, H), y.dtype, dev)
+    if weights is not None:
+        _want(weights, where, "weights", (T, k), torch.float32, dev)
+    if base is not None:
+        _want(base, where, "base", (T, H), y.dtype, dev)
+    if out is None:
+        out = _new((T, H), y.dtype, dev, stream)
+    else:
+        _want(out, where, "out", (T, H), y.dtype, dev)
+    _check(lib().moe_combine(_ptr(y), code, T, k, H, _ptr(inv), R, _ptr(weights), _ptr(base), _ptr(out),
+                             _stream(stream)), where)
+    return out
+
+
+def dispatch_backward(grad_rows, order, out=None, stream=None):
+    """Gradient of dispatch: [T][H], the sum of a token's rows of grad_rows [rows][H]."""
+    return combine(grad_rows, order, None, None, out, stream)
+
+
+def combine_backward(grad_out, y, order, weights, out=None, stream=None):
+    """Gradients of combine: {"grad_y": [rows][H] (zeros where a row holds no pair), "grad_w": [T][k] fp32}.
+
+    base's gradient is grad_out itself.  out["grad_y"] may be y."""
+    where = "moe_combine_backward"
+    dev = y.device
+    rows, inv, R, T, k = _order(order, where, dev)
+    if y.dim() != 2:
+        _refuse(where, "y is not [rows][H]")
+    H = y.shape[1]
+    code = _dtype(y, where)
+    _want(y, where, "y", (R, H), y.dtype, dev)
+    _want(grad_out, where, "grad_out", (T, H), y.dtype, dev)
+    _want(weights, where, "weights", (T, k), torch.float32, dev)
+    if out is None:
+        out = {"grad_y": _new((R, H), y.dtype, dev, stream), "grad_w": _new((T, k), torch.float32, dev, stream)}
+    else:
+        _want(out["grad_y"], where, "out grad_y", (R, H), y.dtype, dev)
+        _want(out["grad_w"], where, "out grad_w", (T, k), torch.float32, dev)
+    _check(lib().moe_combine_backward(_ptr(grad_out), _ptr(y), code, T, k, H, _ptr(rows), _ptr(inv), R, _ptr(weights),
+                                      _ptr(out["grad_y"]), _ptr(out["grad_w"]), _stream(stream)), where)
     return out
 
 
