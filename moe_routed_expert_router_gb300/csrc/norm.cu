@@ -1,12 +1,15 @@
 // Residual addition and root-mean-square norm with an optional 8-bit output,
 // and its gradients (see include/moe_nvfp4.h for the formulas).
 //
-// Forward: one block a row, the row in registers between its two uses (the sum
+// A block takes a row and keeps it in registers between its two uses (the sum
 // of squares, then the products), so every input is read once and every output
-// written once.  Bound by HBM.
+// written once.  Bound by HBM; what keeps it there is that the loads of the
+// next row do not wait for the block-wide reduction of the present one: other
+// blocks' in the forward pass, a ring in shared memory in the backward pass.
 #include <math.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "rows.cuh"
 
@@ -15,9 +18,10 @@ namespace {
 using namespace moe;
 
 constexpr int kMaxH = 16384;
-constexpr int kMaxChunksThread = 4;   // 16-byte pieces of a row a thread holds
-// Threads of a block whose threads hold v pieces (row_shape below).
-constexpr int max_threads(int v) { return v < kMaxChunksThread ? 256 : kMaxH / kChunk / kMaxChunksThread; }
+constexpr int kMaxPieces = 4;         // 16-bit rows: 16-byte pieces a thread holds
+constexpr int kRowThreads = kMaxH / kChunk / kMaxPieces;
+constexpr int kWarpRows = 8;          // rows a block takes where a row takes a warp
+constexpr int kWarpPieces = 32 * kMaxPieces;
 constexpr float kMinAmax = 7.888609052210118e-31f;   // 2^-100
 
 struct NormArgs {
@@ -31,26 +35,33 @@ struct NormArgs {
     float *rstd;
 };
 
-// Maximum that keeps a NaN.
+// Maximum that keeps a NaN; of magnitudes, three at a time.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+__device__ __forceinline__ float amax3(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
-// Sum over the block, the same on every thread; `red` holds 33 words, and two
-// calls in a row use different ones.
-__device__ __forceinline__ float block_sum(float v, float *red) {
+// Sum over the threads of a row (a warp, or the block), the same on every
+// thread; `red` holds 32 words, and two calls in a row use different ones.
+template <bool kWarp> __device__ __forceinline__ float row_sum(float v, float *red) {
     v = warp_sum(v);
+    if constexpr (kWarp) return v;
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
     return warp_sum(lane < nw ? red[lane] : 0.0f);
 }
 
-__device__ __forceinline__ float block_max_nan(float v, float *red) {
+template <bool kWarp> __device__ __forceinline__ float row_max_nan(float v, float *red) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if constexpr (kWarp) return v;
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
@@ -76,74 +87,108 @@ __device__ __forceinline__ float row_rstd(float sumsq, int H, float eps) {
     return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sumsq, (float)H), eps)));
 }
 
-// Thread i holds pieces i, i + n, ... of the row (n threads, a multiple of 32),
-// so a warp's loads are 512 consecutive bytes of a 16-bit row, a 128-value
-// group is 16 neighbouring lanes and a 32-value group is four.
-template <int DT, int Q, int V>
-__global__ void __launch_bounds__(max_threads(V)) k_rms_norm(const NormArgs a) {
+// n = (s * rstd) * weight of one piece, fp32.
+template <int DT> __device__ __forceinline__ void norm8(const Raw8<DT> &s, const Raw8<DT> &w, float rstd, float (&n)[8]) {
+    float g[8];
+    widen8<DT>(s, n);
+    widen8<DT>(w, g);
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        mul2(n, e, rstd, rstd);
+        mul2(n, e, g[e], g[e + 1]);
+    }
+}
+
+__device__ __forceinline__ float amax8(const float (&n)[8], float m) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) m = amax3(m, n[e], n[e + 1]);
+    return m;
+}
+
+// s = round(x + r) of one piece: the type's own addition, one rounding of the
+// exact sum.
+template <int DT> __device__ __forceinline__ uint32_t add_word(uint32_t x, uint32_t r) {
+    uint32_t s;
+    if constexpr (DT == MOE_DTYPE_F32) return __float_as_uint(__fadd_rn(__uint_as_float(x), __uint_as_float(r)));
+    if constexpr (DT == MOE_DTYPE_BF16) asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(s) : "r"(x), "r"(r));
+    if constexpr (DT == MOE_DTYPE_F16) asm("add.rn.f16x2 %0, %1, %2;" : "=r"(s) : "r"(x), "r"(r));
+    return s;
+}
+template <int DT> __device__ __forceinline__ Raw8<DT> add8(const Raw8<DT> &x, const Raw8<DT> &r) {
+    Raw8<DT> s;
+    s.a = make_uint4(add_word<DT>(x.a.x, r.a.x), add_word<DT>(x.a.y, r.a.y), add_word<DT>(x.a.z, r.a.z), add_word<DT>(x.a.w, r.a.w));
+    if constexpr (DT == MOE_DTYPE_F32)
+        s.b = make_uint4(add_word<DT>(x.b.x, r.b.x), add_word<DT>(x.b.y, r.b.y), add_word<DT>(x.b.z, r.b.z), add_word<DT>(x.b.w, r.b.w));
+    return s;
+}
+
+// A row a block (G = 1), or a row a warp and eight of them a block (rows of up
+// to 1024 values: no block barrier, and short rows fill an SM).  Thread i of a
+// row's n (a multiple of 32) holds pieces i, i + n, ..., so a warp's accesses
+// are 512 consecutive bytes of a 16-bit row, a 128-value group is 16
+// neighbouring lanes and a 32-value group is four.  All of a thread's loads are
+// issued before the first use; the row stays in its stored type (half the
+// registers of fp32, so more blocks an SM).
+template <int DT, int Q, int V, bool kWarp>
+__global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_norm(const NormArgs a, int64_t rows) {
     using T = typename RowType<DT>::T;
     __shared__ float red[2][32];
-    const int64_t t = blockIdx.x;
-    const int n8 = a.H / kChunk, n = blockDim.x;
-    const T *x = static_cast<const T *>(a.x) + t * a.xs;
-    const T *r = a.r ? static_cast<const T *>(a.r) + t * a.rs : nullptr;
-    float v[V][8];
-    float ss = 0.0f;
+    const int tid = kWarp ? threadIdx.x & 31 : threadIdx.x;
+    const int n8 = a.H / kChunk, n = kWarp ? 32 : blockDim.x;
+    const int64_t t = kWarp ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+    Raw8<DT> s[V], u[V], w[V];
+    pdl_wait();
+    pdl_trigger();
+    if (kWarp && t >= rows) return;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = threadIdx.x + i * n;
+        const int c = tid + i * n;
+        s[i] = u[i] = w[i] = Raw8<DT>{};
         if (c < n8) {
-            widen8<DT>(load8<DT>(x + c * kChunk), v[i]);
-            if (r) {
-                float u[8];
-                widen8<DT>(load8<DT>(r + c * kChunk), u);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] = __fadd_rn(v[i][e], u[e]);
-                const Raw8<DT> s = narrow8<DT>(v[i]);
-                if (a.sum) store8<DT>(static_cast<T *>(a.sum) + t * a.H + c * kChunk, s);
-                widen8<DT>(s, v[i]);   // the norm is the stored sum's
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
+            s[i] = load8<DT>(static_cast<const T *>(a.x) + t * a.xs + c * kChunk);
+            if (a.r) u[i] = load8<DT>(static_cast<const T *>(a.r) + t * a.rs + c * kChunk);
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(v[i][e], v[i][e], ss);
     }
-    const float rstd = row_rstd(block_sum(ss, red[0]), a.H, a.eps);
-    if (a.rstd && threadIdx.x == 0) a.rstd[t] = rstd;
-    float amax = 0.0f;
+    float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = threadIdx.x + i * n;
-        if (c < n8) {
-            float w[8];
-            widen8<DT>(load8<DT>(static_cast<const T *>(a.w) + c * kChunk), w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][e] = __fmul_rn(__fmul_rn(v[i][e], rstd), w[e]);
-            if (a.y) store8<DT>(static_cast<T *>(a.y) + t * a.H + c * kChunk, narrow8<DT>(v[i]));
+        const int c = tid + i * n;
+        if (c < n8) w[i] = load8_shared<DT>(static_cast<const T *>(a.w) + c * kChunk);
+        if (a.r) {
+            s[i] = add8<DT>(s[i], u[i]);
+            if (a.sum && c < n8) store8<DT>(static_cast<T *>(a.sum) + t * a.H + c * kChunk, s[i]);
         }
-        if constexpr (Q == MOE_QUANT_E4M3_ROW) {
+        float f[8];
+        widen8<DT>(s[i], f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) amax = max_nan(amax, fabsf(v[i][e]));
-        }
+        for (int e = 0; e < 8; e += 2) fma2(s0, s1, f[e], f[e + 1], f[e], f[e + 1]);
     }
-    if constexpr (Q == MOE_QUANT_NONE) return;
+    const float rstd = row_rstd(row_sum<kWarp>(s0 + s1, red[0]), a.H, a.eps);
+    if (a.rstd && tid == 0) a.rstd[t] = rstd;
+    float row_amax = 0.0f;
     if constexpr (Q == MOE_QUANT_E4M3_ROW) {
-        amax = max_nan(block_max_nan(amax, red[1]), kMinAmax);
-        if (threadIdx.x == 0) static_cast<float *>(a.scales)[t] = __fdiv_rn(amax, 448.0f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float f[8];
+            norm8<DT>(s[i], w[i], rstd, f);
+            row_amax = amax8(f, row_amax);
+        }
+        row_amax = max_nan(row_max_nan<kWarp>(row_amax, red[1]), kMinAmax);
+        if (tid == 0) static_cast<float *>(a.scales)[t] = __fdiv_rn(row_amax, 448.0f);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = threadIdx.x + i * n;
+        const int c = tid + i * n;
+        float f[8];
+        norm8<DT>(s[i], w[i], rstd, f);
+        if (a.y && c < n8) store8<DT>(static_cast<T *>(a.y) + t * a.H + c * kChunk, narrow8<DT>(f));
+        if constexpr (Q == MOE_QUANT_NONE) continue;
         float mul;
         if constexpr (Q == MOE_QUANT_E4M3_ROW) {
-            mul = __fdiv_rn(448.0f, amax);
+            mul = __fdiv_rn(448.0f, row_amax);
         } else {
             constexpr int kLanes = Q == MOE_QUANT_MXFP8 ? 4 : 16;
-            float m = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(v[i][e]));
+            float m = amax8(f, 0.0f);
 #pragma unroll
             for (int o = kLanes / 2; o >= 1; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
             const bool first = c < n8 && (c % kLanes) == 0;
@@ -162,9 +207,9 @@ __global__ void __launch_bounds__(max_threads(V)) k_rms_norm(const NormArgs a) {
             }
         }
         if (c < n8) {
-            uint2 o;
-            o.x = e4m3x4(__fmul_rn(v[i][0], mul), __fmul_rn(v[i][1], mul), __fmul_rn(v[i][2], mul), __fmul_rn(v[i][3], mul));
-            o.y = e4m3x4(__fmul_rn(v[i][4], mul), __fmul_rn(v[i][5], mul), __fmul_rn(v[i][6], mul), __fmul_rn(v[i][7], mul));
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) mul2(f, e, mul, mul);
+            const uint2 o = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
             *reinterpret_cast<uint2 *>(a.q + t * a.H + c * kChunk) = o;
         }
     }
@@ -180,93 +225,204 @@ struct NormGradArgs {
 
 // Backward: block b takes rows b, b + blocks, ...; a thread keeps its columns'
 // weight gradient in registers over all of them, so the column sums cost one
-// [blocks][H] store at the end.
-template <int DT, int V>
-__global__ void __launch_bounds__(max_threads(V)) k_rms_norm_backward(const NormGradArgs a) {
+// [blocks][H] store at the end.  With R = 2 the next row is on its way into
+// shared memory while one is worked on (cp.async; a thread copies the pieces that it will
+// use itself and overwrites only what it has used, so its own copies are all
+// that it waits for); R = 1 is for
+// rows of which two do not fit.  Rows of up to 1024 values take a warp each, as
+// in the forward pass; the eight warps' sums are then added in order.
+template <int DT, int V, int R, bool kWarp>
+__global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_norm_backward(const NormGradArgs a) {
     using T = typename RowType<DT>::T;
+    extern __shared__ __align__(16) uint4 smem[];     // a row's [R][gy, s, gs][V][Raw8 words][n]
     __shared__ float red[2][32];
-    const int n8 = a.H / kChunk, n = blockDim.x;
+    const int tid = kWarp ? threadIdx.x & 31 : threadIdx.x, group = kWarp ? threadIdx.x >> 5 : 0;
+    const int n8 = a.H / kChunk, n = kWarp ? 32 : blockDim.x;
+    constexpr int kWords = sizeof(Raw8<DT>) / 16;
+    const int arr = V * kWords * n, stage = (a.gs ? 3 : 2) * arr;
+    uint4 *ring = smem + group * R * stage;
     float gw[V][8];
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) gw[i][e] = 0.0f;
-    int par = 0;
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, par ^= 1) {
-        const float rstd = a.rstd[t];
-        float g[V][8], nn[V][8];
-        float dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = threadIdx.x + i * n;
-            if (c >= n8) continue;
-            const int64_t at = t * a.H + c * kChunk;
-            float w[8];
-            widen8<DT>(load8<DT>(static_cast<const T *>(a.gy) + at), g[i]);
-            widen8<DT>(load8<DT>(static_cast<const T *>(a.s) + at), nn[i]);
-            widen8<DT>(load8<DT>(static_cast<const T *>(a.w) + c * kChunk), w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                nn[i][e] *= rstd;
-                gw[i][e] = fmaf(g[i][e], nn[i][e], gw[i][e]);
-                g[i][e] *= w[e];
-                dot = fmaf(g[i][e], nn[i][e], dot);
-            }
-        }
-        const float c1 = block_sum(dot, red[par]) / (float)a.H;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = threadIdx.x + i * n;
-            if (c >= n8) continue;
-            const int64_t at = t * a.H + c * kChunk;
-            float gs[8], o[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) gs[e] = 0.0f;
-            if (a.gs) widen8<DT>(load8<DT>(static_cast<const T *>(a.gs) + at), gs);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = fmaf(rstd, fmaf(-nn[i][e], c1, g[i][e]), gs[e]);
-            store8<DT>(static_cast<T *>(a.gin) + at, narrow8<DT>(o));
-        }
-    }
+    Raw8<DT> w[V];
+    pdl_wait();
+    pdl_trigger();
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = threadIdx.x + i * n;
-        if (c >= n8) continue;
-        store8<MOE_DTYPE_F32>(a.part + (int64_t)blockIdx.x * a.H + c * kChunk, narrow8<MOE_DTYPE_F32>(gw[i]));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) gw[i][e] = 0.0f;
+        w[i] = Raw8<DT>{};
+        if (tid + i * n < n8) w[i] = load8_shared<DT>(static_cast<const T *>(a.w) + (tid + i * n) * kChunk);
+    }
+    auto fetch = [&](int64_t t, int slot) {
+        if (t < a.T) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int c = tid + i * n;
+                if (c >= n8) continue;
+                const int64_t from = t * a.H + c * kChunk;
+                uint4 *at = ring + slot * stage + i * kWords * n + tid;
+                copy8<DT>(at, n, static_cast<const T *>(a.gy) + from);
+                copy8<DT>(at + arr, n, static_cast<const T *>(a.s) + from);
+                if (a.gs) copy8<DT>(at + 2 * arr, n, static_cast<const T *>(a.gs) + from);
+            }
+        }
+        copy_commit();
+    };
+    const int64_t step = (int64_t)gridDim.x * (kWarp ? kWarpRows : 1);
+    int64_t t = (int64_t)blockIdx.x * (kWarp ? kWarpRows : 1) + group;
+    if constexpr (R == 2) fetch(t, 0);
+    int slot = 0;
+    for (int par = 0; t < a.T; t += step, par ^= 1) {
+        const float rstd = a.rstd[t];
+        fetch(t + (R - 1) * step, R == 2 ? slot ^ 1 : 0);
+        copy_wait<R - 1>();
+        Raw8<DT> g[V], s[V];
+        float d0 = 0.0f, d1 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (tid + i * n >= n8) continue;
+            const uint4 *at = ring + slot * stage + i * kWords * n + tid;
+            g[i] = take8<DT>(at, n);
+            s[i] = take8<DT>(at + arr, n);
+            float f[8], m[8], wf[8];
+            widen8<DT>(g[i], f);
+            widen8<DT>(s[i], m);
+            widen8<DT>(w[i], wf);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                mul2(m, e, rstd, rstd);
+                fma2(gw[i][e], gw[i][e + 1], f[e], f[e + 1], m[e], m[e + 1]);
+                mul2(f, e, wf[e], wf[e + 1]);
+                fma2(d0, d1, f[e], f[e + 1], m[e], m[e + 1]);
+            }
+        }
+        const float c1 = -(row_sum<kWarp>(d0 + d1, red[par]) / (float)a.H);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (tid + i * n >= n8) continue;
+            float f[8], m[8], wf[8], o[8];
+            Raw8<DT> q{};
+            if (a.gs) q = take8<DT>(ring + slot * stage + 2 * arr + i * kWords * n + tid, n);
+            widen8<DT>(g[i], f);
+            widen8<DT>(s[i], m);
+            widen8<DT>(w[i], wf);
+            widen8<DT>(q, o);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                mul2(m, e, rstd, rstd);
+                mul2(f, e, wf[e], wf[e + 1]);
+                fma2(f[e], f[e + 1], m[e], m[e + 1], c1, c1);
+                fma2(o[e], o[e + 1], f[e], f[e + 1], rstd, rstd);
+            }
+            store8<DT>(static_cast<T *>(a.gin) + t * a.H + (tid + i * n) * kChunk, narrow8<DT>(o));
+        }
+        if constexpr (R == 2) slot ^= 1;
+    }
+    if constexpr (kWarp) {
+        copy_wait<0>();
+        __syncthreads();                              // the ring is free: the warps' sums, [8][H]
+        float *sums = reinterpret_cast<float *>(smem);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (tid + i * n >= n8) continue;
+            float4 *at = reinterpret_cast<float4 *>(sums + group * a.H + (tid + i * n) * kChunk);
+            at[0] = make_float4(gw[i][0], gw[i][1], gw[i][2], gw[i][3]);
+            at[1] = make_float4(gw[i][4], gw[i][5], gw[i][6], gw[i][7]);
+        }
+        __syncthreads();
+        for (int h = threadIdx.x; h < a.H; h += blockDim.x) {
+            float v = 0.0f;
+#pragma unroll
+            for (int g = 0; g < kWarpRows; ++g) v += sums[g * a.H + h];
+            a.part[(int64_t)blockIdx.x * a.H + h] = v;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = tid + i * n;
+            if (c >= n8) continue;
+            store8<MOE_DTYPE_F32>(a.part + (int64_t)blockIdx.x * a.H + c * kChunk, narrow8<MOE_DTYPE_F32>(gw[i]));
+        }
     }
 }
 
-// grad_w[h] = sum over the blocks' partial sums, in block order within each of
-// eight interleaved chains.
+// grad_w[h] = sum of the blocks' partial sums: thread (i, j) adds every 32nd
+// block's from j on, four columns wide, then the 32 sums are added in order.
 __global__ void __launch_bounds__(256) k_rms_norm_grad_w(const float *__restrict__ part, int blocks, int H,
                                                          float *__restrict__ gw) {
-    __shared__ float s[8][33];
-    const int h = blockIdx.x * 32 + threadIdx.x;
-    float v = 0.0f;
-    if (h < H)
-        for (int b = threadIdx.y; b < blocks; b += 8) v += part[(int64_t)b * H + h];
-    s[threadIdx.y][threadIdx.x] = v;
+    __shared__ float4 s[32][8];
+    const int i = threadIdx.x & 7, j = threadIdx.x >> 3;
+    const int h = blockIdx.x * 32 + i * 4;
+    pdl_wait();
+    pdl_trigger();
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (h < H) {
+#pragma unroll 8
+        for (int b = j; b < blocks; b += 32) {
+            const float4 p = *reinterpret_cast<const float4 *>(part + (int64_t)b * H + h);
+            v.x += p.x;
+            v.y += p.y;
+            v.z += p.z;
+            v.w += p.w;
+        }
+    }
+    s[j][i] = v;
     __syncthreads();
-    if (threadIdx.y == 0 && h < H) {
-        for (int i = 1; i < 8; ++i) v += s[i][threadIdx.x];
-        gw[h] = v;
+    if (threadIdx.x < 32 && blockIdx.x * 32 + threadIdx.x < H) {
+        const float *c = reinterpret_cast<const float *>(s) + threadIdx.x;
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) sum += c[k * 32];
+        gw[blockIdx.x * 32 + threadIdx.x] = sum;
     }
 }
 
-// Threads and pieces a thread for a row of n8 pieces.
+// Threads and pieces a thread for a row of n8 pieces.  Few rows: as many threads
+// as there are, for the latency.  Many rows: 96 to 256 threads with two pieces
+// or more (bf16, 16384 rows forward with the residual and 8-bit output: H = 2048
+// 36.7 us against 39.5 us with one piece and 256 threads; H = 4096 71.0 us
+// against 80.0 us with 512 threads).
 struct RowShape { int threads, v; };
-RowShape row_shape(int n8) {
-    int v = 1;
-    while (v < kMaxChunksThread && n8 > 256 * v) v *= 2;
+RowShape row_shape(int n8, bool few) {
+    const int v = few ? (n8 <= 512 ? 1 : n8 <= 1024 ? 2 : 4) : (n8 <= 128 ? 1 : n8 <= 512 ? 2 : 4);
     return {((n8 + v - 1) / v + 31) / 32 * 32, v};
 }
 
+// Pieces a lane where a row takes a warp.
+int warp_pieces(int n8) { return n8 <= 32 ? 1 : n8 <= 64 ? 2 : 4; }
+
+constexpr int kSms = 152;
+constexpr size_t kSmemSm = 227 * 1024;   // shared memory of an SM that its blocks share
+
+// The kernel's dynamic shared-memory limit, set once a device.
+template <auto Kernel> cudaError_t allow_smem() {
+    static std::mutex mu;
+    static bool done[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (done[dev]) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemSm - 2048);
+    if (e == cudaSuccess) done[dev] = true;
+    return e;
+}
+
+template <int DT, int Q, bool kWarp>
+cudaError_t launch_norm_v(const NormArgs &a, int T, int threads, int v, cudaStream_t st) {
+    const dim3 grid(kWarp ? (T + kWarpRows - 1) / kWarpRows : T), block(kWarp ? 32 * kWarpRows : threads);
+    if (v == 1) return launch_pdl(k_rms_norm<DT, Q, 1, kWarp>, grid, block, 0, st, a, (int64_t)T);
+    if (v == 2 || kWarp) return launch_pdl(k_rms_norm<DT, Q, 2, kWarp>, grid, block, 0, st, a, (int64_t)T);
+    return launch_pdl(k_rms_norm<DT, Q, kWarp ? 2 : 4, kWarp>, grid, block, 0, st, a, (int64_t)T);
+}
+
 template <int DT, int Q> cudaError_t launch_norm_q(const NormArgs &a, int T, cudaStream_t st) {
-    const RowShape s = row_shape(a.H / kChunk);
-    if (s.v == 1) k_rms_norm<DT, Q, 1><<<T, s.threads, 0, st>>>(a);
-    else if (s.v == 2) k_rms_norm<DT, Q, 2><<<T, s.threads, 0, st>>>(a);
-    else k_rms_norm<DT, Q, 4><<<T, s.threads, 0, st>>>(a);
-    return cudaGetLastError();
+    const int n8 = a.H / kChunk;
+    const bool few = T <= 2 * kSms;
+    // 16384 rows of 512 values: 11.2 us against 17.1 us a block a row; of 1024: 21.1 against 20.7
+    if (n8 <= 64 && !few) return launch_norm_v<DT, Q, true>(a, T, 32, warp_pieces(n8), st);
+    const RowShape s = row_shape(n8, few);
+    return launch_norm_v<DT, Q, false>(a, T, s.threads, s.v, st);
 }
 
 template <int DT> cudaError_t launch_norm(const NormArgs &a, int quant, int T, cudaStream_t st) {
@@ -278,17 +434,48 @@ template <int DT> cudaError_t launch_norm(const NormArgs &a, int quant, int T, c
     }
 }
 
-template <int DT> cudaError_t launch_norm_grad(const NormGradArgs &a, int blocks, cudaStream_t st) {
-    const RowShape s = row_shape(a.H / kChunk);
-    if (s.v == 1) k_rms_norm_backward<DT, 1><<<blocks, s.threads, 0, st>>>(a);
-    else if (s.v == 2) k_rms_norm_backward<DT, 2><<<blocks, s.threads, 0, st>>>(a);
-    else k_rms_norm_backward<DT, 4><<<blocks, s.threads, 0, st>>>(a);
-    return cudaGetLastError();
+// The backward pass's split.  Rows of up to 1024 values take a warp each (16384
+// rows of 1024, bf16: 25.7 us against 65 us a block a row), longer ones a
+// block.  Blocks an SM: 512 threads' worth, two to four (16384 rows: H = 2048
+// 46.0 us with four, 58.1 with two; H = 6144 133 us with two, 171 with three,
+// whose third waits); every block writes a row of partial sums.
+struct GradShape { RowShape row; bool warp; int blocks; };
+GradShape grad_shape(int T, int H) {
+    const int n8 = H / kChunk;
+    GradShape g;
+    g.warp = n8 <= kWarpPieces;
+    g.row = g.warp ? RowShape{32, warp_pieces(n8)} : row_shape(n8, false);
+    const int an_sm = std::max(2, std::min(4, 512 / (g.warp ? 32 * kWarpRows : g.row.threads)));
+    const int rows = g.warp ? kWarpRows : 1;
+    g.blocks = std::min((T - 1) / rows + 1, an_sm * kSms);
+    return g;
 }
 
-// Blocks of the backward pass: two for each of the GB300's 152 SMs.
-constexpr int kGradBlocks = 304;
-int grad_blocks(int T) { return std::min(T, kGradBlocks); }
+template <int DT, int V, int R, bool kWarp>
+cudaError_t launch_norm_grad_v(const NormGradArgs &a, int blocks, int threads, size_t stage, cudaStream_t st) {
+    const cudaError_t e = allow_smem<k_rms_norm_backward<DT, V, R, kWarp>>();
+    if (e != cudaSuccess) return e;
+    size_t smem = R * stage;
+    if (kWarp) {
+        smem = kWarpRows * std::max(smem, sizeof(float) * a.H);
+        threads = 32 * kWarpRows;
+    }
+    return launch_pdl(k_rms_norm_backward<DT, V, R, kWarp>, dim3(blocks), dim3(threads), smem, st, a);
+}
+
+template <int DT> cudaError_t launch_norm_grad(const NormGradArgs &a, const GradShape &g, cudaStream_t st) {
+    const int threads = g.row.threads, v = g.row.v, blocks = g.blocks;
+    const size_t stage = (a.gs ? 3 : 2) * sizeof(Raw8<DT>) * v * threads;
+    if (g.warp) {
+        if (v == 1) return launch_norm_grad_v<DT, 1, 2, true>(a, blocks, threads, stage, st);
+        if (v == 2) return launch_norm_grad_v<DT, 2, 2, true>(a, blocks, threads, stage, st);
+        return launch_norm_grad_v<DT, 4, 2, true>(a, blocks, threads, stage, st);
+    }
+    if (v == 2) return launch_norm_grad_v<DT, 2, 2, false>(a, blocks, threads, stage, st);
+    if constexpr (DT == MOE_DTYPE_F32)
+        if (2 * stage > kSmemSm - 2048) return launch_norm_grad_v<DT, 4, 1, false>(a, blocks, threads, stage, st);
+    return launch_norm_grad_v<DT, 4, 2, false>(a, blocks, threads, stage, st);
+}
 
 moe_status check_rows(int32_t T, int32_t H, int32_t dtype) {
     if (T < 0 || !known_dtype(dtype)) return MOE_ERR_INVALID_ARG;
@@ -331,7 +518,7 @@ moe_status moe_rms_norm(const void *x, int64_t x_stride, const void *residual, i
 
 size_t moe_rms_norm_backward_workspace(int32_t T, int32_t H) {
     if (T <= 0 || H <= 0) return 0;
-    return sizeof(float) * (size_t)grad_blocks(T) * (size_t)H;
+    return sizeof(float) * (size_t)grad_shape(T, H).blocks * (size_t)H;
 }
 
 moe_status moe_rms_norm_backward(const void *grad_y, const void *sum, const void *weight, const float *rstd,
@@ -347,17 +534,17 @@ moe_status moe_rms_norm_backward(const void *grad_y, const void *sum, const void
         return MOE_ERR_MISALIGNED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (T == 0) return cuda_status(cudaMemsetAsync(grad_w, 0, sizeof(float) * H, s));
-    const int blocks = grad_blocks(T);
+    const GradShape g = grad_shape(T, H);
     const NormGradArgs a{grad_y, sum, weight, grad_sum, rstd, T, H, grad_in, static_cast<float *>(workspace)};
     cudaError_t e;
     switch (dtype) {
-        case MOE_DTYPE_F32: e = launch_norm_grad<MOE_DTYPE_F32>(a, blocks, s); break;
-        case MOE_DTYPE_BF16: e = launch_norm_grad<MOE_DTYPE_BF16>(a, blocks, s); break;
-        default: e = launch_norm_grad<MOE_DTYPE_F16>(a, blocks, s); break;
+        case MOE_DTYPE_F32: e = launch_norm_grad<MOE_DTYPE_F32>(a, g, s); break;
+        case MOE_DTYPE_BF16: e = launch_norm_grad<MOE_DTYPE_BF16>(a, g, s); break;
+        default: e = launch_norm_grad<MOE_DTYPE_F16>(a, g, s); break;
     }
     if (e != cudaSuccess) return MOE_ERR_CUDA;
-    k_rms_norm_grad_w<<<(H + 31) / 32, dim3(32, 8), 0, s>>>(a.part, blocks, H, grad_w);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(launch_pdl(k_rms_norm_grad_w, dim3((H + 31) / 32), dim3(256), 0, s, (const float *)a.part, g.blocks,
+                                  (int)H, grad_w));
 }
 
 }  // extern "C"

@@ -30,6 +30,15 @@ __device__ __forceinline__ void st16(void *p, uint4 v) {
                  ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+// 16 bytes from global into shared memory without registers (cp.async); a
+// thread's copies since the last commit form a group.
+__device__ __forceinline__ void copy16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most N of the thread's latest groups are unfinished.
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 template <int DT> __device__ __forceinline__ Raw8<DT> load8(const typename RowType<DT>::T *p) {
     Raw8<DT> r;
     r.a = ld16(p);
@@ -37,9 +46,42 @@ template <int DT> __device__ __forceinline__ Raw8<DT> load8(const typename RowTy
     return r;
 }
 
+// Eight values into shared memory, `n` words apart where they take two, and back.
+template <int DT> __device__ __forceinline__ void copy8(uint4 *at, int n, const typename RowType<DT>::T *p) {
+    copy16(at, p);
+    if constexpr (DT == MOE_DTYPE_F32) copy16(at + n, p + 4);
+}
+template <int DT> __device__ __forceinline__ Raw8<DT> take8(const uint4 *at, int n) {
+    Raw8<DT> v;
+    v.a = at[0];
+    if constexpr (DT == MOE_DTYPE_F32) v.b = at[n];
+    return v;
+}
+
+// The same of a read-only row that other blocks read too (a weight): kept in L1.
+template <int DT> __device__ __forceinline__ Raw8<DT> load8_shared(const typename RowType<DT>::T *p) {
+    Raw8<DT> r;
+    r.a = __ldg(reinterpret_cast<const uint4 *>(p));
+    if constexpr (DT == MOE_DTYPE_F32) r.b = __ldg(reinterpret_cast<const uint4 *>(p + 4));
+    return r;
+}
+
 template <int DT> __device__ __forceinline__ void store8(typename RowType<DT>::T *p, const Raw8<DT> &r) {
     st16(p, r.a);
     if constexpr (DT == MOE_DTYPE_F32) st16(p + 4, r.b);
+}
+
+// Two fp32 operations in one instruction (f32x2), each rounded as the scalar
+// one is: a *= b;  c += a * b.
+__device__ __forceinline__ void mul2(float (&a)[8], int i, float b0, float b1) {
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tmul.rn.f32x2 x, x, y;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a[i]), "+f"(a[i + 1]) : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void fma2(float &c0, float &c1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%0, %1};\n\t"
+        "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "+f"(c0), "+f"(c1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
 template <int DT> __device__ __forceinline__ void widen8(const Raw8<DT> &r, float (&v)[8]) {
