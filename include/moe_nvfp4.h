@@ -407,7 +407,8 @@ moe_status moe_sort_pairs(const int32_t *topk_ids, int32_t T, int32_t k, int32_t
  *   scales [T][scale_bytes], out_scales [rows][scale_bytes]
  *   out    [rows][row_bytes]
  * sorted_rows and pair_rows are moe_sort_pairs' of the same T, k and rows; an
- * entry out of range counts as -1. */
+ * entry out of range counts as -1 (a row about which the two disagree is
+ * unspecified). */
 moe_status moe_dispatch(const void *x, int64_t x_stride_bytes, int64_t row_bytes, const void *scales,
                         int32_t scale_bytes, int32_t T, int32_t k, const int32_t *sorted_rows,
                         const int32_t *pair_rows, int64_t rows, void *out, void *out_scales, void *stream);

@@ -16,25 +16,25 @@ using namespace moe;
 
 // ------------------------------------------------------------------- sort
 
-constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxAlign = 256;
+constexpr int kSortMaxWarps = 32;
+constexpr int kSortIds = 8;           // ids a lane has in flight
 
-// Inclusive scan over the block's 1024 threads; `red` holds 32 words.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *red) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Inclusive scan over the block's threads; `red` holds 32 words.
+__device__ __forceinline__ int block_scan(int v, int *red) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += u;
     }
     if (lane == 31) red[warp] = v;
     __syncthreads();
     if (warp == 0) {
-        int64_t w = red[lane];
+        int w = lane < warps ? red[lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t u = __shfl_up_sync(0xffffffffu, w, o);
+            const int u = __shfl_up_sync(0xffffffffu, w, o);
             if (lane >= o) w += u;
         }
         red[lane] = w;
@@ -43,91 +43,122 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *red) {
     return warp ? v + red[warp - 1] : v;
 }
 
-// Counting sort in one launch of one cluster.  Every warp owns a contiguous
-// run of pairs: it counts them per expert in shared memory; the blocks read
-// each other's per-expert totals through distributed shared memory (a cluster
-// barrier on either side), scan them into the segments' first rows, and place
-// the pairs in order.  Latency-bound: two passes over the ids and two barriers.
-__global__ void __launch_bounds__(kSortThreads) k_sort_pairs(const int32_t *__restrict__ ids, int P, int E, int align,
-                                                             int64_t R, int32_t *__restrict__ offsets,
-                                                             int32_t *__restrict__ rows,
-                                                             int32_t *__restrict__ inv) {
-    cg::cluster_group cl = cg::this_cluster();
+// Shared memory of k_sort_pairs, in words: [warps][E] a warp's counts, then the
+// index of its next pair in the block's run of an expert; [E] the block's
+// counts; [E] an expert's first row for this block.
+struct SortArgs {
+    const int32_t *ids;
+    int P, E, align, warps, run;   // `warps` of a block own `run` consecutive pairs each
+    int64_t R;
+    int32_t *offsets, *rows, *inv;
+};
+
+// Counting sort in one launch of one cluster (or one block).  Every warp owns a
+// run of consecutive pairs and counts them per expert in shared memory; the
+// blocks read each other's counts through distributed shared memory and scan
+// them into the segments' first rows; the pairs are then placed in order, the
+// ones of a warp that share an expert ranked by a match.  All rows are set to
+// -1 while the ids arrive; the barrier in between orders that before the
+// placing.  Latency-bound: one read of the ids, one cluster barrier, one write
+// (4 tokens, k = 8, E = 128: 2.2 us in a graph; 16384 tokens, E = 256: 12.5
+// us with 16 blocks, 20.5 us with 8).  Placing through a sorted copy in shared
+// memory, for neighbouring writes, measured no gain.
+template <bool kCluster>
+__global__ void __launch_bounds__(1024) k_sort_pairs(const SortArgs a) {
     extern __shared__ int smem[];
-    int *wc = smem;                       // [32][E] a warp's counts, then its next rows
-    int *tot = smem + kSortWarps * E;     // [E] this block's counts
-    int *s_pad = tot + E;                 // [E][2] a segment's first row of padding and its end
-    __shared__ int64_t red[32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int nb = (int)cl.num_blocks(), rank = (int)cl.block_rank();
-    for (int i = tid; i < kSortWarps * E; i += kSortThreads) wc[i] = 0;
-    __syncthreads();
-    // this warp's run of pairs, a multiple of 32 long
-    const int64_t seg = ((int64_t)P + (int64_t)nb * kSortThreads - 1) / ((int64_t)nb * kSortThreads) * 32;
-    const int64_t beg = std::min<int64_t>(P, seg * (rank * kSortWarps + warp));
-    const int64_t end = std::min<int64_t>(P, beg + seg);
+    const int E = a.E, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int *wc = smem, *tot = wc + a.warps * E, *first = tot + E;
+    __shared__ int red[32];
+    int nb = 1, rank = 0;
+    if constexpr (kCluster) {
+        nb = (int)cg::this_cluster().num_blocks();
+        rank = (int)cg::this_cluster().block_rank();
+    }
+    for (int i = tid; i < a.warps * E; i += blockDim.x) wc[i] = 0;
+    pdl_wait();
+    pdl_trigger();
+    const bool owns = warp < a.warps;
+    const int64_t beg = owns ? min((int64_t)a.P, ((int64_t)rank * a.warps + warp) * a.run) : a.P;
+    const int64_t end = min((int64_t)a.P, beg + a.run);
     int *mine = wc + warp * E;
-    for (int64_t p = beg + lane; p < end; p += 32) {
-        const int e = ids[p];
-        if (e >= 0 && e < E) atomicAdd(mine + e, 1);
+    int id[kSortIds];
+    auto load = [&](int64_t p0) {
+#pragma unroll
+        for (int i = 0; i < kSortIds; ++i) {
+            const int64_t p = p0 + 32 * i + lane;
+            id[i] = p < end ? a.ids[p] : -1;
+            if (id[i] >= E) id[i] = -1;
+        }
+    };
+    load(beg);
+    for (int64_t r = rank * (int64_t)blockDim.x + tid; r < a.R; r += nb * (int64_t)blockDim.x) a.rows[r] = -1;
+    __syncthreads();
+    for (int64_t p0 = beg; p0 < end; p0 += 32 * kSortIds) {
+        if (p0 != beg) load(p0);
+#pragma unroll
+        for (int i = 0; i < kSortIds; ++i)
+            if (id[i] >= 0) atomicAdd(mine + id[i], 1);
     }
     __syncthreads();
-    for (int e = tid; e < E; e += kSortThreads) {
-        int c = 0;
-        for (int w = 0; w < kSortWarps; ++w) c += wc[w * E + e];
-        tot[e] = c;
-    }
-    cl.sync();
-    int count = 0, before = 0;            // thread e: expert e's pairs, and those of the blocks before
-    if (tid < E)
-        for (int b = 0; b < nb; ++b) {
-            const int c = cl.map_shared_rank(tot, b)[tid];
-            count += c;
-            if (b < rank) before += c;
-        }
-    const int64_t padded = ((int64_t)count + align - 1) / align * align;
-    const int64_t last = block_scan(padded, red);   // E <= 1024 threads
+    int count = 0, before = 0;   // thread e: expert e's pairs in all blocks, and in those before this one
     if (tid < E) {
-        int run = (int)(last - padded);
-        if (rank == 0) {
-            offsets[tid] = run;
-            if (tid == E - 1) offsets[E] = (int)last;
-        }
-        s_pad[2 * tid] = run + count;
-        s_pad[2 * tid + 1] = (int)last;
-        run += before;
-        for (int w = 0; w < kSortWarps; ++w) {
+        for (int w = 0; w < a.warps; ++w) {
             const int c = wc[w * E + tid];
-            wc[w * E + tid] = run;
-            run += c;
+            wc[w * E + tid] = count;
+            count += c;
+        }
+        if constexpr (kCluster) tot[tid] = count;
+    }
+    if constexpr (kCluster) {
+        cg::this_cluster().sync();
+        if (tid < E) {
+            count = 0;
+            for (int b = 0; b < nb; ++b) {
+                const int c = cg::this_cluster().map_shared_rank(tot, b)[tid];
+                count += c;
+                if (b < rank) before += c;
+            }
+        }
+        cg::this_cluster().barrier_arrive();           // this block has read the others' counts
+    }
+    const int padded = (int)(((int64_t)count + a.align - 1) / a.align * a.align);
+    const int segment = block_scan(padded, red);
+    if (tid < E) {
+        first[tid] = segment - padded + before;
+        if (rank == 0) {
+            a.offsets[tid] = segment - padded;
+            if (tid == E - 1) a.offsets[E] = segment;
         }
     }
-    cl.sync();                            // the other blocks have read `tot`; this one's tables are written
-    for (int64_t p0 = beg; p0 < end; p0 += 32) {
-        const int64_t p = p0 + lane;
-        int e = p < end ? ids[p] : -1;
-        if (e >= E) e = -1;
-        const unsigned peers = __match_any_sync(0xffffffffu, e);
-        int row = -1;
-        if (e >= 0) row = mine[e] + __popc(peers & ((1u << lane) - 1u));
-        __syncwarp();
-        if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
-        __syncwarp();
-        if (p < end) {
-            inv[p] = row;
-            if (row >= 0 && row < R) rows[row] = (int)p;   // ids that changed meanwhile write nothing out of range
+    __syncthreads();
+    for (int64_t p0 = beg; p0 < end; p0 += 32 * kSortIds) {
+        if (end - beg > 32 * kSortIds) load(p0);
+#pragma unroll
+        for (int i = 0; i < kSortIds; ++i) {
+            const int64_t p = p0 + 32 * i + lane;
+            if (p0 + 32 * i >= end) break;
+            const int e = id[i];
+            const unsigned peers = __match_any_sync(0xffffffffu, e);
+            int row = -1;
+            if (e >= 0) row = first[e] + mine[e] + __popc(peers & ((1u << lane) - 1u));
+            __syncwarp();
+            if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
+            __syncwarp();
+            if (p >= end) continue;
+            if (row >= 0 && row < a.R) a.rows[row] = (int)p;   // ids that changed meanwhile write nothing out of range
+            a.inv[p] = row;
         }
     }
-    // rows without a pair: every segment's padding, then what is past the last segment
-    for (int e = rank * kSortWarps + warp; e < E; e += nb * kSortWarps)
-        for (int r = s_pad[2 * e] + lane; r < s_pad[2 * e + 1]; r += 32) rows[r] = -1;
-    for (int64_t r = (int64_t)s_pad[2 * E - 1] + rank * kSortThreads + tid; r < R; r += (int64_t)nb * kSortThreads)
-        rows[r] = -1;
+    if constexpr (kCluster) cg::this_cluster().barrier_wait();   // the others have read this block's counts
 }
 
-size_t sort_smem(int E) { return sizeof(int) * ((size_t)kSortWarps + 3) * E; }
+// Pairs a block of the cluster takes before there is another, up to 16 blocks
+// (1024 tokens, k = 8: 4.4 us; with 1024 pairs a block 5.3 us, with 2048 6.0).
+constexpr int kSortPairs = 512, kSortBlocks = 16;
 
-// The kernel's shared-memory limit, once a device and for the largest E.
+size_t sort_smem(int warps, int E) { return sizeof(int) * ((size_t)warps + 2) * E; }
+
+// The kernels' attributes, once a device: shared memory, and the cluster size.
 cudaError_t configure_sort() {
     static std::mutex mu;
     static bool done[kMaxDevices] = {};
@@ -137,156 +168,302 @@ cudaError_t configure_sort() {
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
     if (done[dev]) return cudaSuccess;
-    e = cudaFuncSetAttribute(k_sort_pairs, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sort_smem(kMaxExperts));
-    if (e == cudaSuccess) done[dev] = true;
-    return e;
+    for (auto kernel : {k_sort_pairs<false>, k_sort_pairs<true>}) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)sort_smem(kSortMaxWarps, kMaxExperts));
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    done[dev] = true;
+    return cudaSuccess;
 }
 
 // --------------------------------------------------------------- dispatch
 
-// One warp a row of out: 16 bytes a lane and step.
-__global__ void __launch_bounds__(256) k_dispatch(const char *x, int64_t xs, int64_t row_bytes, const char *scales,
-                                                  int scale_bytes, int T, int k, const int32_t *__restrict__ rows,
-                                                  int64_t R, char *out, char *out_scales) {
+// Bound by the HBM writes, so nothing is read twice: a thread holds two 16-byte
+// pieces of a token's row and stores them to each of the token's rows (4096 x
+// 7168, 8 of 256 experts: 73 us in 8 bits with padding to 128 rows, 104 % of
+// the measured copy bandwidth; a warp a row of out, which reads a token's row
+// once a pair, 97 us).  Blocks: threadIdx.y and blockIdx.x choose the token,
+// blockIdx.y the part of its row.  Blocks past the tokens' write zeros to the
+// rows without a pair.
+constexpr int kCopyPieces = 2;
+
+// Rows that a warp looks at for ones without a pair: a row of 512 pieces, up to
+// 32 shorter ones.
+int zero_rows_a_warp(int pieces) { return std::max(1, std::min(32, 512 / pieces)); }
+
+template <typename W>
+__global__ void __launch_bounds__(256) k_dispatch(const char *x, int64_t xs, int n, const char *scales, int scale_words,
+                                                  int T, int k, const int32_t *__restrict__ rows,
+                                                  const int32_t *__restrict__ inv, int64_t R, char *out,
+                                                  char *out_scales, int token_blocks, int zero_rows) {
+    const int64_t row_bytes = (int64_t)n * 16;
     const int lane = threadIdx.x & 31;
-    const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (r >= R) return;
-    const int p = rows[r];
-    const int64_t t = (p >= 0 && p < T * (int64_t)k) ? p / k : -1;
-    for (int64_t c = lane * 16; c < row_bytes; c += 512)
-        st16(out + r * row_bytes + c, t < 0 ? make_uint4(0, 0, 0, 0) : ld16(x + t * xs + c));
-    for (int c = lane; c < scale_bytes; c += 32)
-        out_scales[r * scale_bytes + c] = t < 0 ? 0 : scales[t * scale_bytes + c];
+    W *const oscale = reinterpret_cast<W *>(out_scales);
+    pdl_wait();
+    pdl_trigger();
+    if ((int)blockIdx.x >= token_blocks) {
+        if (blockIdx.y) return;
+        const int warp = (threadIdx.y * blockDim.x + threadIdx.x) >> 5, warps = (blockDim.x * blockDim.y) >> 5;
+        const int64_t r0 = (((int64_t)blockIdx.x - token_blocks) * warps + warp) * zero_rows;
+        bool none = false;
+        if (lane < zero_rows && r0 + lane < R) {
+            const int p = rows[r0 + lane];
+            none = p < 0 || p >= T * (int64_t)k;
+        }
+        for (unsigned m = __ballot_sync(0xffffffffu, none); m; m &= m - 1) {
+            const int64_t r = r0 + __ffs(m) - 1;
+            for (int c = lane; c < n; c += 32) st16(out + r * row_bytes + c * 16, make_uint4(0, 0, 0, 0));
+            for (int c = lane; c < scale_words; c += 32) oscale[r * scale_words + c] = W{};
+        }
+        return;
+    }
+    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    if (t >= T) return;
+    // every lane of a warp has the same token: lane j holds pair j's row
+    int64_t mine = lane < k ? inv[t * k + lane] : -1;
+    if (mine >= R) mine = -1;
+    const int c0 = blockIdx.y * blockDim.x * kCopyPieces + threadIdx.x;
+    uint4 v[kCopyPieces];
+#pragma unroll
+    for (int i = 0; i < kCopyPieces; ++i)
+        if (c0 + i * (int)blockDim.x < n) v[i] = ld16(x + t * xs + (c0 + i * (int)blockDim.x) * 16);
+    for (int j = 0; j < k; ++j) {
+        const int64_t r = __shfl_sync(0xffffffffu, mine, j);
+        if (r < 0) continue;
+#pragma unroll
+        for (int i = 0; i < kCopyPieces; ++i)
+            if (c0 + i * (int)blockDim.x < n) st16(out + r * row_bytes + (c0 + i * (int)blockDim.x) * 16, v[i]);
+    }
+    const int parts = gridDim.y * blockDim.x;      // the scales, spread over the row's blocks
+    for (int c = blockIdx.y * blockDim.x + threadIdx.x - lane; c < scale_words; c += parts) {
+        const bool on = c + lane < scale_words;
+        const W s = on ? reinterpret_cast<const W *>(scales)[t * scale_words + c + lane] : W{};
+        for (int j = 0; j < k; ++j) {
+            const int64_t r = __shfl_sync(0xffffffffu, mine, j);
+            if (r >= 0 && on) oscale[r * scale_words + c + lane] = s;
+        }
+    }
 }
 
 // ---------------------------------------------------------------- combine
 
-constexpr int kPairBatch = 8;   // rows of a token in flight together
+// Bound by HBM: every pair's row read once, every token's written once.  A
+// thread has up to eight 16-byte loads in flight: KB pairs' rows of PP pieces
+// (KB x PP = 8), so that a token of two pairs asks for as much as one of eight
+// (16384 tokens of 4096, k = 2, bf16: 61 us against 99 us with one piece).
+// The registers are held to what lets an SM keep its blocks (4096 x 7168, k = 8,
+// bf16: 77.1 us at 64 registers, 101 % of the measured copy bandwidth; 80.8 us
+// at 66, with a block less; the rows passed between lanes by shuffles 87.9 us).
+constexpr int kCombineThreads = 128;
+constexpr int combine_blocks(int dt, int kb) { return dt == MOE_DTYPE_F32 ? (kb == 2 ? 4 : 5) : (kb == 2 ? 6 : 8); }
 
-template <int DT>
-__global__ void k_combine(const typename RowType<DT>::T *y, int k, int H, const int32_t *__restrict__ inv, int64_t R,
-                          const float *__restrict__ w, const typename RowType<DT>::T *base,
-                          typename RowType<DT>::T *out) {
-    const int64_t t = blockIdx.x;
-    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * kChunk;
-    if (c >= H) return;
-    float acc[8] = {};
-    for (int j0 = 0; j0 < k; j0 += kPairBatch) {
-        Raw8<DT> v[kPairBatch];
-        bool on[kPairBatch];
+template <int DT, int KB, int PP>
+__global__ void __launch_bounds__(kCombineThreads, combine_blocks(DT, KB)) k_combine(const typename RowType<DT>::T *y, int T, int k, int H,
+                                                 const int32_t *__restrict__ inv, int64_t R,
+                                                 const float *__restrict__ w, const typename RowType<DT>::T *base,
+                                                 typename RowType<DT>::T *out) {
+    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_trigger();
+    if (t >= T) return;
+    const int c0 = (blockIdx.y * PP * blockDim.x + threadIdx.x) * kChunk, dc = blockDim.x * kChunk;
+    if (c0 >= H) return;
+    float acc[PP][8] = {};
+    for (int j0 = 0; j0 < k; j0 += KB) {
+        Raw8<DT> v[KB][PP];
+        int row[KB];
 #pragma unroll
-        for (int j = 0; j < kPairBatch; ++j) {
-            const int row = j0 + j < k ? inv[t * k + j0 + j] : -1;
-            on[j] = row >= 0 && row < R;
-            if (on[j]) v[j] = load8<DT>(y + (int64_t)row * H + c);
+        for (int j = 0; j < KB; ++j) {
+            row[j] = j0 + j < k ? inv[t * k + j0 + j] : -1;
+            if (row[j] >= R) row[j] = -1;
+#pragma unroll
+            for (int i = 0; i < PP; ++i)
+                if (row[j] >= 0 && c0 + i * dc < H) v[j][i] = load8<DT>(y + (int64_t)row[j] * H + c0 + i * dc);
         }
 #pragma unroll
-        for (int j = 0; j < kPairBatch; ++j) {
-            if (!on[j]) continue;
+        for (int j = 0; j < KB; ++j) {
+            if (row[j] < 0) continue;
             const float wj = w ? w[t * k + j0 + j] : 1.0f;
-            float f[8];
-            widen8<DT>(v[j], f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = fmaf(wj, f[e], acc[e]);
+            for (int i = 0; i < PP; ++i) {
+                if (c0 + i * dc >= H) continue;
+                float f[8];
+                widen8<DT>(v[j][i], f);
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) fma2(acc[i][e], acc[i][e + 1], f[e], f[e + 1], wj, wj);
+            }
         }
     }
-    if (base) {
-        float f[8];
-        widen8<DT>(load8<DT>(base + t * H + c), f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += f[e];
+    for (int i = 0; i < PP; ++i) {
+        const int c = c0 + i * dc;
+        if (c >= H) continue;
+        if (base) {
+            float f[8];
+            widen8<DT>(load8<DT>(base + t * H + c), f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[i][e] += f[e];
+        }
+        store8<DT>(out + t * H + c, narrow8<DT>(acc[i]));
     }
-    store8<DT>(out + t * H + c, narrow8<DT>(acc));
 }
 
-// Blocks 0..T-1: one token each, its gradient row read once, every pair's row
-// of y read and of grad_y written once, the dot products reduced over the
-// block.  Later blocks: zeros for the rows without a pair, 8 rows a block.
-template <int DT>
+// Blocks (token, batch of kb pairs): the token's gradient row is read once a
+// batch, every pair's row of y read and of grad_y written once, the dot
+// products reduced over the block; or a token a warp and eight of them a block
+// (short rows: no block barrier).  Later blocks: zeros for the rows without a
+// pair, a warp a row.
+template <int DT, int KB, int PP, bool kWarp>
 __global__ void __launch_bounds__(256) k_combine_backward(const typename RowType<DT>::T *go,
-                                                          const typename RowType<DT>::T *y, int T, int k, int H,
+                                                          const typename RowType<DT>::T *y, int T, int k, int kb, int H,
                                                           const int32_t *__restrict__ rows,
                                                           const int32_t *__restrict__ inv, int64_t R,
                                                           const float *__restrict__ w,
-                                                          typename RowType<DT>::T *gy, float *__restrict__ gw) {
-    __shared__ float red[8][kPairBatch];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (blockIdx.x >= T) {
-        const int64_t r = ((int64_t)blockIdx.x - T) * 8 + warp;
-        if (r >= R) return;
-        const int p = rows[r];
-        if (p >= 0 && p < T * (int64_t)k) return;
-        const float zero[8] = {};
-        for (int c = lane * kChunk; c < H; c += 32 * kChunk) store8<DT>(gy + r * H + c, narrow8<DT>(zero));
+                                                          typename RowType<DT>::T *gy, float *__restrict__ gw,
+                                                          int token_blocks, int zero_rows) {
+    __shared__ float red[8][KB];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    pdl_wait();
+    pdl_trigger();
+    if ((int)blockIdx.x >= token_blocks) {
+        if (blockIdx.y) return;
+        const int64_t r0 = (((int64_t)blockIdx.x - token_blocks) * warps + warp) * zero_rows;
+        bool none = false;
+        if (lane < zero_rows && r0 + lane < R) {
+            const int p = rows[r0 + lane];
+            none = p < 0 || p >= T * (int64_t)k;
+        }
+        for (unsigned m = __ballot_sync(0xffffffffu, none); m; m &= m - 1) {
+            const int64_t r = r0 + __ffs(m) - 1;
+            for (int c = lane * kChunk; c < H; c += 32 * kChunk) store8<DT>(gy + r * H + c, Raw8<DT>{});
+        }
         return;
     }
-    const int64_t t = blockIdx.x;
-    for (int j0 = 0; j0 < k; j0 += kPairBatch) {
-        int64_t row[kPairBatch];
-        float wj[kPairBatch], dot[kPairBatch];
+    const int64_t t = kWarp ? (int64_t)blockIdx.x * 8 + warp : blockIdx.x;
+    if (kWarp && t >= T) return;
+    const int tid = kWarp ? lane : threadIdx.x, dc = (kWarp ? 32 : blockDim.x) * kChunk;
+    const int j0 = blockIdx.y * kb;
+    int row[KB];
+    float wj[KB], dot[KB];
 #pragma unroll
-        for (int j = 0; j < kPairBatch; ++j) {
-            row[j] = j0 + j < k ? inv[t * k + j0 + j] : -1;
-            if (row[j] >= R) row[j] = -1;
-            wj[j] = row[j] >= 0 ? w[t * k + j0 + j] : 0.0f;
-            dot[j] = 0.0f;
-        }
-        for (int c = threadIdx.x * kChunk; c < H; c += blockDim.x * kChunk) {
-            float g[8];
-            widen8<DT>(load8<DT>(go + t * H + c), g);
-            Raw8<DT> v[kPairBatch];
+    for (int j = 0; j < KB; ++j) {
+        const bool on = j < kb && j0 + j < k;
+        row[j] = on ? inv[t * k + j0 + j] : -1;
+        if (row[j] >= R) row[j] = -1;
+        wj[j] = row[j] >= 0 ? w[t * k + j0 + j] : 0.0f;
+        dot[j] = 0.0f;
+    }
+    for (int c0 = tid * kChunk; c0 < H; c0 += PP * dc) {
+        Raw8<DT> g[PP], v[KB][PP];
 #pragma unroll
-            for (int j = 0; j < kPairBatch; ++j)
-                if (row[j] >= 0) v[j] = load8<DT>(y + row[j] * H + c);
+        for (int i = 0; i < PP; ++i)
+            if (c0 + i * dc < H) g[i] = load8<DT>(go + t * H + c0 + i * dc);
 #pragma unroll
-            for (int j = 0; j < kPairBatch; ++j) {
+        for (int j = 0; j < KB; ++j)
+#pragma unroll
+            for (int i = 0; i < PP; ++i)
+                if (row[j] >= 0 && c0 + i * dc < H) v[j][i] = load8<DT>(y + (int64_t)row[j] * H + c0 + i * dc);
+#pragma unroll
+        for (int i = 0; i < PP; ++i) {
+            if (c0 + i * dc >= H) continue;
+            float gf[8];
+            widen8<DT>(g[i], gf);
+#pragma unroll
+            for (int j = 0; j < KB; ++j) {
                 if (row[j] < 0) continue;
-                float f[8], o[8];
-                widen8<DT>(v[j], f);
+                float f[8], d1 = 0.0f;
+                widen8<DT>(v[j][i], f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    dot[j] = fmaf(g[e], f[e], dot[j]);
-                    o[e] = wj[j] * g[e];
+                for (int e = 0; e < 8; e += 2) {
+                    fma2(dot[j], d1, f[e], f[e + 1], gf[e], gf[e + 1]);
+                    f[e] = gf[e];
+                    f[e + 1] = gf[e + 1];
+                    mul2(f, e, wj[j], wj[j]);
                 }
-                store8<DT>(gy + row[j] * H + c, narrow8<DT>(o));
+                dot[j] += d1;
+                store8<DT>(gy + (int64_t)row[j] * H + c0 + i * dc, narrow8<DT>(f));
             }
         }
+    }
 #pragma unroll
-        for (int j = 0; j < kPairBatch; ++j) {
-            const float s = warp_sum(dot[j]);
-            if (lane == 0) red[warp][j] = s;
+    for (int j = 0; j < KB; ++j) {
+        dot[j] = warp_sum(dot[j]);
+        if (kWarp) {
+            if (lane == j && j < kb && j0 + j < k) gw[t * k + j0 + j] = dot[j];
+        } else if (lane == 0) {
+            red[warp][j] = dot[j];
         }
-        __syncthreads();
-        if (threadIdx.x < kPairBatch && j0 + threadIdx.x < k) {
-            float s = 0.0f;
-            for (int i = 0; i < (int)blockDim.x / 32; ++i) s += red[i][threadIdx.x];
-            gw[t * k + j0 + threadIdx.x] = s;
-        }
-        __syncthreads();
+    }
+    if constexpr (kWarp) return;
+    __syncthreads();
+    if (threadIdx.x < kb && j0 + threadIdx.x < k) {
+        float s = 0.0f;
+        for (int i = 0; i < warps; ++i) s += red[i][threadIdx.x];
+        gw[t * k + j0 + threadIdx.x] = s;
     }
 }
 
-// Threads for a row of n8 pieces.
-int row_threads(int n8) { return std::min(256, (n8 + 31) / 32 * 32); }
+// Pairs a thread loads together, of k: 8, 4 or 2; few tokens have too few
+// threads for more than one piece each.
+int pair_batch(int k, bool few) { return few || k > 4 ? 8 : k > 2 ? 4 : 2; }
+int even_batch(int k, int most) { const int n = (k + most - 1) / most; return (k + n - 1) / n; }
+constexpr int kFewTokens = 2 * 152;
+// Up to here the backward pass takes a block a pair (4096 wide, k = 8, bf16: 4
+// tokens 2.3 us against 3.5 us, 128 tokens 5.7 against 6.2, 200 tokens 7.8 against 7.6).
+constexpr int kFewBackward = 152;
+
+template <int DT, int KB>
+cudaError_t launch_combine_k(const void *y, int T, int k, int H, const int32_t *inv, int64_t R, const float *w,
+                             const void *base, void *out, cudaStream_t st) {
+    using E = typename RowType<DT>::T;
+    constexpr int PP = 8 / KB;
+    const int n = (H / kChunk + PP - 1) / PP;                       // threads that a row can use
+    const int tx = std::min(kCombineThreads, (n + 31) / 32 * 32), ty = kCombineThreads / tx;
+    return launch_pdl(k_combine<DT, KB, PP>, dim3((T + ty - 1) / ty, (n + tx - 1) / tx), dim3(tx, ty), 0, st,
+                      static_cast<const E *>(y), T, k, H, inv, R, w, static_cast<const E *>(base),
+                      static_cast<E *>(out));
+}
 
 template <int DT>
 cudaError_t launch_combine(const void *y, int T, int k, int H, const int32_t *inv, int64_t R, const float *w,
                            const void *base, void *out, cudaStream_t st) {
+    switch (pair_batch(k, T <= kFewTokens)) {
+        case 2: return launch_combine_k<DT, 2>(y, T, k, H, inv, R, w, base, out, st);
+        case 4: return launch_combine_k<DT, 4>(y, T, k, H, inv, R, w, base, out, st);
+        default: return launch_combine_k<DT, 8>(y, T, k, H, inv, R, w, base, out, st);
+    }
+}
+
+template <int DT, int KB>
+cudaError_t launch_combine_backward_k(const void *go, const void *y, int T, int k, int H, const int32_t *rows,
+                                      const int32_t *inv, int64_t R, const float *w, void *gy, float *gw,
+                                      cudaStream_t st) {
     using E = typename RowType<DT>::T;
-    const int n8 = H / kChunk, th = row_threads(n8);
-    k_combine<DT><<<dim3(T, (n8 + th - 1) / th), th, 0, st>>>(static_cast<const E *>(y), k, H, inv, R, w,
-                                                             static_cast<const E *>(base), static_cast<E *>(out));
-    return cudaGetLastError();
+    constexpr int PP = 8 / KB;
+    const bool few = T <= kFewBackward, warp = !few && H / kChunk <= 128;
+    const int kb = few ? 1 : even_batch(k, KB);
+    const int pieces = (H / kChunk + PP - 1) / PP;                  // threads that a row can use
+    const int threads = warp ? 256 : std::min(256, (pieces + 31) / 32 * 32);
+    const int token_blocks = warp ? (T + 7) / 8 : T;
+    const int zero_rows = zero_rows_a_warp(H * (int)sizeof(E) / 16), block_rows = threads / 32 * zero_rows;
+    const dim3 grid((unsigned)(token_blocks + (R + block_rows - 1) / block_rows), (k + kb - 1) / kb);
+    auto kernel = warp ? k_combine_backward<DT, KB, PP, true> : k_combine_backward<DT, KB, PP, false>;
+    return launch_pdl(kernel, grid, dim3(threads), 0, st, static_cast<const E *>(go), static_cast<const E *>(y), T, k,
+                      kb, H, rows, inv, R, w, static_cast<E *>(gy), gw, token_blocks, zero_rows);
 }
 
 template <int DT>
 cudaError_t launch_combine_backward(const void *go, const void *y, int T, int k, int H, const int32_t *rows,
                                     const int32_t *inv, int64_t R, const float *w, void *gy, float *gw,
                                     cudaStream_t st) {
-    using E = typename RowType<DT>::T;
-    k_combine_backward<DT><<<(unsigned)(T + (R + 7) / 8), 256, 0, st>>>(
-        static_cast<const E *>(go), static_cast<const E *>(y), T, k, H, rows, inv, R, w, static_cast<E *>(gy), gw);
-    return cudaGetLastError();
+    switch (T <= kFewBackward ? 2 : pair_batch(k, false)) {
+        case 2: return launch_combine_backward_k<DT, 2>(go, y, T, k, H, rows, inv, R, w, gy, gw, st);
+        case 4: return launch_combine_backward_k<DT, 4>(go, y, T, k, H, rows, inv, R, w, gy, gw, st);
+        default: return launch_combine_backward_k<DT, 8>(go, y, T, k, H, rows, inv, R, w, gy, gw, st);
+    }
 }
 
 // ----------------------------------------------------------------- checks
@@ -334,20 +511,25 @@ moe_status moe_sort_pairs(const int32_t *topk_ids, int32_t T, int32_t k, int32_t
     if (configure_sort() != cudaSuccess) return MOE_ERR_CUDA;
     const int P = T * k, E = num_experts;
     int blocks = 1;
-    while (blocks < 8 && (int64_t)blocks * 2048 < P) blocks *= 2;
+    while (blocks < kSortBlocks && (int64_t)blocks * kSortPairs < P) blocks *= 2;
+    SortArgs a{topk_ids, P, E, align, 0, 0, rows, expert_offsets, sorted_rows, pair_rows};
+    a.warps = (int)std::min<int64_t>(kSortMaxWarps, ((int64_t)P + 32 * blocks - 1) / (32 * blocks));
+    a.run = (int)(((int64_t)P + 32LL * a.warps * blocks - 1) / (32LL * a.warps * blocks)) * 32;
+    const int threads = std::max(32 * a.warps, (E + 31) / 32 * 32);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(kSortThreads);
-    cfg.dynamicSmemBytes = sort_smem(E);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = sort_smem(a.warps, E);
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = blocks;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = blocks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, k_sort_pairs, topk_ids, P, E, (int)align, rows, expert_offsets,
-                                          sorted_rows, pair_rows));
+    cfg.numAttrs = blocks > 1 ? 2 : 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, blocks > 1 ? k_sort_pairs<true> : k_sort_pairs<false>, a));
 }
 
 moe_status moe_dispatch(const void *x, int64_t x_stride_bytes, int64_t row_bytes, const void *scales,
@@ -363,10 +545,26 @@ moe_status moe_dispatch(const void *x, int64_t x_stride_bytes, int64_t row_bytes
     if ((T > 0 && (!x || !pair_rows)) || !sorted_rows || !out) return MOE_ERR_INVALID_ARG;
     if (!aligned_to(x, 16) || !aligned_to(out, 16) || !aligned_to(sorted_rows, 4) || !aligned_to(pair_rows, 4))
         return MOE_ERR_MISALIGNED;
-    k_dispatch<<<(unsigned)((rows + 7) / 8), 256, 0, static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const char *>(x), x_stride_bytes, row_bytes, static_cast<const char *>(scales), scale_bytes, T, k,
-        sorted_rows, rows, static_cast<char *>(out), static_cast<char *>(out_scales));
-    return cuda_status(cudaGetLastError());
+    // a row's threads, the rows a block takes, and the blocks a row takes
+    const int n = (int)(row_bytes / 16);
+    const int tx = std::min(256, ((n + kCopyPieces - 1) / kCopyPieces + 31) / 32 * 32), ty = 256 / tx;
+    const int parts = (n + tx * kCopyPieces - 1) / (tx * kCopyPieces);
+    const int token_blocks = (T + ty - 1) / ty, zero_rows = zero_rows_a_warp(n);
+    const int block_rows = tx * ty / 32 * zero_rows;
+    const dim3 grid((unsigned)(token_blocks + (rows + block_rows - 1) / block_rows), parts);
+    if (parts > 65535) return MOE_ERR_UNSUPPORTED_SHAPE;
+    auto launch = [&](auto kernel, int word) {
+        return cuda_status(launch_pdl(kernel, grid, dim3(tx, ty), 0, static_cast<cudaStream_t>(stream),
+                                      static_cast<const char *>(x), x_stride_bytes, n,
+                                      static_cast<const char *>(scales), (int)(scale_bytes / word), (int)T, (int)k,
+                                      sorted_rows, pair_rows, rows, static_cast<char *>(out),
+                                      static_cast<char *>(out_scales), token_blocks, zero_rows));
+    };
+    // scale rows are copied in words as wide as their length and addresses allow
+    auto wide = [&](int a) { return scale_bytes % a == 0 && aligned_to(scales, a) && aligned_to(out_scales, a); };
+    if (wide(16)) return launch(k_dispatch<uint4>, 16);
+    if (wide(4)) return launch(k_dispatch<uint32_t>, 4);
+    return launch(k_dispatch<uint8_t>, 1);
 }
 
 moe_status moe_combine(const void *y, int32_t dtype, int32_t T, int32_t k, int32_t H, const int32_t *pair_rows,

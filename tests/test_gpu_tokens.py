@@ -253,6 +253,7 @@ def test_entries_out_of_range_count_as_no_pair():
     y = torch.randn(12, 32, device="cuda")
     bad = dict(order, pair_rows=order["pair_rows"].clone(), sorted_rows=order["sorted_rows"].clone())
     bad["pair_rows"][3] = torch.tensor([12, -9], dtype=torch.int32)
+    bad["pair_rows"][bad["pair_rows"] == 5] = 12      # in both arrays: no pair at row 5
     bad["sorted_rows"][5] = 12
     assert (moe.combine(y, bad)[3] == 0).all()
     assert (moe.dispatch(torch.randn(6, 32, device="cuda"), bad)["rows"][5] == 0).all()
