@@ -333,8 +333,10 @@ typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2 } moe_dt
  *   NONE:     no 8-bit output.
  *   E4M3_128: groups of 128 consecutive values, fp32 scales [T][ceil(H/128)].
  *   E4M3_ROW: one group a row, fp32 scales [T].
- *             For both: a = max(amax of the group, 2^-100), scale = a / 448,
- *             code = E4M3_rne_sat(n * (448 / a)).  A NaN makes its group NaN.
+ *             For both: a = max(amax of |n| in the group, 2^-100), scale =
+ *             a / 448, code = E4M3_rne_sat(n * 448 / a), computed from the
+ *             products p = s * weight as p * (448 / amax |p|), which must stay
+ *             in fp32's range.  A NaN makes its group NaN.
  *   MXFP8:    groups of 32, E8M0 scales uint8[T][ceil(H/32)]: byte =
  *             clamp(floor(log2(amax)) - 8 + 127, 0, 254) (0 for an all-zero
  *             group), code = E4M3_rne_sat(n * 2^(127 - byte)); a group whose

@@ -122,6 +122,11 @@ def _stream(stream=None):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+# The current stream's handle: 0.1 us a call where torch has it, 2.9 us through a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _check(status: int, where: str):
     if status != OK:
         raise MoeError(status, where)
@@ -185,9 +190,13 @@ def convert_f32(src: torch.Tensor, fmt: int, out: torch.Tensor | None = None, st
 
 
 # ------------------------------------------------ the token path around the experts' products
+#
+# A decode step makes these calls for a few microseconds of work each, so the checks are written
+# to cost little when they pass: one expression an argument, the text of a refusal only when one is due.
 
 _DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
 _GROUP = {QUANT_E4M3_128: 128, QUANT_MXFP8: 32}
+_F32, _I32 = torch.float32, torch.int32
 
 
 def _refuse(where: str, what: str, status: int = ERR_INVALID_ARG):
@@ -201,27 +210,37 @@ def _dtype(t, where):
     return d
 
 
-def _want(t, where, name, shape, dtype, device, strided=False):
-    """A tensor argument is where and what the kernels take it to be: contiguous (strided: rows of contiguous values)."""
-    if t.device != device or not t.is_cuda:
-        _refuse(where, f"{name} on {t.device}; every tensor is on one CUDA device")
-    if t.dtype != dtype or t.shape != shape:
-        _refuse(where, f"{name} {t.dtype}{list(t.shape)}; {dtype}{list(shape)} expected")
-    if not t.is_contiguous() and not (strided and t.dim() == 2 and t.stride(1) == 1):
-        _refuse(where, f"{name} is not contiguous")
-    return t
+def _device(t, where):
+    dev = t.device
+    if dev.type != "cuda":
+        _refuse(where, f"tensor on {dev}; a CUDA device expected")
+    return dev
 
 
-def _new(shape, dtype, device, stream):
+def _want(t, where, name, shape, dtype, dev):
+    """The tensor is where and what the kernel takes it to be; returns its address."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _refuse(where, f"{name} {t.dtype}{list(t.shape)} on {t.device}; contiguous {dtype}{list(shape)} on {dev} expected")
+    return t.data_ptr()
+
+
+def _want_rows(t, where, name, shape, dtype, dev):
+    """The same of rows of contiguous values a stride apart; returns their address and stride in values."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not (t.is_contiguous() or t.stride(1) == 1):
+        _refuse(where, f"{name} {t.dtype}{list(t.shape)} on {t.device}; rows of contiguous {dtype}{list(shape)} on {dev} expected")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _new(shape, dtype, dev, stream):
     """Memory that belongs to the stream the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _row_stride(t):
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _on(dev, stream):
+    return _raw_stream(dev.index) if stream is None else stream.cuda_stream
 
 
 def rms_norm(x, weight, residual=None, eps=1e-6, quant=QUANT_NONE, out=None, stream=None):
@@ -232,43 +251,47 @@ def rms_norm(x, weight, residual=None, eps=1e-6, quant=QUANT_NONE, out=None, str
     float8_e8m0fnu [T][ceil(H/32)] for QUANT_MXFP8).  An `out` may hold "y" beside "q", leave out "sum" or "rstd"
     (not written then), and give x or residual themselves as "sum"."""
     where = "moe_rms_norm"
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         _refuse(where, "x is not [T][H]")
-    T, H = x.shape
-    dev, dt = x.device, x.dtype
-    code = _dtype(x, where)
-    _want(x, where, "x", (T, H), dt, dev, strided=True)
-    _want(weight, where, "weight", (H,), dt, dev)
-    if residual is not None:
-        _want(residual, where, "residual", (T, H), dt, dev, strided=True)
-    if quant not in (QUANT_NONE, QUANT_E4M3_128, QUANT_E4M3_ROW, QUANT_MXFP8):
-        _refuse(where, f"quant {quant}")
-    sc_dtype = torch.float8_e8m0fnu if quant == QUANT_MXFP8 else torch.float32
-    sc_shape = (T, 1) if quant == QUANT_E4M3_ROW else (T, -(-H // _GROUP.get(quant, 1)))
+    T, H = shape
+    dev, dt, code = _device(x, where), x.dtype, _dtype(x, where)
+    xp, xs = _want_rows(x, where, "x", shape, dt, dev)
+    wp = _want(weight, where, "weight", (H,), dt, dev)
+    rp, rs = (None, 0) if residual is None else _want_rows(residual, where, "residual", shape, dt, dev)
+    sc_shape, sc_dtype = None, _F32
+    if quant != QUANT_NONE:
+        if quant not in (QUANT_E4M3_128, QUANT_E4M3_ROW, QUANT_MXFP8):
+            _refuse(where, f"quant {quant}")
+        sc_shape = (T, -(-H // _GROUP.get(quant, H or 1)))
+        if quant == QUANT_MXFP8:
+            sc_dtype = torch.float8_e8m0fnu
     if out is None:
-        out = {"rstd": _new((T,), torch.float32, dev, stream)}
+        out = {"rstd": _new((T,), _F32, dev, stream)}
         if residual is not None:
-            out["sum"] = _new((T, H), dt, dev, stream)
-        if quant == QUANT_NONE:
-            out["y"] = _new((T, H), dt, dev, stream)
+            out["sum"] = _new(shape, dt, dev, stream)
+        if sc_shape is None:
+            out["y"] = _new(shape, dt, dev, stream)
         else:
-            out["q"] = _new((T, H), torch.float8_e4m3fn, dev, stream)
+            out["q"] = _new(shape, torch.float8_e4m3fn, dev, stream)
             out["scales"] = _new(sc_shape, sc_dtype, dev, stream)
-    else:
-        for name, t in out.items():
-            if name in ("sum", "y"):
-                _want(t, where, name, (T, H), dt, dev)
-            elif name == "rstd":
-                _want(t, where, name, (T,), torch.float32, dev)
-            elif name == "q" and quant != QUANT_NONE:
-                _want(t, where, name, (T, H), torch.float8_e4m3fn, dev)
-            elif name == "scales" and quant != QUANT_NONE:
-                _want(t, where, name, sc_shape, sc_dtype, dev)
-            else:
-                _refuse(where, f"no output {name!r}")
-    _check(lib().moe_rms_norm(_ptr(x), _row_stride(x), _ptr(residual), 0 if residual is None else _row_stride(residual),
-                              _ptr(weight), T, H, code, eps, quant, _ptr(out.get("sum")), _ptr(out.get("y")),
-                              _ptr(out.get("q")), _ptr(out.get("scales")), _ptr(out.get("rstd")), _stream(stream)), where)
+    sp = yp = qp = cp = dp = None
+    for name, t in out.items():
+        if name == "sum":
+            sp = _want(t, where, name, shape, dt, dev)
+        elif name == "y":
+            yp = _want(t, where, name, shape, dt, dev)
+        elif name == "rstd":
+            dp = _want(t, where, name, (T,), _F32, dev)
+        elif name == "q" and sc_shape is not None:
+            qp = _want(t, where, name, shape, torch.float8_e4m3fn, dev)
+        elif name == "scales" and sc_shape is not None:
+            cp = _want(t, where, name, sc_shape, sc_dtype, dev)
+        else:
+            _refuse(where, f"no output {name!r}")
+    st = lib().moe_rms_norm(xp, xs, rp, rs, wp, T, H, code, eps, quant, sp, yp, qp, cp, dp, _on(dev, stream))
+    if st:
+        raise MoeError(st, where)
     return out
 
 
@@ -278,26 +301,26 @@ def rms_norm_backward(grad_y, sum, weight, rstd, grad_sum=None, out=None, stream
     `sum` is rms_norm's "sum" (x itself without a residual), `rstd` its "rstd"; `grad_sum` the gradient that reaches
     the sum on its other way (the residual stream)."""
     where = "moe_rms_norm_backward"
-    if sum.dim() != 2:
+    shape = sum.shape
+    if len(shape) != 2:
         _refuse(where, "sum is not [T][H]")
-    T, H = sum.shape
-    dev, dt = sum.device, sum.dtype
-    code = _dtype(sum, where)
-    _want(sum, where, "sum", (T, H), dt, dev)
-    _want(grad_y, where, "grad_y", (T, H), dt, dev)
-    _want(weight, where, "weight", (H,), dt, dev)
-    _want(rstd, where, "rstd", (T,), torch.float32, dev)
-    if grad_sum is not None:
-        _want(grad_sum, where, "grad_sum", (T, H), dt, dev)
+    T, H = shape
+    dev, dt, code = _device(sum, where), sum.dtype, _dtype(sum, where)
+    sp = _want(sum, where, "sum", shape, dt, dev)
+    yp = _want(grad_y, where, "grad_y", shape, dt, dev)
+    wp = _want(weight, where, "weight", (H,), dt, dev)
+    dp = _want(rstd, where, "rstd", (T,), _F32, dev)
+    gp = None if grad_sum is None else _want(grad_sum, where, "grad_sum", shape, dt, dev)
     if out is None:
-        out = {"grad_sum": _new((T, H), dt, dev, stream), "grad_w": _new((H,), torch.float32, dev, stream)}
-    else:
-        _want(out["grad_sum"], where, "out grad_sum", (T, H), dt, dev)
-        _want(out["grad_w"], where, "out grad_w", (H,), torch.float32, dev)
-    n = lib().moe_rms_norm_backward_workspace(T, H)
+        out = {"grad_sum": _new(shape, dt, dev, stream), "grad_w": _new((H,), _F32, dev, stream)}
+    op = _want(out["grad_sum"], where, "out grad_sum", shape, dt, dev)
+    ow = _want(out["grad_w"], where, "out grad_w", (H,), _F32, dev)
+    L = lib()
+    n = L.moe_rms_norm_backward_workspace(T, H)
     ws = _new((n,), torch.uint8, dev, stream)
-    _check(lib().moe_rms_norm_backward(_ptr(grad_y), _ptr(sum), _ptr(weight), _ptr(rstd), _ptr(grad_sum), T, H, code,
-                                       _ptr(out["grad_sum"]), _ptr(out["grad_w"]), _ptr(ws), n, _stream(stream)), where)
+    st = L.moe_rms_norm_backward(yp, sp, wp, dp, gp, T, H, code, op, ow, ws.data_ptr(), n, _on(dev, stream))
+    if st:
+        raise MoeError(st, where)
     return out
 
 
@@ -315,33 +338,32 @@ def sort_pairs(topk_ids, num_experts, align=1, out=None, stream=None):
     Returns {"expert_offsets": [E+1], "sorted_rows": [rows] (pair at a row, -1 none), "pair_rows": [T][k] (row of a
     pair, -1 dropped)}, int32; every expert's segment is padded to a multiple of `align` rows."""
     where = "moe_sort_pairs"
-    if topk_ids.dim() != 2:
+    shape = topk_ids.shape
+    if len(shape) != 2:
         _refuse(where, "topk_ids is not [T][k]")
-    T, k = topk_ids.shape
-    dev = topk_ids.device
-    _want(topk_ids, where, "topk_ids", (T, k), torch.int32, dev)
+    T, k = shape
+    dev = _device(topk_ids, where)
+    ip = _want(topk_ids, where, "topk_ids", shape, _I32, dev)
     R = sorted_rows(T * k, num_experts, align)
     if out is None:
-        out = {"expert_offsets": _new((num_experts + 1,), torch.int32, dev, stream),
-               "sorted_rows": _new((R,), torch.int32, dev, stream),
-               "pair_rows": _new((T, k), torch.int32, dev, stream)}
-    else:
-        _want(out["expert_offsets"], where, "out expert_offsets", (num_experts + 1,), torch.int32, dev)
-        _want(out["sorted_rows"], where, "out sorted_rows", (R,), torch.int32, dev)
-        _want(out["pair_rows"], where, "out pair_rows", (T, k), torch.int32, dev)
-    _check(lib().moe_sort_pairs(_ptr(topk_ids), T, k, num_experts, align, R, _ptr(out["expert_offsets"]),
-                                _ptr(out["sorted_rows"]), _ptr(out["pair_rows"]), _stream(stream)), where)
+        out = {"expert_offsets": _new((num_experts + 1,), _I32, dev, stream), "sorted_rows": _new((R,), _I32, dev, stream),
+               "pair_rows": _new(shape, _I32, dev, stream)}
+    op = _want(out["expert_offsets"], where, "out expert_offsets", (num_experts + 1,), _I32, dev)
+    rp = _want(out["sorted_rows"], where, "out sorted_rows", (R,), _I32, dev)
+    pp = _want(out["pair_rows"], where, "out pair_rows", shape, _I32, dev)
+    st = lib().moe_sort_pairs(ip, T, k, num_experts, align, R, op, rp, pp, _on(dev, stream))
+    if st:
+        raise MoeError(st, where)
     return out
 
 
 def _order(order, where, dev):
-    """sort_pairs' result: (sorted_rows, pair_rows, rows, T, k)."""
+    """sort_pairs' result: the addresses of sorted_rows and pair_rows, the number of rows, T and k."""
     rows, inv = order["sorted_rows"], order["pair_rows"]
-    if inv.dim() != 2 or rows.dim() != 1:
+    if rows.dim() != 1 or inv.dim() != 2:
         _refuse(where, "order is not sort_pairs' result")
-    _want(rows, where, "sorted_rows", rows.shape, torch.int32, dev)
-    _want(inv, where, "pair_rows", inv.shape, torch.int32, dev)
-    return rows, inv, rows.shape[0], inv.shape[0], inv.shape[1]
+    R, (T, k) = rows.shape[0], inv.shape
+    return _want(rows, where, "sorted_rows", (R,), _I32, dev), _want(inv, where, "pair_rows", (T, k), _I32, dev), R, T, k
 
 
 def dispatch(x, order, scales=None, out=None, stream=None):
@@ -349,30 +371,28 @@ def dispatch(x, order, scales=None, out=None, stream=None):
 
     Returns {"rows": [rows][H]} and, with scales [T][n], {"scales": [rows][n]}."""
     where = "moe_dispatch"
-    dev = x.device
-    rows, inv, R, T, k = _order(order, where, dev)
-    if x.dim() != 2 or x.shape[0] != T:
-        _refuse(where, f"x is not [{T}][H]")
-    H, es = x.shape[1], x.element_size()
-    _want(x, where, "x", (T, H), x.dtype, dev, strided=True)
-    sb = 0
+    dev = _device(x, where)
+    rp, pp, R, T, k = _order(order, where, dev)
+    if x.dim() != 2:
+        _refuse(where, "x is not [T][H]")
+    H, dt, es = x.shape[1], x.dtype, x.element_size()
+    xp, xs = _want_rows(x, where, "x", (T, H), dt, dev)
+    cp, cn, sb = None, 0, 0
     if scales is not None:
         if scales.dim() != 2:
             _refuse(where, "scales is not [T][n]")
-        _want(scales, where, "scales", (T, scales.shape[1]), scales.dtype, dev)
-        sb = scales.shape[1] * scales.element_size()
+        cn = scales.shape[1]
+        cp, sb = _want(scales, where, "scales", (T, cn), scales.dtype, dev), cn * scales.element_size()
     if out is None:
-        out = {"rows": _new((R, H), x.dtype, dev, stream)}
+        out = {"rows": _new((R, H), dt, dev, stream)}
         if scales is not None:
-            out["scales"] = _new((R, scales.shape[1]), scales.dtype, dev, stream)
-    else:
-        _want(out["rows"], where, "out rows", (R, H), x.dtype, dev)
-        if scales is not None:
-            _want(out["scales"], where, "out scales", (R, scales.shape[1]), scales.dtype, dev)
-        elif "scales" in out:
-            _refuse(where, "out scales without scales")
-    _check(lib().moe_dispatch(_ptr(x), _row_stride(x) * es, H * es, _ptr(scales), sb, T, k, _ptr(rows), _ptr(inv), R,
-                              _ptr(out["rows"]), _ptr(out.get("scales")), _stream(stream)), where)
+            out["scales"] = _new((R, cn), scales.dtype, dev, stream)
+    op, oc = _want(out["rows"], where, "out rows", (R, H), dt, dev), None
+    if scales is not None:
+        oc = _want(out["scales"], where, "out scales", (R, cn), scales.dtype, dev)
+    st = lib().moe_dispatch(xp, xs * es, H * es, cp, sb, T, k, rp, pp, R, op, oc, _on(dev, stream))
+    if st:
+        raise MoeError(st, where)
     return out
 
 
@@ -381,23 +401,20 @@ def combine(y, order, weights=None, base=None, out=None, stream=None):
 
     weights [T][k] fp32 (None: 1); base [T][H] is added where given.  Rows of y that hold no pair are not read."""
     where = "moe_combine"
-    dev = y.device
-    rows, inv, R, T, k = _order(order, where, dev)
+    dev = _device(y, where)
+    rp, pp, R, T, k = _order(order, where, dev)
     if y.dim() != 2:
         _refuse(where, "y is not [rows][H]")
-    H = y.shape[1]
-    code = _dtype(y, where)
-    _want(y, where, "y", (R, H), y.dtype, dev)
-    if weights is not None:
-        _want(weights, where, "weights", (T, k), torch.float32, dev)
-    if base is not None:
-        _want(base, where, "base", (T, H), y.dtype, dev)
+    H, dt, code = y.shape[1], y.dtype, _dtype(y, where)
+    yp = _want(y, where, "y", (R, H), dt, dev)
+    wp = None if weights is None else _want(weights, where, "weights", (T, k), _F32, dev)
+    bp = None if base is None else _want(base, where, "base", (T, H), dt, dev)
     if out is None:
-        out = _new((T, H), y.dtype, dev, stream)
-    else:
-        _want(out, where, "out", (T, H), y.dtype, dev)
-    _check(lib().moe_combine(_ptr(y), code, T, k, H, _ptr(inv), R, _ptr(weights), _ptr(base), _ptr(out),
-                             _stream(stream)), where)
+        out = _new((T, H), dt, dev, stream)
+    op = _want(out, where, "out", (T, H), dt, dev)
+    st = lib().moe_combine(yp, code, T, k, H, pp, R, wp, bp, op, _on(dev, stream))
+    if st:
+        raise MoeError(st, where)
     return out
 
 
@@ -411,22 +428,21 @@ def combine_backward(grad_out, y, order, weights, out=None, stream=None):
 
     base's gradient is grad_out itself.  out["grad_y"] may be y."""
     where = "moe_combine_backward"
-    dev = y.device
-    rows, inv, R, T, k = _order(order, where, dev)
+    dev = _device(y, where)
+    rp, pp, R, T, k = _order(order, where, dev)
     if y.dim() != 2:
         _refuse(where, "y is not [rows][H]")
-    H = y.shape[1]
-    code = _dtype(y, where)
-    _want(y, where, "y", (R, H), y.dtype, dev)
-    _want(grad_out, where, "grad_out", (T, H), y.dtype, dev)
-    _want(weights, where, "weights", (T, k), torch.float32, dev)
+    H, dt, code = y.shape[1], y.dtype, _dtype(y, where)
+    yp = _want(y, where, "y", (R, H), dt, dev)
+    gp = _want(grad_out, where, "grad_out", (T, H), dt, dev)
+    wp = _want(weights, where, "weights", (T, k), _F32, dev)
     if out is None:
-        out = {"grad_y": _new((R, H), y.dtype, dev, stream), "grad_w": _new((T, k), torch.float32, dev, stream)}
-    else:
-        _want(out["grad_y"], where, "out grad_y", (R, H), y.dtype, dev)
-        _want(out["grad_w"], where, "out grad_w", (T, k), torch.float32, dev)
-    _check(lib().moe_combine_backward(_ptr(grad_out), _ptr(y), code, T, k, H, _ptr(rows), _ptr(inv), R, _ptr(weights),
-                                      _ptr(out["grad_y"]), _ptr(out["grad_w"]), _stream(stream)), where)
+        out = {"grad_y": _new((R, H), dt, dev, stream), "grad_w": _new((T, k), _F32, dev, stream)}
+    oy = _want(out["grad_y"], where, "out grad_y", (R, H), dt, dev)
+    ow = _want(out["grad_w"], where, "out grad_w", (T, k), _F32, dev)
+    st = lib().moe_combine_backward(gp, yp, code, T, k, H, rp, pp, R, wp, oy, ow, _on(dev, stream))
+    if st:
+        raise MoeError(st, where)
     return out
 
 

@@ -99,6 +99,22 @@ template <int DT> __device__ __forceinline__ void norm8(const Raw8<DT> &s, const
     }
 }
 
+// p = s * weight of one piece, exact for 16-bit rows.
+template <int DT> __device__ __forceinline__ void product8(const Raw8<DT> &s, const Raw8<DT> &w, float (&p)[8]) {
+    float g[8];
+    widen8<DT>(s, p);
+    widen8<DT>(w, g);
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) mul2(p, e, g[e], g[e + 1]);
+}
+
+// A group's factor to its codes' scale, of its products p: with top = amax p *
+// rstd and a = max(top, 2^-100) a code is that of p * rstd * 448 / a, which is
+// p * (448 / amax p) but for the bound.
+__device__ __forceinline__ float e4m3_factor(float amax_p, float top, float rstd) {
+    return top > kMinAmax ? __fdiv_rn(448.0f, amax_p) : __fmul_rn(rstd, 448.0f / kMinAmax);
+}
+
 __device__ __forceinline__ float amax8(const float (&n)[8], float m) {
 #pragma unroll
     for (int e = 0; e < 8; e += 2) m = amax3(m, n[e], n[e + 1]);
@@ -165,38 +181,45 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
     }
     const float rstd = row_rstd(row_sum<kWarp>(s0 + s1, red[0]), a.H, a.eps);
     if (a.rstd && tid == 0) a.rstd[t] = rstd;
-    float row_amax = 0.0f;
+    float row_mul = 0.0f;
     if constexpr (Q == MOE_QUANT_E4M3_ROW) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float f[8];
-            norm8<DT>(s[i], w[i], rstd, f);
-            row_amax = amax8(f, row_amax);
+            product8<DT>(s[i], w[i], f);
+            row_mul = amax8(f, row_mul);
         }
-        row_amax = max_nan(row_max_nan<kWarp>(row_amax, red[1]), kMinAmax);
-        if (tid == 0) static_cast<float *>(a.scales)[t] = __fdiv_rn(row_amax, 448.0f);
+        row_mul = row_max_nan<kWarp>(row_mul, red[1]);
+        const float top = __fmul_rn(row_mul, rstd);
+        row_mul = e4m3_factor(row_mul, top, rstd);
+        if (tid == 0) static_cast<float *>(a.scales)[t] = __fdiv_rn(max_nan(top, kMinAmax), 448.0f);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = tid + i * n;
         float f[8];
-        norm8<DT>(s[i], w[i], rstd, f);
-        if (a.y && c < n8) store8<DT>(static_cast<T *>(a.y) + t * a.H + c * kChunk, narrow8<DT>(f));
+        if (a.y) {
+            norm8<DT>(s[i], w[i], rstd, f);
+            if (c < n8) store8<DT>(static_cast<T *>(a.y) + t * a.H + c * kChunk, narrow8<DT>(f));
+        }
         if constexpr (Q == MOE_QUANT_NONE) continue;
-        float mul;
-        if constexpr (Q == MOE_QUANT_E4M3_ROW) {
-            mul = __fdiv_rn(448.0f, row_amax);
-        } else {
+        product8<DT>(s[i], w[i], f);
+        float mul = row_mul;
+        if constexpr (Q != MOE_QUANT_E4M3_ROW) {
             constexpr int kLanes = Q == MOE_QUANT_MXFP8 ? 4 : 16;
+            if constexpr (Q == MOE_QUANT_MXFP8) {
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) mul2(f, e, rstd, rstd);
+            }
             float m = amax8(f, 0.0f);
 #pragma unroll
             for (int o = kLanes / 2; o >= 1; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
             const bool first = c < n8 && (c % kLanes) == 0;
             const int64_t at = t * ((n8 + kLanes - 1) / kLanes) + c / kLanes;
             if constexpr (Q == MOE_QUANT_E4M3_128) {
-                m = max_nan(m, kMinAmax);
-                mul = __fdiv_rn(448.0f, m);
-                if (first) static_cast<float *>(a.scales)[at] = __fdiv_rn(m, 448.0f);
+                const float top = __fmul_rn(m, rstd);
+                mul = e4m3_factor(m, top, rstd);
+                if (first) static_cast<float *>(a.scales)[at] = __fdiv_rn(max_nan(top, kMinAmax), 448.0f);
             } else {
                 // floor(log2(amax)) + 127 is the exponent field of a normal amax;
                 // E4M3's largest exponent is 8
