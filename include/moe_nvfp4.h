@@ -421,7 +421,7 @@ moe_status moe_dispatch(const void *x, int64_t x_stride_bytes, int64_t row_bytes
  * padding are not read; a token without pairs gets base (0 without one).
  *   y [rows][H], base (NULL: none) and out [T][H] of `dtype`; weights [T][k]
  *   fp32 or NULL for 1 (the gradient of moe_dispatch).  out may be base's
- *   memory.  H: a multiple of 8. */
+ *   memory.  H: a multiple of 8 up to 65536. */
 moe_status moe_combine(const void *y, int32_t dtype, int32_t T, int32_t k, int32_t H, const int32_t *pair_rows,
                        int64_t rows, const float *weights, const void *base, void *out, void *stream);
 

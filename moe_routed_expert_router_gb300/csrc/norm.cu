@@ -58,17 +58,24 @@ template <bool kWarp> __device__ __forceinline__ float row_sum(float v, float *r
     return warp_sum(lane < nw ? red[lane] : 0.0f);
 }
 
-template <bool kWarp> __device__ __forceinline__ float row_max_nan(float v, float *red) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
-    if constexpr (kWarp) return v;
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
-    v = lane < nw ? red[lane] : 0.0f;
+// The sum of one value and the maximum of another, with one barrier.
+__device__ __forceinline__ float warp_max_nan(float v) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
+}
+template <bool kWarp> __device__ __forceinline__ void row_sum_max(float &sum, float &top, float (&red)[2][32]) {
+    sum = warp_sum(sum);
+    top = warp_max_nan(top);
+    if constexpr (kWarp) return;
+    const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) {
+        red[0][threadIdx.x >> 5] = sum;
+        red[1][threadIdx.x >> 5] = top;
+    }
+    __syncthreads();
+    sum = warp_sum(lane < nw ? red[0][lane] : 0.0f);
+    top = warp_max_nan(lane < nw ? red[1][lane] : 0.0f);
 }
 
 // Four fp32 -> four E4M3 bytes, round to nearest even, saturating; NaN -> 0x7F.
@@ -138,8 +145,8 @@ template <int DT> __device__ __forceinline__ Raw8<DT> add8(const Raw8<DT> &x, co
     return s;
 }
 
-// A row a block (G = 1), or a row a warp and eight of them a block (rows of up
-// to 1024 values: no block barrier, and short rows fill an SM).  Thread i of a
+// A row a block, or (rows of up to 512 values) a row a warp and eight of them a
+// block: no block barrier, and short rows fill an SM.  Thread i of a
 // row's n (a multiple of 32) holds pieces i, i + n, ..., so a warp's accesses
 // are 512 consecutive bytes of a 16-bit row, a 128-value group is 16
 // neighbouring lanes and a 32-value group is four.  All of a thread's loads are
@@ -179,17 +186,21 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
 #pragma unroll
         for (int e = 0; e < 8; e += 2) fma2(s0, s1, f[e], f[e + 1], f[e], f[e + 1]);
     }
-    const float rstd = row_rstd(row_sum<kWarp>(s0 + s1, red[0]), a.H, a.eps);
-    if (a.rstd && tid == 0) a.rstd[t] = rstd;
-    float row_mul = 0.0f;
-    if constexpr (Q == MOE_QUANT_E4M3_ROW) {
+    float sum = s0 + s1, row_mul = 0.0f;
+    if constexpr (Q == MOE_QUANT_E4M3_ROW) {   // the row's largest product, on the same barrier
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float f[8];
             product8<DT>(s[i], w[i], f);
             row_mul = amax8(f, row_mul);
         }
-        row_mul = row_max_nan<kWarp>(row_mul, red[1]);
+        row_sum_max<kWarp>(sum, row_mul, red);
+    } else {
+        sum = row_sum<kWarp>(sum, red[0]);
+    }
+    const float rstd = row_rstd(sum, a.H, a.eps);
+    if (a.rstd && tid == 0) a.rstd[t] = rstd;
+    if constexpr (Q == MOE_QUANT_E4M3_ROW) {
         const float top = __fmul_rn(row_mul, rstd);
         row_mul = e4m3_factor(row_mul, top, rstd);
         if (tid == 0) static_cast<float *>(a.scales)[t] = __fdiv_rn(max_nan(top, kMinAmax), 448.0f);
@@ -254,16 +265,23 @@ struct NormGradArgs {
 // that it waits for); R = 1 is for
 // rows of which two do not fit.  Rows of up to 1024 values take a warp each, as
 // in the forward pass; the eight warps' sums are then added in order.
+//
+// Piece i of a thread is one 16-byte word of a 16-bit row or two of an fp32
+// row, n words apart: neighbouring lanes copy neighbouring words (8192 fp32
+// rows of 4096: 83 us, with a thread's two words side by side 141 us).  Words
+// past an fp32 row are zeros; a 16-bit piece past the row is passed over.
 template <int DT, int V, int R, bool kWarp>
 __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_norm_backward(const NormGradArgs a) {
     using T = typename RowType<DT>::T;
-    extern __shared__ __align__(16) uint4 smem[];     // a row's [R][gy, s, gs][V][Raw8 words][n]
+    extern __shared__ __align__(16) uint4 smem[];     // a row's [R][gy, s, gs][V][words][n]
     __shared__ float red[2][32];
     const int tid = kWarp ? threadIdx.x & 31 : threadIdx.x, group = kWarp ? threadIdx.x >> 5 : 0;
-    const int n8 = a.H / kChunk, n = kWarp ? 32 : blockDim.x;
-    constexpr int kWords = sizeof(Raw8<DT>) / 16;
+    const int n = kWarp ? 32 : blockDim.x;
+    constexpr int kWords = sizeof(Raw8<DT>) / 16, kWord = 8 / kWords;   // values a word
     const int arr = V * kWords * n, stage = (a.gs ? 3 : 2) * arr;
     uint4 *ring = smem + group * R * stage;
+    auto col = [&](int i, int h) { return ((i * kWords + h) * n + tid) * kWord; };
+    auto past = [&](int i) { return kWords == 1 && col(i, 0) >= a.H; };
     float gw[V][8];
     Raw8<DT> w[V];
     pdl_wait();
@@ -273,19 +291,25 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
 #pragma unroll
         for (int e = 0; e < 8; ++e) gw[i][e] = 0.0f;
         w[i] = Raw8<DT>{};
-        if (tid + i * n < n8) w[i] = load8_shared<DT>(static_cast<const T *>(a.w) + (tid + i * n) * kChunk);
+#pragma unroll
+        for (int h = 0; h < kWords; ++h)
+            if (col(i, h) < a.H)
+                (&w[i].a)[h] = ld16_shared(static_cast<const T *>(a.w) + col(i, h));
     }
     auto fetch = [&](int64_t t, int slot) {
         if (t < a.T) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int c = tid + i * n;
-                if (c >= n8) continue;
-                const int64_t from = t * a.H + c * kChunk;
-                uint4 *at = ring + slot * stage + i * kWords * n + tid;
-                copy8<DT>(at, n, static_cast<const T *>(a.gy) + from);
-                copy8<DT>(at + arr, n, static_cast<const T *>(a.s) + from);
-                if (a.gs) copy8<DT>(at + 2 * arr, n, static_cast<const T *>(a.gs) + from);
+                if (past(i)) continue;
+#pragma unroll
+                for (int h = 0; h < kWords; ++h) {
+                    const bool on = kWords == 1 || col(i, h) < a.H;
+                    const int64_t from = t * a.H + (on ? col(i, h) : 0);
+                    uint4 *at = ring + slot * stage + (i * kWords + h) * n + tid;
+                    copy16(at, static_cast<const T *>(a.gy) + from, on);
+                    copy16(at + arr, static_cast<const T *>(a.s) + from, on);
+                    if (a.gs) copy16(at + 2 * arr, static_cast<const T *>(a.gs) + from, on);
+                }
             }
         }
         copy_commit();
@@ -302,7 +326,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
         float d0 = 0.0f, d1 = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (tid + i * n >= n8) continue;
+            if (past(i)) continue;
             const uint4 *at = ring + slot * stage + i * kWords * n + tid;
             g[i] = take8<DT>(at, n);
             s[i] = take8<DT>(at + arr, n);
@@ -321,7 +345,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
         const float c1 = -(row_sum<kWarp>(d0 + d1, red[par]) / (float)a.H);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (tid + i * n >= n8) continue;
+            if (past(i)) continue;
             float f[8], m[8], wf[8], o[8];
             Raw8<DT> q{};
             if (a.gs) q = take8<DT>(ring + slot * stage + 2 * arr + i * kWords * n + tid, n);
@@ -336,42 +360,42 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
                 fma2(f[e], f[e + 1], m[e], m[e + 1], c1, c1);
                 fma2(o[e], o[e + 1], f[e], f[e + 1], rstd, rstd);
             }
-            store8<DT>(static_cast<T *>(a.gin) + t * a.H + (tid + i * n) * kChunk, narrow8<DT>(o));
+            const Raw8<DT> out = narrow8<DT>(o);
+#pragma unroll
+            for (int h = 0; h < kWords; ++h)
+                if (col(i, h) < a.H) st16(static_cast<T *>(a.gin) + t * a.H + col(i, h), (&out.a)[h]);
         }
         if constexpr (R == 2) slot ^= 1;
     }
+    float *sums = kWarp ? reinterpret_cast<float *>(smem) + group * a.H : a.part + (int64_t)blockIdx.x * a.H;
     if constexpr (kWarp) {
         copy_wait<0>();
         __syncthreads();                              // the ring is free: the warps' sums, [8][H]
-        float *sums = reinterpret_cast<float *>(smem);
+    }
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if (tid + i * n >= n8) continue;
-            float4 *at = reinterpret_cast<float4 *>(sums + group * a.H + (tid + i * n) * kChunk);
-            at[0] = make_float4(gw[i][0], gw[i][1], gw[i][2], gw[i][3]);
-            at[1] = make_float4(gw[i][4], gw[i][5], gw[i][6], gw[i][7]);
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int h = 0; h < kWords; ++h) {
+            if (col(i, h) >= a.H) continue;
+#pragma unroll
+            for (int e = 0; e < kWord; e += 4)
+                *reinterpret_cast<float4 *>(sums + col(i, h) + e) =
+                    make_float4(gw[i][h * kWord + e], gw[i][h * kWord + e + 1], gw[i][h * kWord + e + 2], gw[i][h * kWord + e + 3]);
         }
+    if constexpr (kWarp) {
         __syncthreads();
         for (int h = threadIdx.x; h < a.H; h += blockDim.x) {
             float v = 0.0f;
 #pragma unroll
-            for (int g = 0; g < kWarpRows; ++g) v += sums[g * a.H + h];
+            for (int g = 0; g < kWarpRows; ++g) v += reinterpret_cast<float *>(smem)[g * a.H + h];
             a.part[(int64_t)blockIdx.x * a.H + h] = v;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = tid + i * n;
-            if (c >= n8) continue;
-            store8<MOE_DTYPE_F32>(a.part + (int64_t)blockIdx.x * a.H + c * kChunk, narrow8<MOE_DTYPE_F32>(gw[i]));
         }
     }
 }
 
 // grad_w[h] = sum of the blocks' partial sums: thread (i, j) adds every 32nd
 // block's from j on, four columns wide, then the 32 sums are added in order.
-__global__ void __launch_bounds__(256) k_rms_norm_grad_w(const float *__restrict__ part, int blocks, int H,
-                                                         float *__restrict__ gw) {
+__global__ void __launch_bounds__(256) k_rms_norm_grad_w(const float *part, int blocks, int H, float *gw) {
     __shared__ float4 s[32][8];
     const int i = threadIdx.x & 7, j = threadIdx.x >> 3;
     const int h = blockIdx.x * 32 + i * 4;
@@ -463,14 +487,14 @@ template <int DT> cudaError_t launch_norm(const NormArgs &a, int quant, int T, c
 // 46.0 us with four, 58.1 with two; H = 6144 133 us with two, 171 with three,
 // whose third waits); every block writes a row of partial sums.
 struct GradShape { RowShape row; bool warp; int blocks; };
-GradShape grad_shape(int T, int H) {
+GradShape grad_shape(int T, int H, int dtype) {
     const int n8 = H / kChunk;
     GradShape g;
-    g.warp = n8 <= kWarpPieces;
+    g.warp = n8 <= (dtype == MOE_DTYPE_F32 ? kWarpPieces / 2 : kWarpPieces);   // a warp's ring of fp32 rows is twice as large
     g.row = g.warp ? RowShape{32, warp_pieces(n8)} : row_shape(n8, false);
     const int an_sm = std::max(2, std::min(4, 512 / (g.warp ? 32 * kWarpRows : g.row.threads)));
-    const int rows = g.warp ? kWarpRows : 1;
-    g.blocks = std::min((T - 1) / rows + 1, an_sm * kSms);
+    const int groups = g.warp ? (T - 1) / kWarpRows + 1 : T;          // rows, or eights of them
+    g.blocks = std::min(groups, an_sm * kSms);
     return g;
 }
 
@@ -489,14 +513,17 @@ cudaError_t launch_norm_grad_v(const NormGradArgs &a, int blocks, int threads, s
 template <int DT> cudaError_t launch_norm_grad(const NormGradArgs &a, const GradShape &g, cudaStream_t st) {
     const int threads = g.row.threads, v = g.row.v, blocks = g.blocks;
     const size_t stage = (a.gs ? 3 : 2) * sizeof(Raw8<DT>) * v * threads;
+    constexpr bool f32 = DT == MOE_DTYPE_F32;
     if (g.warp) {
         if (v == 1) return launch_norm_grad_v<DT, 1, 2, true>(a, blocks, threads, stage, st);
-        if (v == 2) return launch_norm_grad_v<DT, 2, 2, true>(a, blocks, threads, stage, st);
-        return launch_norm_grad_v<DT, 4, 2, true>(a, blocks, threads, stage, st);
+        if (v == 2 || f32) return launch_norm_grad_v<DT, 2, 2, true>(a, blocks, threads, stage, st);
+        return launch_norm_grad_v<DT, f32 ? 2 : 4, 2, true>(a, blocks, threads, stage, st);
+    }
+    if constexpr (f32) {
+        if (v == 1) return launch_norm_grad_v<DT, 1, 2, false>(a, blocks, threads, stage, st);
+        if (2 * stage > kSmemSm - 2048) return launch_norm_grad_v<DT, 4, 1, false>(a, blocks, threads, stage, st);
     }
     if (v == 2) return launch_norm_grad_v<DT, 2, 2, false>(a, blocks, threads, stage, st);
-    if constexpr (DT == MOE_DTYPE_F32)
-        if (2 * stage > kSmemSm - 2048) return launch_norm_grad_v<DT, 4, 1, false>(a, blocks, threads, stage, st);
     return launch_norm_grad_v<DT, 4, 2, false>(a, blocks, threads, stage, st);
 }
 
@@ -541,7 +568,9 @@ moe_status moe_rms_norm(const void *x, int64_t x_stride, const void *residual, i
 
 size_t moe_rms_norm_backward_workspace(int32_t T, int32_t H) {
     if (T <= 0 || H <= 0) return 0;
-    return sizeof(float) * (size_t)grad_shape(T, H).blocks * (size_t)H;
+    size_t blocks = 0;
+    for (int dtype : {MOE_DTYPE_F32, MOE_DTYPE_BF16}) blocks = std::max(blocks, (size_t)grad_shape(T, H, dtype).blocks);
+    return sizeof(float) * blocks * (size_t)H;
 }
 
 moe_status moe_rms_norm_backward(const void *grad_y, const void *sum, const void *weight, const float *rstd,
@@ -557,7 +586,7 @@ moe_status moe_rms_norm_backward(const void *grad_y, const void *sum, const void
         return MOE_ERR_MISALIGNED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (T == 0) return cuda_status(cudaMemsetAsync(grad_w, 0, sizeof(float) * H, s));
-    const GradShape g = grad_shape(T, H);
+    const GradShape g = grad_shape(T, H, dtype);
     const NormGradArgs a{grad_y, sum, weight, grad_sum, rstd, T, H, grad_in, static_cast<float *>(workspace)};
     cudaError_t e;
     switch (dtype) {

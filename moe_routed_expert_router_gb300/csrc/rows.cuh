@@ -32,8 +32,10 @@ __device__ __forceinline__ void st16(void *p, uint4 v) {
 
 // 16 bytes from global into shared memory without registers (cp.async); a
 // thread's copies since the last commit form a group.
-__device__ __forceinline__ void copy16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+// `on` false: zeros, and `src` (any valid address) is not read.
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Until at most N of the thread's latest groups are unfinished.
@@ -46,11 +48,7 @@ template <int DT> __device__ __forceinline__ Raw8<DT> load8(const typename RowTy
     return r;
 }
 
-// Eight values into shared memory, `n` words apart where they take two, and back.
-template <int DT> __device__ __forceinline__ void copy8(uint4 *at, int n, const typename RowType<DT>::T *p) {
-    copy16(at, p);
-    if constexpr (DT == MOE_DTYPE_F32) copy16(at + n, p + 4);
-}
+// Eight values from shared memory, `n` words apart where they take two.
 template <int DT> __device__ __forceinline__ Raw8<DT> take8(const uint4 *at, int n) {
     Raw8<DT> v;
     v.a = at[0];
@@ -58,11 +56,19 @@ template <int DT> __device__ __forceinline__ Raw8<DT> take8(const uint4 *at, int
     return v;
 }
 
-// The same of a read-only row that other blocks read too (a weight): kept in L1.
+// The same of a row that other blocks read too (a weight): kept in L1.  Not the
+// read-only kind either: with dependent launches the kernel before may still be
+// writing when this one's first blocks start.
+__device__ __forceinline__ uint4 ld16_shared(const void *p) {
+    uint4 r;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+    return r;
+}
 template <int DT> __device__ __forceinline__ Raw8<DT> load8_shared(const typename RowType<DT>::T *p) {
     Raw8<DT> r;
-    r.a = __ldg(reinterpret_cast<const uint4 *>(p));
-    if constexpr (DT == MOE_DTYPE_F32) r.b = __ldg(reinterpret_cast<const uint4 *>(p + 4));
+    r.a = ld16_shared(p);
+    if constexpr (DT == MOE_DTYPE_F32) r.b = ld16_shared(p + 4);
     return r;
 }
 

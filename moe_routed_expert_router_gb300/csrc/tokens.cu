@@ -14,6 +14,9 @@ namespace {
 
 using namespace moe;
 
+constexpr int64_t kMaxRows = 0x7fffffff;   // rows, pairs and blocks of a launch
+constexpr int kMaxCombineH = 65536;
+
 // ------------------------------------------------------------------- sort
 
 constexpr int kMaxAlign = 256;
@@ -180,51 +183,76 @@ cudaError_t configure_sort() {
 
 // --------------------------------------------------------------- dispatch
 
+// Rows that a warp looks at for ones without a pair: a row of 512 pieces, up to
+// 32 shorter ones (16384 x 256, bf16, no padding: 12.6 us for the dispatch,
+// with one row a warp 25.8 us).
+int zero_rows_a_warp(int pieces) { return std::max(1, std::min(32, 512 / pieces)); }
+
+// Zeros for those of the `zero_rows` rows from r0 on that hold no pair, n words
+// of each at `out`: a row at a time, or, where a row is shorter than a warp is
+// wide, the lanes spread over all of them.
+__device__ __forceinline__ void put_zero(uint4 *p) { st16(p, make_uint4(0, 0, 0, 0)); }
+__device__ __forceinline__ void put_zero(uint32_t *p) { *p = 0; }
+__device__ __forceinline__ void put_zero(uint8_t *p) { *p = 0; }
+
+template <typename W>
+__device__ __forceinline__ void zero_words(W *out, int n, int64_t r0, int zero_rows, unsigned none, int lane) {
+    if (n >= 32) {
+        for (unsigned m = none; m; m &= m - 1) {
+            W *row = out + (r0 + __ffs(m) - 1) * n;
+            for (int c = lane; c < n; c += 32) put_zero(row + c);
+        }
+    } else {
+        for (int i = lane; i < zero_rows * n; i += 32)
+            if (none >> (i / n) & 1) put_zero(out + r0 * n + i);
+    }
+}
+
+__device__ __forceinline__ unsigned rows_without_pair(const int32_t *rows, int64_t r0, int zero_rows, int64_t R,
+                                                      int64_t P, int lane) {
+    bool none = false;
+    if (lane < zero_rows && r0 + lane < R) {
+        const int p = rows[r0 + lane];
+        none = p < 0 || p >= P;
+    }
+    return __ballot_sync(0xffffffffu, none);
+}
+
 // Bound by the HBM writes, so nothing is read twice: a thread holds two 16-byte
 // pieces of a token's row and stores them to each of the token's rows (4096 x
-// 7168, 8 of 256 experts: 73 us in 8 bits with padding to 128 rows, 104 % of
+// 7168, 8 of 256 experts: 73 us in 8 bits with padding to 128 rows, 102 % of
 // the measured copy bandwidth; a warp a row of out, which reads a token's row
-// once a pair, 97 us).  Blocks: threadIdx.y and blockIdx.x choose the token,
-// blockIdx.y the part of its row.  Blocks past the tokens' write zeros to the
-// rows without a pair.
+// once a pair, 97 us).  A row of threads has a token and a part of its row; the
+// blocks past the tokens' write zeros to the rows without a pair.
 constexpr int kCopyPieces = 2;
-
-// Rows that a warp looks at for ones without a pair: a row of 512 pieces, up to
-// 32 shorter ones.
-int zero_rows_a_warp(int pieces) { return std::max(1, std::min(32, 512 / pieces)); }
 
 template <typename W>
 __global__ void __launch_bounds__(256) k_dispatch(const char *x, int64_t xs, int n, const char *scales, int scale_words,
-                                                  int T, int k, const int32_t *__restrict__ rows,
-                                                  const int32_t *__restrict__ inv, int64_t R, char *out,
-                                                  char *out_scales, int token_blocks, int zero_rows) {
+                                                  int T, int k, const int32_t *rows,
+                                                  const int32_t *inv, int64_t R, char *out,
+                                                  char *out_scales, int token_blocks, int parts,
+                                                  int zero_rows) {
     const int64_t row_bytes = (int64_t)n * 16;
     const int lane = threadIdx.x & 31;
     W *const oscale = reinterpret_cast<W *>(out_scales);
     pdl_wait();
     pdl_trigger();
     if ((int)blockIdx.x >= token_blocks) {
-        if (blockIdx.y) return;
         const int warp = (threadIdx.y * blockDim.x + threadIdx.x) >> 5, warps = (blockDim.x * blockDim.y) >> 5;
         const int64_t r0 = (((int64_t)blockIdx.x - token_blocks) * warps + warp) * zero_rows;
-        bool none = false;
-        if (lane < zero_rows && r0 + lane < R) {
-            const int p = rows[r0 + lane];
-            none = p < 0 || p >= T * (int64_t)k;
-        }
-        for (unsigned m = __ballot_sync(0xffffffffu, none); m; m &= m - 1) {
-            const int64_t r = r0 + __ffs(m) - 1;
-            for (int c = lane; c < n; c += 32) st16(out + r * row_bytes + c * 16, make_uint4(0, 0, 0, 0));
-            for (int c = lane; c < scale_words; c += 32) oscale[r * scale_words + c] = W{};
-        }
+        const unsigned none = rows_without_pair(rows, r0, zero_rows, R, T * (int64_t)k, lane);
+        if (none == 0) return;
+        zero_words(reinterpret_cast<uint4 *>(out), n, r0, zero_rows, none, lane);
+        zero_words(oscale, scale_words, r0, zero_rows, none, lane);
         return;
     }
-    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int part = blockIdx.x % parts;
+    const int64_t t = (int64_t)(blockIdx.x / parts) * blockDim.y + threadIdx.y;
     if (t >= T) return;
     // every lane of a warp has the same token: lane j holds pair j's row
     int64_t mine = lane < k ? inv[t * k + lane] : -1;
     if (mine >= R) mine = -1;
-    const int c0 = blockIdx.y * blockDim.x * kCopyPieces + threadIdx.x;
+    const int c0 = part * blockDim.x * kCopyPieces + threadIdx.x;
     uint4 v[kCopyPieces];
 #pragma unroll
     for (int i = 0; i < kCopyPieces; ++i)
@@ -236,8 +264,8 @@ __global__ void __launch_bounds__(256) k_dispatch(const char *x, int64_t xs, int
         for (int i = 0; i < kCopyPieces; ++i)
             if (c0 + i * (int)blockDim.x < n) st16(out + r * row_bytes + (c0 + i * (int)blockDim.x) * 16, v[i]);
     }
-    const int parts = gridDim.y * blockDim.x;      // the scales, spread over the row's blocks
-    for (int c = blockIdx.y * blockDim.x + threadIdx.x - lane; c < scale_words; c += parts) {
+    // the scales, spread over the row's blocks
+    for (int c = part * blockDim.x + threadIdx.x - lane; c < scale_words; c += parts * blockDim.x) {
         const bool on = c + lane < scale_words;
         const W s = on ? reinterpret_cast<const W *>(scales)[t * scale_words + c + lane] : W{};
         for (int j = 0; j < k; ++j) {
@@ -256,16 +284,18 @@ __global__ void __launch_bounds__(256) k_dispatch(const char *x, int64_t xs, int
 // The registers are held to what lets an SM keep its blocks (4096 x 7168, k = 8,
 // bf16: 77.1 us at 64 registers, 101 % of the measured copy bandwidth; 80.8 us
 // at 66, with a block less; the rows passed between lanes by shuffles 87.9 us).
+constexpr int pair_pieces(int kb) { return kb == 5 ? 2 : 8 / kb; }
 constexpr int kCombineThreads = 128;
-constexpr int combine_blocks(int dt, int kb) { return dt == MOE_DTYPE_F32 ? (kb == 2 ? 4 : 5) : (kb == 2 ? 6 : 8); }
+constexpr int combine_blocks(int dt, int kb) {
+    const bool wide = kb == 2 || kb == 5;      // more registers for the sums
+    return dt == MOE_DTYPE_F32 ? (wide ? 4 : 5) : (wide ? 6 : 8);
+}
 
 template <int DT, int KB, int PP>
-__global__ void __launch_bounds__(kCombineThreads, combine_blocks(DT, KB)) k_combine(const typename RowType<DT>::T *y, int T, int k, int H,
-                                                 const int32_t *__restrict__ inv, int64_t R,
-                                                 const float *__restrict__ w, const typename RowType<DT>::T *base,
-                                                 typename RowType<DT>::T *out) {
+__global__ void __launch_bounds__(kCombineThreads, combine_blocks(DT, KB))
+k_combine(const typename RowType<DT>::T *y, int T, int k, int H, const int32_t *inv, int64_t R, const float *w,
+          const typename RowType<DT>::T *base, typename RowType<DT>::T *out) {
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
     if (t >= T) return;
@@ -316,36 +346,31 @@ __global__ void __launch_bounds__(kCombineThreads, combine_blocks(DT, KB)) k_com
 // products reduced over the block; or a token a warp and eight of them a block
 // (short rows: no block barrier).  Later blocks: zeros for the rows without a
 // pair, a warp a row.
+constexpr int combine_backward_blocks(int dt) { return dt == MOE_DTYPE_F32 ? 2 : 3; }
+
 template <int DT, int KB, int PP, bool kWarp>
-__global__ void __launch_bounds__(256) k_combine_backward(const typename RowType<DT>::T *go,
+__global__ void __launch_bounds__(256, combine_backward_blocks(DT)) k_combine_backward(const typename RowType<DT>::T *go,
                                                           const typename RowType<DT>::T *y, int T, int k, int kb, int H,
-                                                          const int32_t *__restrict__ rows,
-                                                          const int32_t *__restrict__ inv, int64_t R,
-                                                          const float *__restrict__ w,
-                                                          typename RowType<DT>::T *gy, float *__restrict__ gw,
-                                                          int token_blocks, int zero_rows) {
+                                                          const int32_t *rows,
+                                                          const int32_t *inv, int64_t R,
+                                                          const float *w,
+                                                          typename RowType<DT>::T *gy, float *gw,
+                                                          int token_blocks, int parts, int zero_rows) {
     __shared__ float red[8][KB];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     pdl_wait();
     pdl_trigger();
     if ((int)blockIdx.x >= token_blocks) {
-        if (blockIdx.y) return;
         const int64_t r0 = (((int64_t)blockIdx.x - token_blocks) * warps + warp) * zero_rows;
-        bool none = false;
-        if (lane < zero_rows && r0 + lane < R) {
-            const int p = rows[r0 + lane];
-            none = p < 0 || p >= T * (int64_t)k;
-        }
-        for (unsigned m = __ballot_sync(0xffffffffu, none); m; m &= m - 1) {
-            const int64_t r = r0 + __ffs(m) - 1;
-            for (int c = lane * kChunk; c < H; c += 32 * kChunk) store8<DT>(gy + r * H + c, Raw8<DT>{});
-        }
+        const unsigned none = rows_without_pair(rows, r0, zero_rows, R, T * (int64_t)k, lane);
+        if (none) zero_words(reinterpret_cast<uint4 *>(gy), H * (int)sizeof(*gy) / 16, r0, zero_rows, none, lane);
         return;
     }
-    const int64_t t = kWarp ? (int64_t)blockIdx.x * 8 + warp : blockIdx.x;
+    const int part = blockIdx.x % parts;
+    const int64_t t = kWarp ? (int64_t)(blockIdx.x / parts) * 8 + warp : blockIdx.x / parts;
     if (kWarp && t >= T) return;
     const int tid = kWarp ? lane : threadIdx.x, dc = (kWarp ? 32 : blockDim.x) * kChunk;
-    const int j0 = blockIdx.y * kb;
+    const int j0 = part * kb;
     int row[KB];
     float wj[KB], dot[KB];
 #pragma unroll
@@ -406,9 +431,15 @@ __global__ void __launch_bounds__(256) k_combine_backward(const typename RowType
     }
 }
 
-// Pairs a thread loads together, of k: 8, 4 or 2; few tokens have too few
-// threads for more than one piece each.
-int pair_batch(int k, bool few) { return few || k > 4 ? 8 : k > 2 ? 4 : 2; }
+// Pairs a thread loads together, of k: 8, 5 (two pieces: 5, 9 and 10 pairs), 4 or
+// 2; few tokens have too few threads for more than one piece each.
+// (fp32 has no registers for two pieces of five: 287 us against 236 us at 4096 x
+// 4096, k = 10, backward.)
+int pair_batch(int k, bool few, int dtype) {
+    if (few) return 8;
+    if (k <= 4) return k <= 2 ? 2 : 4;
+    return dtype != MOE_DTYPE_F32 && (k == 5 || k == 9 || k == 10) ? 5 : 8;
+}
 int even_batch(int k, int most) { const int n = (k + most - 1) / most; return (k + n - 1) / n; }
 constexpr int kFewTokens = 2 * 152;
 // Up to here the backward pass takes a block a pair (4096 wide, k = 8, bf16: 4
@@ -419,7 +450,7 @@ template <int DT, int KB>
 cudaError_t launch_combine_k(const void *y, int T, int k, int H, const int32_t *inv, int64_t R, const float *w,
                              const void *base, void *out, cudaStream_t st) {
     using E = typename RowType<DT>::T;
-    constexpr int PP = 8 / KB;
+    constexpr int PP = pair_pieces(KB);
     const int n = (H / kChunk + PP - 1) / PP;                       // threads that a row can use
     const int tx = std::min(kCombineThreads, (n + 31) / 32 * 32), ty = kCombineThreads / tx;
     return launch_pdl(k_combine<DT, KB, PP>, dim3((T + ty - 1) / ty, (n + tx - 1) / tx), dim3(tx, ty), 0, st,
@@ -430,9 +461,10 @@ cudaError_t launch_combine_k(const void *y, int T, int k, int H, const int32_t *
 template <int DT>
 cudaError_t launch_combine(const void *y, int T, int k, int H, const int32_t *inv, int64_t R, const float *w,
                            const void *base, void *out, cudaStream_t st) {
-    switch (pair_batch(k, T <= kFewTokens)) {
+    switch (pair_batch(k, T <= kFewTokens, DT)) {
         case 2: return launch_combine_k<DT, 2>(y, T, k, H, inv, R, w, base, out, st);
         case 4: return launch_combine_k<DT, 4>(y, T, k, H, inv, R, w, base, out, st);
+        case 5: return launch_combine_k<DT, DT == MOE_DTYPE_F32 ? 8 : 5>(y, T, k, H, inv, R, w, base, out, st);
         default: return launch_combine_k<DT, 8>(y, T, k, H, inv, R, w, base, out, st);
     }
 }
@@ -442,33 +474,37 @@ cudaError_t launch_combine_backward_k(const void *go, const void *y, int T, int 
                                       const int32_t *inv, int64_t R, const float *w, void *gy, float *gw,
                                       cudaStream_t st) {
     using E = typename RowType<DT>::T;
-    constexpr int PP = 8 / KB;
-    const bool few = T <= kFewBackward, warp = !few && H / kChunk <= 128;
+    constexpr int PP = pair_pieces(KB);
+    const bool few = T <= kFewBackward, warp = !few && H / kChunk <= 32 * (KB > 4 ? 4 : 8);
     const int kb = few ? 1 : even_batch(k, KB);
     const int pieces = (H / kChunk + PP - 1) / PP;                  // threads that a row can use
-    const int threads = warp ? 256 : std::min(256, (pieces + 31) / 32 * 32);
-    const int token_blocks = warp ? (T + 7) / 8 : T;
+    const int threads = warp ? 256 : std::max(few ? 128 : 32, std::min(256, (pieces + 31) / 32 * 32));
+    const int parts = (k + kb - 1) / kb;
+    const int64_t token_blocks = (int64_t)(warp ? (T + 7) / 8 : T) * parts;
     const int zero_rows = zero_rows_a_warp(H * (int)sizeof(E) / 16), block_rows = threads / 32 * zero_rows;
-    const dim3 grid((unsigned)(token_blocks + (R + block_rows - 1) / block_rows), (k + kb - 1) / kb);
+    const int64_t blocks = token_blocks + (R + block_rows - 1) / block_rows;
+    if (blocks > kMaxRows) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)blocks);
     auto kernel = warp ? k_combine_backward<DT, KB, PP, true> : k_combine_backward<DT, KB, PP, false>;
     return launch_pdl(kernel, grid, dim3(threads), 0, st, static_cast<const E *>(go), static_cast<const E *>(y), T, k,
-                      kb, H, rows, inv, R, w, static_cast<E *>(gy), gw, token_blocks, zero_rows);
+                      kb, H, rows, inv, R, w, static_cast<E *>(gy), gw, (int)token_blocks, parts, zero_rows);
 }
 
 template <int DT>
 cudaError_t launch_combine_backward(const void *go, const void *y, int T, int k, int H, const int32_t *rows,
                                     const int32_t *inv, int64_t R, const float *w, void *gy, float *gw,
                                     cudaStream_t st) {
-    switch (T <= kFewBackward ? 2 : pair_batch(k, false)) {
+    switch (T <= kFewBackward ? 2 : pair_batch(k, false, DT)) {
         case 2: return launch_combine_backward_k<DT, 2>(go, y, T, k, H, rows, inv, R, w, gy, gw, st);
         case 4: return launch_combine_backward_k<DT, 4>(go, y, T, k, H, rows, inv, R, w, gy, gw, st);
+        case 5: return launch_combine_backward_k<DT, DT == MOE_DTYPE_F32 ? 8 : 5>(go, y, T, k, H, rows, inv, R, w, gy, gw, st);
         default: return launch_combine_backward_k<DT, 8>(go, y, T, k, H, rows, inv, R, w, gy, gw, st);
     }
 }
 
 // ----------------------------------------------------------------- checks
 
-constexpr int64_t kMaxRows = 0x7fffffff;
+
 
 moe_status check_pairs(int32_t T, int32_t k, int64_t rows) {
     if (T < 0 || rows < 0) return MOE_ERR_INVALID_ARG;
@@ -478,7 +514,7 @@ moe_status check_pairs(int32_t T, int32_t k, int64_t rows) {
 
 moe_status check_values(int32_t dtype, int32_t H) {
     if (!known_dtype(dtype)) return MOE_ERR_INVALID_ARG;
-    if (H < kChunk || H % kChunk) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (H < kChunk || H > kMaxCombineH || H % kChunk) return MOE_ERR_UNSUPPORTED_SHAPE;
     return MOE_OK;
 }
 
@@ -549,16 +585,17 @@ moe_status moe_dispatch(const void *x, int64_t x_stride_bytes, int64_t row_bytes
     const int n = (int)(row_bytes / 16);
     const int tx = std::min(256, ((n + kCopyPieces - 1) / kCopyPieces + 31) / 32 * 32), ty = 256 / tx;
     const int parts = (n + tx * kCopyPieces - 1) / (tx * kCopyPieces);
-    const int token_blocks = (T + ty - 1) / ty, zero_rows = zero_rows_a_warp(n);
-    const int block_rows = tx * ty / 32 * zero_rows;
-    const dim3 grid((unsigned)(token_blocks + (rows + block_rows - 1) / block_rows), parts);
-    if (parts > 65535) return MOE_ERR_UNSUPPORTED_SHAPE;
+    const int64_t token_blocks = (int64_t)((T + ty - 1) / ty) * parts;
+    const int zero_rows = zero_rows_a_warp(n), block_rows = tx * ty / 32 * zero_rows;
+    const int64_t blocks = token_blocks + (rows + block_rows - 1) / block_rows;
+    if (blocks > kMaxRows) return MOE_ERR_UNSUPPORTED_SHAPE;
+    const dim3 grid((unsigned)blocks);
     auto launch = [&](auto kernel, int word) {
         return cuda_status(launch_pdl(kernel, grid, dim3(tx, ty), 0, static_cast<cudaStream_t>(stream),
                                       static_cast<const char *>(x), x_stride_bytes, n,
                                       static_cast<const char *>(scales), (int)(scale_bytes / word), (int)T, (int)k,
                                       sorted_rows, pair_rows, rows, static_cast<char *>(out),
-                                      static_cast<char *>(out_scales), token_blocks, zero_rows));
+                                      static_cast<char *>(out_scales), (int)token_blocks, parts, zero_rows));
     };
     // scale rows are copied in words as wide as their length and addresses allow
     auto wide = [&](int a) { return scale_bytes % a == 0 && aligned_to(scales, a) && aligned_to(out_scales, a); };
