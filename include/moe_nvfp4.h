@@ -334,9 +334,9 @@ typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2 } moe_dt
  *   E4M3_128: groups of 128 consecutive values, fp32 scales [T][ceil(H/128)].
  *   E4M3_ROW: one group a row, fp32 scales [T].
  *             For both: a = max(amax of |n| in the group, 2^-100), scale =
- *             a / 448, code = E4M3_rne_sat(n * 448 / a), computed from the
- *             products p = s * weight as p * (448 / amax |p|), which must stay
- *             in fp32's range.  A NaN makes its group NaN.
+ *             a / 448, code = E4M3_rne_sat(n * 448 / a), where n * 448 / a is
+ *             (s * weight) * (448 / amax |s * weight|).  A NaN makes its group
+ *             NaN.
  *   MXFP8:    groups of 32, E8M0 scales uint8[T][ceil(H/32)]: byte =
  *             clamp(floor(log2(amax)) - 8 + 127, 0, 254) (0 for an all-zero
  *             group), code = E4M3_rne_sat(n * 2^(127 - byte)); a group whose
@@ -348,10 +348,11 @@ typedef enum {
 
 /* Residual addition and root-mean-square norm of T rows of H values:
  *   s = round(x + residual)  (s = x without a residual),
- *   rstd = 1 / sqrt(mean(s^2) + eps),  n = (s * rstd) * weight  in fp32,
+ *   rstd = 1 / sqrt(mean(s^2) + eps),  n = (s * weight) * rstd  in fp32,
  *   y = round(n), and/or n in 8 bits (moe_quant8).
  * The statistic is that of the stored (rounded) sum, summed in fp32: a row
- * whose sum of squares leaves fp32's range has rstd 0.
+ * whose sum of squares leaves fp32's range has rstd 0; s * weight has to stay
+ * in that range too.
  *   x        [T] rows of H, x_stride elements apart
  *   residual NULL, or [T] rows of H, residual_stride elements apart
  *   weight   [H], in `dtype` as x, residual, sum and y are

@@ -94,25 +94,12 @@ __device__ __forceinline__ float row_rstd(float sumsq, int H, float eps) {
     return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sumsq, (float)H), eps)));
 }
 
-// n = (s * rstd) * weight of one piece, fp32.
-template <int DT> __device__ __forceinline__ void norm8(const Raw8<DT> &s, const Raw8<DT> &w, float rstd, float (&n)[8]) {
+// p = s * weight of one piece, in fp32 (exact for 16-bit rows), from f = s.
+template <int DT> __device__ __forceinline__ void product8(float (&f)[8], const Raw8<DT> &w) {
     float g[8];
-    widen8<DT>(s, n);
     widen8<DT>(w, g);
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-        mul2(n, e, rstd, rstd);
-        mul2(n, e, g[e], g[e + 1]);
-    }
-}
-
-// p = s * weight of one piece, exact for 16-bit rows.
-template <int DT> __device__ __forceinline__ void product8(const Raw8<DT> &s, const Raw8<DT> &w, float (&p)[8]) {
-    float g[8];
-    widen8<DT>(s, p);
-    widen8<DT>(w, g);
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) mul2(p, e, g[e], g[e + 1]);
+    for (int e = 0; e < 8; e += 2) mul2(f, e, g[e], g[e + 1]);
 }
 
 // A group's factor to its codes' scale, of its products p: with top = amax p *
@@ -121,6 +108,8 @@ template <int DT> __device__ __forceinline__ void product8(const Raw8<DT> &s, co
 __device__ __forceinline__ float e4m3_factor(float amax_p, float top, float rstd) {
     return top > kMinAmax ? __fdiv_rn(448.0f, amax_p) : __fmul_rn(rstd, 448.0f / kMinAmax);
 }
+
+__device__ __forceinline__ float e4m3_scale(float top) { return __fdiv_rn(max_nan(top, kMinAmax), 448.0f); }
 
 __device__ __forceinline__ float amax8(const float (&n)[8], float m) {
 #pragma unroll
@@ -145,13 +134,12 @@ template <int DT> __device__ __forceinline__ Raw8<DT> add8(const Raw8<DT> &x, co
     return s;
 }
 
-// A row a block, or (rows of up to 512 values) a row a warp and eight of them a
-// block: no block barrier, and short rows fill an SM.  Thread i of a
-// row's n (a multiple of 32) holds pieces i, i + n, ..., so a warp's accesses
-// are 512 consecutive bytes of a 16-bit row, a 128-value group is 16
-// neighbouring lanes and a 32-value group is four.  All of a thread's loads are
-// issued before the first use; the row stays in its stored type (half the
-// registers of fp32, so more blocks an SM).
+// A row a block, or (short rows) a row a warp and eight of them a
+// block: no block barrier, and short rows fill an SM.  Thread i of a row's n (a
+// multiple of 32) holds pieces i, i + n, ..., so a warp's accesses are 512
+// consecutive bytes of a 16-bit row, a 128-value group is 16 neighbouring lanes
+// and a 32-value group is four.  All of a thread's loads are issued before the
+// first use; what it holds over the reduction is the products p = s * weight.
 template <int DT, int Q, int V, bool kWarp>
 __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_norm(const NormArgs a, int64_t rows) {
     using T = typename RowType<DT>::T;
@@ -172,7 +160,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
             if (a.r) u[i] = load8<DT>(static_cast<const T *>(a.r) + t * a.rs + c * kChunk);
         }
     }
-    float s0 = 0.0f, s1 = 0.0f;
+    float p[V][8], s0 = 0.0f, s1 = 0.0f, row_mul = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = tid + i * n;
@@ -181,69 +169,63 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
             s[i] = add8<DT>(s[i], u[i]);
             if (a.sum && c < n8) store8<DT>(static_cast<T *>(a.sum) + t * a.H + c * kChunk, s[i]);
         }
-        float f[8];
-        widen8<DT>(s[i], f);
+        widen8<DT>(s[i], p[i]);
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) fma2(s0, s1, f[e], f[e + 1], f[e], f[e + 1]);
+        for (int e = 0; e < 8; e += 2) fma2(s0, s1, p[i][e], p[i][e + 1], p[i][e], p[i][e + 1]);
+        product8<DT>(p[i], w[i]);
+        if constexpr (Q == MOE_QUANT_E4M3_ROW) row_mul = amax8(p[i], row_mul);
     }
-    float sum = s0 + s1, row_mul = 0.0f;
-    if constexpr (Q == MOE_QUANT_E4M3_ROW) {   // the row's largest product, on the same barrier
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float f[8];
-            product8<DT>(s[i], w[i], f);
-            row_mul = amax8(f, row_mul);
-        }
-        row_sum_max<kWarp>(sum, row_mul, red);
-    } else {
-        sum = row_sum<kWarp>(sum, red[0]);
-    }
+    float sum = s0 + s1;
+    if constexpr (Q == MOE_QUANT_E4M3_ROW) row_sum_max<kWarp>(sum, row_mul, red);
+    else sum = row_sum<kWarp>(sum, red[0]);
     const float rstd = row_rstd(sum, a.H, a.eps);
     if (a.rstd && tid == 0) a.rstd[t] = rstd;
     if constexpr (Q == MOE_QUANT_E4M3_ROW) {
         const float top = __fmul_rn(row_mul, rstd);
         row_mul = e4m3_factor(row_mul, top, rstd);
-        if (tid == 0) static_cast<float *>(a.scales)[t] = __fdiv_rn(max_nan(top, kMinAmax), 448.0f);
+        if (tid == 0) static_cast<float *>(a.scales)[t] = e4m3_scale(top);
     }
+    constexpr int kLanes = Q == MOE_QUANT_MXFP8 ? 4 : 16;      // of a group
+    const int64_t group0 = t * ((n8 + kLanes - 1) / kLanes);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = tid + i * n;
-        float f[8];
-        if (a.y) {
-            norm8<DT>(s[i], w[i], rstd, f);
+        if (Q == MOE_QUANT_NONE || a.y) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = p[i][e];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) mul2(f, e, rstd, rstd);
             if (c < n8) store8<DT>(static_cast<T *>(a.y) + t * a.H + c * kChunk, narrow8<DT>(f));
         }
         if constexpr (Q == MOE_QUANT_NONE) continue;
-        product8<DT>(s[i], w[i], f);
         float mul = row_mul;
         if constexpr (Q != MOE_QUANT_E4M3_ROW) {
-            constexpr int kLanes = Q == MOE_QUANT_MXFP8 ? 4 : 16;
             if constexpr (Q == MOE_QUANT_MXFP8) {
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) mul2(f, e, rstd, rstd);
+                for (int e = 0; e < 8; e += 2) mul2(p[i], e, rstd, rstd);
             }
-            float m = amax8(f, 0.0f);
+            float m = amax8(p[i], 0.0f);
 #pragma unroll
             for (int o = kLanes / 2; o >= 1; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
             const bool first = c < n8 && (c % kLanes) == 0;
-            const int64_t at = t * ((n8 + kLanes - 1) / kLanes) + c / kLanes;
             if constexpr (Q == MOE_QUANT_E4M3_128) {
                 const float top = __fmul_rn(m, rstd);
                 mul = e4m3_factor(m, top, rstd);
-                if (first) static_cast<float *>(a.scales)[at] = __fdiv_rn(max_nan(top, kMinAmax), 448.0f);
+                if (first) static_cast<float *>(a.scales)[group0 + c / kLanes] = e4m3_scale(top);
             } else {
                 // floor(log2(amax)) + 127 is the exponent field of a normal amax;
                 // E4M3's largest exponent is 8
                 const int field = (int)((__float_as_uint(m) >> 23) & 0xFFu);
                 const int byte = field == 255 ? 255 : max(field - 8, 0);
                 mul = field == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(254 - byte) << 23);
-                if (first) static_cast<uint8_t *>(a.scales)[at] = (uint8_t)byte;
+                if (first) static_cast<uint8_t *>(a.scales)[group0 + c / kLanes] = (uint8_t)byte;
             }
         }
         if (c < n8) {
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) mul2(f, e, mul, mul);
-            const uint2 o = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+            for (int e = 0; e < 8; e += 2) mul2(p[i], e, mul, mul);
+            const uint2 o = make_uint2(e4m3x4(p[i][0], p[i][1], p[i][2], p[i][3]), e4m3x4(p[i][4], p[i][5], p[i][6], p[i][7]));
             *reinterpret_cast<uint2 *>(a.q + t * a.H + c * kChunk) = o;
         }
     }
@@ -459,15 +441,18 @@ template <int DT, int Q, bool kWarp>
 cudaError_t launch_norm_v(const NormArgs &a, int T, int threads, int v, cudaStream_t st) {
     const dim3 grid(kWarp ? (T + kWarpRows - 1) / kWarpRows : T), block(kWarp ? 32 * kWarpRows : threads);
     if (v == 1) return launch_pdl(k_rms_norm<DT, Q, 1, kWarp>, grid, block, 0, st, a, (int64_t)T);
-    if (v == 2 || kWarp) return launch_pdl(k_rms_norm<DT, Q, 2, kWarp>, grid, block, 0, st, a, (int64_t)T);
-    return launch_pdl(k_rms_norm<DT, Q, kWarp ? 2 : 4, kWarp>, grid, block, 0, st, a, (int64_t)T);
+    if (v == 2) return launch_pdl(k_rms_norm<DT, Q, 2, kWarp>, grid, block, 0, st, a, (int64_t)T);
+    return launch_pdl(k_rms_norm<DT, Q, 4, kWarp>, grid, block, 0, st, a, (int64_t)T);
 }
 
 template <int DT, int Q> cudaError_t launch_norm_q(const NormArgs &a, int T, cudaStream_t st) {
     const int n8 = a.H / kChunk;
     const bool few = T <= 2 * kSms;
-    // 16384 rows of 512 values: 11.2 us against 17.1 us a block a row; of 1024: 21.1 against 20.7
-    if (n8 <= 64 && !few) return launch_norm_v<DT, Q, true>(a, T, 32, warp_pieces(n8), st);
+    // 16384 rows, bf16 with the residual: of 512 values 11.2 us against 17.1 us a
+    // block a row, of 624 15.3 against 17.1, of 1024 20.8 against 20.2; without
+    // it, of 1024 14.1 against 17.8.  1216 rows of 624: 3.2 against 2.7.
+    const int most = T < 2048 ? kWarpPieces / 2 : a.r ? kWarpPieces * 3 / 4 : kWarpPieces;
+    if (n8 <= most && !few) return launch_norm_v<DT, Q, true>(a, T, 32, warp_pieces(n8), st);
     const RowShape s = row_shape(n8, few);
     return launch_norm_v<DT, Q, false>(a, T, s.threads, s.v, st);
 }
