@@ -22,6 +22,9 @@ constexpr int kMaxCombineH = 65536;
 constexpr int kMaxAlign = 256;
 constexpr int kSortMaxWarps = 32;
 constexpr int kSortIds = 8;           // ids a lane has in flight
+// Pairs a block of the cluster takes before there is another, up to 16 blocks
+// (1024 tokens, k = 8: 4.4 us; with 1024 pairs a block 5.3 us, with 2048 6.0).
+constexpr int kSortPairs = 512, kSortBlocks = 16;
 
 // Inclusive scan over the block's threads; `red` holds 32 words.
 __device__ __forceinline__ int block_scan(int v, int *red) {
@@ -60,12 +63,14 @@ struct SortArgs {
 // run of consecutive pairs and counts them per expert in shared memory; the
 // blocks read each other's counts through distributed shared memory and scan
 // them into the segments' first rows; the pairs are then placed in order, the
-// ones of a warp that share an expert ranked by a match.  All rows are set to
-// -1 while the ids arrive; the barrier in between orders that before the
+// ones of a warp that share an expert ranked by ballots of the expert's bits (by
+// a match of the warp's ids 131072 pairs took 12.5 us, so 10.7).  All rows are
+// set to -1 while the ids arrive; the barrier in between orders that before the
 // placing.  Latency-bound: one read of the ids, one cluster barrier, one write
-// (4 tokens, k = 8, E = 128: 2.2 us in a graph; 16384 tokens, E = 256: 12.5
-// us with 16 blocks, 20.5 us with 8).  Placing through a sorted copy in shared
-// memory, for neighbouring writes, measured no gain.
+// (4 tokens, k = 8, E = 128: 2.3 us in a graph; 16384 tokens, E = 256: 10.7 us
+// with 16 blocks), of which the placing's scattered 4-byte stores are half at
+// 131072 pairs.  Placing through a sorted copy in shared memory, for
+// neighbouring writes, measured no gain.
 template <bool kCluster>
 __global__ void __launch_bounds__(1024) k_sort_pairs(const SortArgs a) {
     extern __shared__ int smem[];
@@ -90,7 +95,7 @@ __global__ void __launch_bounds__(1024) k_sort_pairs(const SortArgs a) {
         for (int i = 0; i < kSortIds; ++i) {
             const int64_t p = p0 + 32 * i + lane;
             id[i] = p < end ? a.ids[p] : -1;
-            if (id[i] >= E) id[i] = -1;
+            if (id[i] < 0 || id[i] >= E) id[i] = -1;
         }
     };
     load(beg);
@@ -115,11 +120,15 @@ __global__ void __launch_bounds__(1024) k_sort_pairs(const SortArgs a) {
     if constexpr (kCluster) {
         cg::this_cluster().sync();
         if (tid < E) {
+            int c[kSortBlocks];
+#pragma unroll
+            for (int b = 0; b < kSortBlocks; ++b)
+                c[b] = b < nb ? cg::this_cluster().map_shared_rank(tot, b)[tid] : 0;
             count = 0;
-            for (int b = 0; b < nb; ++b) {
-                const int c = cg::this_cluster().map_shared_rank(tot, b)[tid];
-                count += c;
-                if (b < rank) before += c;
+#pragma unroll
+            for (int b = 0; b < kSortBlocks; ++b) {
+                count += c[b];
+                if (b < rank) before += c[b];
             }
         }
         cg::this_cluster().barrier_arrive();           // this block has read the others' counts
@@ -134,6 +143,7 @@ __global__ void __launch_bounds__(1024) k_sort_pairs(const SortArgs a) {
         }
     }
     __syncthreads();
+    const int bits = 33 - __clz((E - 1) | 1);   // of an expert, and one that -1 has and no expert
     for (int64_t p0 = beg; p0 < end; p0 += 32 * kSortIds) {
         if (end - beg > 32 * kSortIds) load(p0);
 #pragma unroll
@@ -141,7 +151,13 @@ __global__ void __launch_bounds__(1024) k_sort_pairs(const SortArgs a) {
             const int64_t p = p0 + 32 * i + lane;
             if (p0 + 32 * i >= end) break;
             const int e = id[i];
-            const unsigned peers = __match_any_sync(0xffffffffu, e);
+            // the lanes with the same expert, bit by bit
+            unsigned peers = 0xffffffffu;
+            for (int b = 0; b < bits; ++b) {
+                const bool on = e >> b & 1;
+                const unsigned with = __ballot_sync(0xffffffffu, on);
+                peers &= on ? with : ~with;
+            }
             int row = -1;
             if (e >= 0) row = first[e] + mine[e] + __popc(peers & ((1u << lane) - 1u));
             __syncwarp();
@@ -154,10 +170,6 @@ __global__ void __launch_bounds__(1024) k_sort_pairs(const SortArgs a) {
     }
     if constexpr (kCluster) cg::this_cluster().barrier_wait();   // the others have read this block's counts
 }
-
-// Pairs a block of the cluster takes before there is another, up to 16 blocks
-// (1024 tokens, k = 8: 4.4 us; with 1024 pairs a block 5.3 us, with 2048 6.0).
-constexpr int kSortPairs = 512, kSortBlocks = 16;
 
 size_t sort_smem(int warps, int E) { return sizeof(int) * ((size_t)warps + 2) * E; }
 
