@@ -351,8 +351,8 @@ typedef enum {
  *   rstd = 1 / sqrt(mean(s^2) + eps),  n = (s * weight) * rstd  in fp32,
  *   y = round(n), and/or n in 8 bits (moe_quant8).
  * The statistic is that of the stored (rounded) sum, summed in fp32: a row
- * whose sum of squares leaves fp32's range has rstd 0; s * weight has to stay
- * in that range too.
+ * whose sum of squares leaves fp32's range has rstd 0.  s * weight is held in
+ * fp32 as well: what of it leaves that range, or its normal numbers, is lost.
  *   x        [T] rows of H, x_stride elements apart
  *   residual NULL, or [T] rows of H, residual_stride elements apart
  *   weight   [H], in `dtype` as x, residual, sum and y are

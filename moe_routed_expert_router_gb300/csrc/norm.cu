@@ -102,13 +102,18 @@ template <int DT> __device__ __forceinline__ void product8(float (&f)[8], const 
     for (int e = 0; e < 8; e += 2) mul2(f, e, g[e], g[e + 1]);
 }
 
-// A group's factor to its codes' scale, of its products p: with top = amax p *
-// rstd and a = max(top, 2^-100) a code is that of p * rstd * 448 / a, which is
-// p * (448 / amax p) but for the bound.
-__device__ __forceinline__ float e4m3_factor(float amax_p, float top, float rstd) {
-    return top > kMinAmax ? __fdiv_rn(448.0f, amax_p) : __fmul_rn(rstd, 448.0f / kMinAmax);
+// A group's scale, and the factor that takes its products to its codes: with top
+// = amax p * rstd and a = max(top, 2^-100) a code is that of p * rstd * 448 / a,
+// which is p * (448 / amax p) but for groups at the bound (or with a NaN), whose
+// products are taken times rstd first: rstd * 448 / 2^-100 may leave fp32.
+__device__ __forceinline__ float e4m3_factor(float amax_p, float top) {
+    return __fdiv_rn(448.0f, top > kMinAmax ? amax_p : kMinAmax);
 }
-
+__device__ __forceinline__ void at_the_bound(float (&p)[8], float top, float rstd) {
+    if (top > kMinAmax) return;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) mul2(p, e, rstd, rstd);
+}
 __device__ __forceinline__ float e4m3_scale(float top) { return __fdiv_rn(max_nan(top, kMinAmax), 448.0f); }
 
 __device__ __forceinline__ float amax8(const float (&n)[8], float m) {
@@ -160,7 +165,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
             if (a.r) u[i] = load8<DT>(static_cast<const T *>(a.r) + t * a.rs + c * kChunk);
         }
     }
-    float p[V][8], s0 = 0.0f, s1 = 0.0f, row_mul = 0.0f;
+    float p[V][8], s0 = 0.0f, s1 = 0.0f, row_mul = 0.0f, row_top = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = tid + i * n;
@@ -181,9 +186,9 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
     const float rstd = row_rstd(sum, a.H, a.eps);
     if (a.rstd && tid == 0) a.rstd[t] = rstd;
     if constexpr (Q == MOE_QUANT_E4M3_ROW) {
-        const float top = __fmul_rn(row_mul, rstd);
-        row_mul = e4m3_factor(row_mul, top, rstd);
-        if (tid == 0) static_cast<float *>(a.scales)[t] = e4m3_scale(top);
+        row_top = __fmul_rn(row_mul, rstd);
+        row_mul = e4m3_factor(row_mul, row_top);
+        if (tid == 0) static_cast<float *>(a.scales)[t] = e4m3_scale(row_top);
     }
     constexpr int kLanes = Q == MOE_QUANT_MXFP8 ? 4 : 16;      // of a group
     const int64_t group0 = t * ((n8 + kLanes - 1) / kLanes);
@@ -200,7 +205,9 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
         }
         if constexpr (Q == MOE_QUANT_NONE) continue;
         float mul = row_mul;
-        if constexpr (Q != MOE_QUANT_E4M3_ROW) {
+        if constexpr (Q == MOE_QUANT_E4M3_ROW) {
+            at_the_bound(p[i], row_top, rstd);
+        } else {
             if constexpr (Q == MOE_QUANT_MXFP8) {
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) mul2(p[i], e, rstd, rstd);
@@ -211,7 +218,8 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
             const bool first = c < n8 && (c % kLanes) == 0;
             if constexpr (Q == MOE_QUANT_E4M3_128) {
                 const float top = __fmul_rn(m, rstd);
-                mul = e4m3_factor(m, top, rstd);
+                mul = e4m3_factor(m, top);
+                at_the_bound(p[i], top, rstd);
                 if (first) static_cast<float *>(a.scales)[group0 + c / kLanes] = e4m3_scale(top);
             } else {
                 // floor(log2(amax)) + 127 is the exponent field of a normal amax;

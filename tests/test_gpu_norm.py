@@ -136,6 +136,29 @@ def test_norm_rows_that_are_not_finite_stay_alone(quant):
         assert bad["scales"][1].isnan().all()
 
 
+@pytest.mark.parametrize("eps", [1e-6, 1e-12, 1e-20, 1e-40])
+@pytest.mark.parametrize("quant", [moe.QUANT_E4M3_128, moe.QUANT_E4M3_ROW, moe.QUANT_MXFP8])
+def test_norm_8_bit_output_of_groups_next_to_nothing(quant, eps):
+    """Zero rows, zero groups and groups below the scale's bound of 2^-100, whatever rstd is."""
+    H = 512
+    g = torch.Generator(device="cuda").manual_seed(31)
+    x = torch.randn(5, H, generator=g, device="cuda") * 2.0 ** -40
+    x[0] = 0
+    x[1, :256] = 0
+    x[2, 128:] *= 2.0 ** -60
+    x[3] *= 2.0 ** -50
+    w = torch.ones(H, device="cuda")
+    w[256:384] = 2.0 ** -20
+    out = moe.rms_norm(x, w, eps=eps, quant=quant)
+    s = x.double()
+    # eps as the kernel gets it: rounded to fp32
+    n = s / torch.sqrt((s * s).mean(1, keepdim=True) + float(np.float32(eps))) * w.double()
+    # squares below 2^-126 lose bits: up to half of 2^-149 each, against a sum of at least H * eps
+    rel = N_REL + 2.0 ** -150 / float(np.float32(eps))
+    _check_quant(n.cpu().numpy(), out["q"], out["scales"], quant, rel)
+    assert (out["q"][0].float() == 0).all() and out["scales"].float().isfinite().all()
+
+
 def test_norm_of_values_whose_squares_leave_fp32():
     w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
     out = moe.rms_norm(torch.full((1, 64), 1e25, dtype=torch.bfloat16, device="cuda"), w)
