@@ -192,6 +192,28 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
     }
     constexpr int kLanes = Q == MOE_QUANT_MXFP8 ? 4 : 16;      // of a group
     const int64_t group0 = t * ((n8 + kLanes - 1) / kLanes);
+    auto group_max = [&](float m) {
+#pragma unroll
+        for (int o = kLanes / 2; o >= 1; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        return m;
+    };
+    // E4M3_128: lane i of a group's 16 does the divisions of its piece i, all
+    // pieces' at once
+    float top[V], factor = row_mul;
+    if constexpr (Q == MOE_QUANT_E4M3_128) {
+        const int mine = threadIdx.x & 15;
+        float m = 0.0f, own = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            top[i] = group_max(amax8(p[i], 0.0f));
+            if (mine == i) m = top[i];
+            top[i] = __fmul_rn(top[i], rstd);
+            if (mine == i) own = top[i];
+        }
+        factor = e4m3_factor(m, own);
+        const int c = (tid & ~15) + mine * n;
+        if (mine < V && c < n8) static_cast<float *>(a.scales)[group0 + c / 16] = e4m3_scale(own);
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = tid + i * n;
@@ -204,31 +226,21 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
             if (c < n8) store8<DT>(static_cast<T *>(a.y) + t * a.H + c * kChunk, narrow8<DT>(f));
         }
         if constexpr (Q == MOE_QUANT_NONE) continue;
-        float mul = row_mul;
-        if constexpr (Q == MOE_QUANT_E4M3_ROW) {
-            at_the_bound(p[i], row_top, rstd);
-        } else {
-            if constexpr (Q == MOE_QUANT_MXFP8) {
+        float mul = factor;
+        if constexpr (Q == MOE_QUANT_E4M3_ROW) at_the_bound(p[i], row_top, rstd);
+        if constexpr (Q == MOE_QUANT_E4M3_128) {
+            mul = __shfl_sync(0xffffffffu, factor, (threadIdx.x & 16) + i);
+            at_the_bound(p[i], top[i], rstd);
+        }
+        if constexpr (Q == MOE_QUANT_MXFP8) {
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) mul2(p[i], e, rstd, rstd);
-            }
-            float m = amax8(p[i], 0.0f);
-#pragma unroll
-            for (int o = kLanes / 2; o >= 1; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const bool first = c < n8 && (c % kLanes) == 0;
-            if constexpr (Q == MOE_QUANT_E4M3_128) {
-                const float top = __fmul_rn(m, rstd);
-                mul = e4m3_factor(m, top);
-                at_the_bound(p[i], top, rstd);
-                if (first) static_cast<float *>(a.scales)[group0 + c / kLanes] = e4m3_scale(top);
-            } else {
-                // floor(log2(amax)) + 127 is the exponent field of a normal amax;
-                // E4M3's largest exponent is 8
-                const int field = (int)((__float_as_uint(m) >> 23) & 0xFFu);
-                const int byte = field == 255 ? 255 : max(field - 8, 0);
-                mul = field == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(254 - byte) << 23);
-                if (first) static_cast<uint8_t *>(a.scales)[group0 + c / kLanes] = (uint8_t)byte;
-            }
+            for (int e = 0; e < 8; e += 2) mul2(p[i], e, rstd, rstd);
+            // floor(log2(amax)) + 127 is the exponent field of a normal amax;
+            // E4M3's largest exponent is 8
+            const int field = (int)((__float_as_uint(group_max(amax8(p[i], 0.0f))) >> 23) & 0xFFu);
+            const int byte = field == 255 ? 255 : max(field - 8, 0);
+            mul = field == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(254 - byte) << 23);
+            if (c < n8 && c % kLanes == 0) static_cast<uint8_t *>(a.scales)[group0 + c / kLanes] = (uint8_t)byte;
         }
         if (c < n8) {
 #pragma unroll
