@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(256) k_dispatch(const char *x, int64_t xs, int
 // Bound by HBM: every pair's row read once, every token's written once.  A
 // thread has up to eight 16-byte loads in flight: KB pairs' rows of PP pieces
 // (KB x PP = 8), so that a token of two pairs asks for as much as one of eight
-// (16384 tokens of 4096, k = 2, bf16: 61 us against 99 us with one piece).
+// (16384 tokens of 4096, k = 2, bf16: 59 us against 99 us with one piece).
 // The registers are held to what lets an SM keep its blocks (4096 x 7168, k = 8,
 // bf16: 77.1 us at 64 registers, 101 % of the measured copy bandwidth; 80.8 us
 // at 66, with a block less; the rows passed between lanes by shuffles 87.9 us).
@@ -353,21 +353,19 @@ k_combine(const typename RowType<DT>::T *y, int T, int k, int H, const int32_t *
     }
 }
 
-// Blocks (token, batch of kb pairs): the token's gradient row is read once a
-// batch, every pair's row of y read and of grad_y written once, the dot
-// products reduced over the block; or a token a warp and eight of them a block
-// (short rows: no block barrier).  Later blocks: zeros for the rows without a
-// pair, a warp a row.
+// Bound by HBM (8192 x 4096, k = 8, bf16, padded to 128 rows: 195 us, 97 % of
+// the measured copy bandwidth).  Blocks (token, batch of kb pairs): the token's
+// gradient row is read once a batch, every pair's row of y read and of grad_y
+// written once, the dot products reduced over the block; or a token a warp and
+// eight of them a block (short rows, no block barrier: 16384 x 256, k = 8 24.7 us
+// against 105 us).  Later blocks write zeros to the rows without a pair.
 constexpr int combine_backward_blocks(int dt) { return dt == MOE_DTYPE_F32 ? 2 : 3; }
 
 template <int DT, int KB, int PP, bool kWarp>
-__global__ void __launch_bounds__(256, combine_backward_blocks(DT)) k_combine_backward(const typename RowType<DT>::T *go,
-                                                          const typename RowType<DT>::T *y, int T, int k, int kb, int H,
-                                                          const int32_t *rows,
-                                                          const int32_t *inv, int64_t R,
-                                                          const float *w,
-                                                          typename RowType<DT>::T *gy, float *gw,
-                                                          int token_blocks, int parts, int zero_rows) {
+__global__ void __launch_bounds__(256, combine_backward_blocks(DT))
+k_combine_backward(const typename RowType<DT>::T *go, const typename RowType<DT>::T *y, int T, int k, int kb, int H,
+                   const int32_t *rows, const int32_t *inv, int64_t R, const float *w, typename RowType<DT>::T *gy,
+                   float *gw, int token_blocks, int parts, int zero_rows) {
     __shared__ float red[8][KB];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     pdl_wait();
@@ -443,10 +441,10 @@ __global__ void __launch_bounds__(256, combine_backward_blocks(DT)) k_combine_ba
     }
 }
 
-// Pairs a thread loads together, of k: 8, 5 (two pieces: 5, 9 and 10 pairs), 4 or
-// 2; few tokens have too few threads for more than one piece each.
-// (fp32 has no registers for two pieces of five: 287 us against 236 us at 4096 x
-// 4096, k = 10, backward.)
+// Pairs a thread loads together, of k: 8, 5 (two pieces: 5, 9 and 10 pairs; 4096 x
+// 8192, k = 10, bf16: 109 us against 113 with 8 and 2), 4 or 2; few tokens have
+// too few threads for more than one piece each, and fp32 has no registers for
+// two pieces of five (4096 x 4096, k = 10, backward: 287 us against 239).
 int pair_batch(int k, bool few, int dtype) {
     if (few) return 8;
     if (k <= 4) return k <= 2 ? 2 : 4;

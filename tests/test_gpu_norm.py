@@ -67,7 +67,11 @@ def _check_quant(n, q, scales, quant, rel):
         assert ((c == lo) | (c == hi)).all()
 
 
-SHAPES = [(1, 8), (1, 256), (3, 136), (5, 1840), (2, 2056), (4, 4096), (7, 7168), (3, 16384), (300, 520)]
+# few rows; then rows enough for the kernels' other splits: a warp a row, one, two and four pieces a thread
+SHAPES = [(1, 8), (1, 256), (3, 136), (5, 1840), (2, 2056), (4, 4096), (7, 7168), (3, 16384), (300, 520),
+          (310, 8), (310, 136), (2050, 264), (310, 520), (2050, 776), (2049, 1000), (333, 1032), (320, 4104), (310, 16384)]
+# several rows a block in the backward pass, in each of its splits
+LONG = [(5000, 264), (5001, 1000), (2500, 1024), (1300, 2056), (650, 4104), (640, 7176), (620, 16384)]
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
@@ -165,8 +169,9 @@ def test_norm_of_values_whose_squares_leave_fp32():
     assert out["rstd"].item() == 0 and (out["y"] == 0).all()
 
 
-def test_norm_strided_rows_and_in_place():
-    dt, T, H = torch.bfloat16, 9, 712
+@pytest.mark.parametrize("T,H", [(9, 712), (2100, 712), (400, 2064)])
+def test_norm_strided_rows_and_in_place(T, H):
+    dt = torch.bfloat16
     x, r, w = _inputs(T, H, dt, 3)
     want = moe.rms_norm(x, w, residual=r)
     wide = torch.full((T, 3 * H), float("nan"), dtype=dt, device="cuda")
@@ -203,7 +208,7 @@ def _grads(T, H, dt, seed, with_sum):
 
 @pytest.mark.parametrize("with_sum", [False, True])
 @pytest.mark.parametrize("dtype", list(DTYPES))
-@pytest.mark.parametrize("T,H", SHAPES + [(1000, 256)])
+@pytest.mark.parametrize("T,H", SHAPES + [(1000, 256)] + LONG)
 def test_norm_backward_against_64_bits(T, H, dtype, with_sum):
     dt = DTYPES[dtype]
     s, gy, gs, w = _grads(T, H, dt, T + H, with_sum)
@@ -246,14 +251,15 @@ def test_norm_backward_against_differences():
 
 
 def test_norm_backward_in_place():
-    s, gy, gs, w = _grads(400, 1024, torch.bfloat16, 1, True)
-    rstd = moe.rms_norm(s, w)["rstd"]
-    want = moe.rms_norm_backward(gy, s, w, rstd, grad_sum=gs)
-    for at in ("gy", "gs"):
-        a, b = gy.clone(), gs.clone()
-        out = dict(grad_sum=a if at == "gy" else b, grad_w=torch.empty(1024, device="cuda"))
-        moe.rms_norm_backward(a, s, w, rstd, grad_sum=b, out=out)
-        assert torch.equal(out["grad_sum"], want["grad_sum"]) and torch.equal(out["grad_w"], want["grad_w"])
+    for T, H in ((400, 1024), (700, 2048), (1300, 4096)):
+        s, gy, gs, w = _grads(T, H, torch.bfloat16, 1, True)
+        rstd = moe.rms_norm(s, w)["rstd"]
+        want = moe.rms_norm_backward(gy, s, w, rstd, grad_sum=gs)
+        for at in ("gy", "gs"):
+            a, b = gy.clone(), gs.clone()
+            out = dict(grad_sum=a if at == "gy" else b, grad_w=torch.empty(H, device="cuda"))
+            moe.rms_norm_backward(a, s, w, rstd, grad_sum=b, out=out)
+            assert torch.equal(out["grad_sum"], want["grad_sum"]) and torch.equal(out["grad_w"], want["grad_w"])
 
 
 def test_norm_on_another_stream_and_in_a_graph():

@@ -74,7 +74,7 @@ def _check_sort(ids, E, align):
 @pytest.mark.parametrize("T,k,E,drop,kind", [
     (1, 1, 1, 0, "zipf"), (1, 8, 128, 0, "zipf"), (4, 8, 128, 0, "zipf"), (5, 3, 7, 0.4, "zipf"),
     (33, 1, 2, 0, "zipf"), (129, 10, 500, 0.1, "zipf"), (257, 8, 256, 0, "zipf"), (64, 32, 64, 0, "zipf"),
-    (1000, 8, 1024, 0.05, "zipf"), (4093, 7, 255, 0.05, "zipf"), (16384, 8, 256, 0, "zipf"),
+    (1000, 8, 1024, 0.05, "zipf"), (4093, 7, 255, 0.05, "zipf"), (16384, 8, 256, 0, "zipf"), (20001, 7, 64, 0.05, "zipf"),
     (300, 2, 5, 0, "one"), (4096, 8, 33, 0, "one"), (50, 4, 16, 0, "none"), (5000, 3, 16, 0, "none")])
 def test_sort_is_exact(T, k, E, drop, kind, align):
     _check_sort(_ids(T, k, E, T + E, drop, kind), E, align)
@@ -107,6 +107,9 @@ def test_sort_agrees_with_the_router(name):
 
 CASES = [(1, 1, 4, 1, 0.0), (4, 8, 128, 1, 0.0), (37, 3, 9, 16, 0.3), (130, 10, 40, 128, 0.0), (515, 11, 17, 8, 0.2),
          (90, 32, 64, 1, 0.5)]
+# tokens enough for the splits by pairs: two, four, five and eight at a time, and what is left of them
+MANY = [(400, k, 24, 8, drop) for k, drop in ((1, 0.0), (2, 0.1), (3, 0.0), (4, 0.3), (5, 0.1), (7, 0.0), (9, 0.1), (10, 0.0),
+                                               (16, 0.1), (20, 0.0))]
 
 
 def _order(T, k, E, align, drop, seed=0):
@@ -157,7 +160,7 @@ def _rows_in(order, H, dt, seed):
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("H", [8, 136, 1840, 4096])
-@pytest.mark.parametrize("T,k,E,align,drop", CASES)
+@pytest.mark.parametrize("T,k,E,align,drop", CASES + MANY)
 def test_combine_against_64_bits(T, k, E, align, drop, H, dtype):
     dt = DTYPES[dtype]
     order = _order(T, k, E, align, drop)
@@ -183,7 +186,7 @@ def test_combine_against_64_bits(T, k, E, align, drop, H, dtype):
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("H", [8, 136, 1840, 4096])
-@pytest.mark.parametrize("T,k,E,align,drop", CASES)
+@pytest.mark.parametrize("T,k,E,align,drop", CASES + MANY)
 def test_combine_backward_against_64_bits(T, k, E, align, drop, H, dtype):
     dt = DTYPES[dtype]
     order = _order(T, k, E, align, drop)
