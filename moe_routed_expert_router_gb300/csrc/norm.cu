@@ -3,9 +3,9 @@
 //
 // A block takes a row and keeps it in registers over the reduction, so every
 // input is read once and every output written once.  Bound by HBM (4096 x 7168
-// bf16 with residual and E4M3_128 output 33.3 us, 92 % of the measured copy
+// bf16 with residual and E4M3_128 output 32.9 us, 93 % of the measured copy
 // bandwidth; without the residual, three bytes a value, by instructions: 8192 x
-// 7168 40.6 us, 64 %).  What keeps it there is that the loads of the next row do
+// 7168 36 us, 72 %).  What keeps it there is that the loads of the next row do
 // not wait for the reduction of the present one: other blocks' in the forward
 // pass, a ring in shared memory in the backward pass.  (A ring in the forward
 // pass too: 33.7 against 34.3 us at 4096 x 7168, 20.8 against 20.1 at 4096 x 4096.)
@@ -31,7 +31,7 @@ struct NormArgs {
     const void *x, *r, *w;
     int64_t xs, rs;
     int H;
-    float eps;
+    float inv_h, eps;
     void *sum, *y;
     uint8_t *q;
     void *scales;
@@ -50,6 +50,15 @@ __device__ __forceinline__ float amax3(float a, float b, float c) {
     return r;
 }
 
+// Sum of the warps' sums (at most 16), on every lane of either half of a warp.
+__device__ __forceinline__ float half_sum(const float *red) {
+    const int i = threadIdx.x & 15;
+    float v = i < (int)(blockDim.x >> 5) ? red[i] : 0.0f;
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
 // Sum over the threads of a row (a warp, or the block), the same on every
 // thread; `red` holds 32 words, and two calls in a row use different ones.
 template <bool kWarp> __device__ __forceinline__ float row_sum(float v, float *red) {
@@ -57,8 +66,7 @@ template <bool kWarp> __device__ __forceinline__ float row_sum(float v, float *r
     if constexpr (kWarp) return v;
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
-    return warp_sum(lane < nw ? red[lane] : 0.0f);
+    return half_sum(red);
 }
 
 // The sum of one value and the maximum of another, with one barrier.
@@ -71,14 +79,16 @@ template <bool kWarp> __device__ __forceinline__ void row_sum_max(float &sum, fl
     sum = warp_sum(sum);
     top = warp_max_nan(top);
     if constexpr (kWarp) return;
-    const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) {
+    if ((threadIdx.x & 31) == 0) {
         red[0][threadIdx.x >> 5] = sum;
         red[1][threadIdx.x >> 5] = top;
     }
     __syncthreads();
-    sum = warp_sum(lane < nw ? red[0][lane] : 0.0f);
-    top = warp_max_nan(lane < nw ? red[1][lane] : 0.0f);
+    sum = half_sum(red[0]);
+    const int i = threadIdx.x & 15;
+    top = i < (int)(blockDim.x >> 5) ? red[1][i] : 0.0f;
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
 }
 
 // Four fp32 -> four E4M3 bytes, round to nearest even, saturating; NaN -> 0x7F.
@@ -92,9 +102,9 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return out;
 }
 
-// 1 / sqrt(mean + eps): the IEEE square root and division, once a row.
-__device__ __forceinline__ float row_rstd(float sumsq, int H, float eps) {
-    return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sumsq, (float)H), eps)));
+// 1 / sqrt(mean + eps).
+__device__ __forceinline__ float row_rstd(float sumsq, float inv_h, float eps) {
+    return __frsqrt_rn(fmaf(sumsq, inv_h, eps));
 }
 
 // p = s * weight of one piece, in fp32 (exact for 16-bit rows), from f = s.
@@ -155,6 +165,10 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
     const int tid = kWarp ? threadIdx.x & 31 : threadIdx.x;
     const int n8 = a.H / kChunk, n = kWarp ? 32 : blockDim.x;
     const int64_t t = kWarp ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+    // whether piece i is inside the row.  A block's are, but the last: n <=
+    // n8 / V + 32 and n8 >= 32 V (V - 1) in every row_shape, so (V - 1) n <= n8; so
+    // is the first half of a warp's, which has V pieces from n8 > 16 V on
+    auto inside = [&](int i) { return i < (kWarp ? V / 2 : V - 1) || tid + i * n < n8; };
     Raw8<DT> s[V], u[V], w[V];
     pdl_wait();
     pdl_trigger();
@@ -163,7 +177,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
     for (int i = 0; i < V; ++i) {
         const int c = tid + i * n;
         s[i] = u[i] = w[i] = Raw8<DT>{};
-        if (c < n8) {
+        if (inside(i)) {
             s[i] = load8<DT>(static_cast<const T *>(a.x) + t * a.xs + c * kChunk);
             if (a.r) u[i] = load8<DT>(static_cast<const T *>(a.r) + t * a.rs + c * kChunk);
         }
@@ -172,10 +186,10 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = tid + i * n;
-        if (c < n8) w[i] = load8_shared<DT>(static_cast<const T *>(a.w) + c * kChunk);
+        if (inside(i)) w[i] = load8_shared<DT>(static_cast<const T *>(a.w) + c * kChunk);
         if (a.r) {
             s[i] = add8<DT>(s[i], u[i]);
-            if (a.sum && c < n8) store8<DT>(static_cast<T *>(a.sum) + t * a.H + c * kChunk, s[i]);
+            if (a.sum && inside(i)) store8<DT>(static_cast<T *>(a.sum) + t * a.H + c * kChunk, s[i]);
         }
         widen8<DT>(s[i], p[i]);
 #pragma unroll
@@ -186,7 +200,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
     float sum = s0 + s1;
     if constexpr (Q == MOE_QUANT_E4M3_ROW) row_sum_max<kWarp>(sum, row_mul, red);
     else sum = row_sum<kWarp>(sum, red[0]);
-    const float rstd = row_rstd(sum, a.H, a.eps);
+    const float rstd = row_rstd(sum, a.inv_h, a.eps);
     if (a.rstd && tid == 0) a.rstd[t] = rstd;
     if constexpr (Q == MOE_QUANT_E4M3_ROW) {
         row_top = __fmul_rn(row_mul, rstd);
@@ -226,7 +240,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
             for (int e = 0; e < 8; ++e) f[e] = p[i][e];
 #pragma unroll
             for (int e = 0; e < 8; e += 2) mul2(f, e, rstd, rstd);
-            if (c < n8) store8<DT>(static_cast<T *>(a.y) + t * a.H + c * kChunk, narrow8<DT>(f));
+            if (inside(i)) store8<DT>(static_cast<T *>(a.y) + t * a.H + c * kChunk, narrow8<DT>(f));
         }
         if constexpr (Q == MOE_QUANT_NONE) continue;
         float mul = factor;
@@ -245,7 +259,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
             mul = field == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(254 - byte) << 23);
             if (c < n8 && c % kLanes == 0) static_cast<uint8_t *>(a.scales)[group0 + c / kLanes] = (uint8_t)byte;
         }
-        if (c < n8) {
+        if (inside(i)) {
 #pragma unroll
             for (int e = 0; e < 8; e += 2) mul2(p[i], e, mul, mul);
             const uint2 o = make_uint2(e4m3x4(p[i][0], p[i][1], p[i][2], p[i][3]), e4m3x4(p[i][4], p[i][5], p[i][6], p[i][7]));
@@ -430,13 +444,14 @@ __global__ void __launch_bounds__(256) k_rms_norm_grad_w(const float *part, int 
 }
 
 // Threads and pieces a thread for a row of n8 pieces.  Few rows: as many threads
-// as there are, for the latency.  Many rows: 96 to 256 threads with two pieces
-// or more (bf16, 16384 rows forward with the residual and 8-bit output: H = 2048
-// 36.7 us against 39.5 us with one piece and 256 threads; H = 4096 71.0 us
-// against 80.0 us with 512 threads).
+// as there are, for the latency.  Many rows: 96 to 256 threads with two pieces,
+// and four above `two` pieces a row.  Forward 384 (bf16, 8 bits out, 8192 rows of
+// 4096 without residual 20.1 us against 23.8 with two pieces, with residual 4096
+// rows 20.1 against 19.7; 2048 wide, one piece and 256 threads 39.5 us against
+// 36.7 at 16384 rows), backward 512 (four pieces need the registers).
 struct RowShape { int threads, v; };
-RowShape row_shape(int n8, bool few) {
-    const int v = few ? (n8 <= 512 ? 1 : n8 <= 1024 ? 2 : 4) : (n8 <= 128 ? 1 : n8 <= 512 ? 2 : 4);
+RowShape row_shape(int n8, bool few, int two) {
+    const int v = few ? (n8 <= 512 ? 1 : n8 <= 1024 ? 2 : 4) : (n8 <= 128 ? 1 : n8 <= two ? 2 : 4);
     return {((n8 + v - 1) / v + 31) / 32 * 32, v};
 }
 
@@ -478,7 +493,7 @@ template <int DT, int Q> cudaError_t launch_norm_q(const NormArgs &a, int T, cud
     // has the bits of the norm that stored it).  1216 rows of 624: 3.2 against 2.7.
     const int most = T < 2048 ? kWarpPieces / 2 : kWarpPieces;
     if (n8 <= most && !few) return launch_norm_v<DT, Q, true>(a, T, 32, warp_pieces(n8), st);
-    const RowShape s = row_shape(n8, few);
+    const RowShape s = row_shape(n8, few, 384);
     return launch_norm_v<DT, Q, false>(a, T, s.threads, s.v, st);
 }
 
@@ -501,7 +516,7 @@ GradShape grad_shape(int T, int H, int dtype) {
     const int n8 = H / kChunk;
     GradShape g;
     g.warp = n8 <= (dtype == MOE_DTYPE_F32 ? kWarpPieces / 2 : kWarpPieces);   // a warp's ring of fp32 rows is twice as large
-    g.row = g.warp ? RowShape{32, warp_pieces(n8)} : row_shape(n8, false);
+    g.row = g.warp ? RowShape{32, warp_pieces(n8)} : row_shape(n8, false, 512);
     const int an_sm = std::max(2, std::min(4, 512 / (g.warp ? 32 * kWarpRows : g.row.threads)));
     const int groups = g.warp ? (T - 1) / kWarpRows + 1 : T;          // rows, or eights of them
     g.blocks = std::min(groups, an_sm * kSms);
@@ -567,7 +582,8 @@ moe_status moe_rms_norm(const void *x, int64_t x_stride, const void *residual, i
         !aligned_to(y, 16) || !aligned_to(q, 16) || !aligned_to(scales, quant == MOE_QUANT_MXFP8 ? 1 : 4) ||
         !aligned_to(rstd, 4))
         return MOE_ERR_MISALIGNED;
-    const NormArgs a{x, residual, weight, x_stride, residual_stride, H, eps, sum, y, q, scales, rstd};
+    const NormArgs a{x, residual, weight, x_stride, residual_stride, H, 1.0f / (float)H, eps, sum, y, q, scales,
+                     rstd};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (dtype) {
         case MOE_DTYPE_F32: return cuda_status(launch_norm<MOE_DTYPE_F32>(a, quant, T, s));
