@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(256) k_rms_norm_grad_w(const float *part, int 
 
 // Threads and pieces a thread for a row of n8 pieces.  Few rows: as many threads
 // as there are, for the latency.  Many rows: 96 to 256 threads with two pieces,
-// and four above `two` pieces a row.  Forward 384 (bf16, 8 bits out, 8192 rows of
+// and four above `two` pieces a row.  Forward 400 (bf16, 8 bits out, 8192 rows of
 // 4096 without residual 20.1 us against 23.8 with two pieces, with residual 4096
 // rows 20.1 against 19.7; 2048 wide, one piece and 256 threads 39.5 us against
 // 36.7 at 16384 rows), backward 512 (four pieces need the registers).
@@ -493,7 +493,7 @@ template <int DT, int Q> cudaError_t launch_norm_q(const NormArgs &a, int T, cud
     // has the bits of the norm that stored it).  1216 rows of 624: 3.2 against 2.7.
     const int most = T < 2048 ? kWarpPieces / 2 : kWarpPieces;
     if (n8 <= most && !few) return launch_norm_v<DT, Q, true>(a, T, 32, warp_pieces(n8), st);
-    const RowShape s = row_shape(n8, few, 384);
+    const RowShape s = row_shape(n8, few, 400);
     return launch_norm_v<DT, Q, false>(a, T, s.threads, s.v, st);
 }
 
