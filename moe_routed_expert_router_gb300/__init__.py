@@ -217,17 +217,17 @@ def _device(t, where):
     return dev
 
 
-def _want(t, where, name, shape, dtype, dev):
+def _want(t, where, name, shape, dtype, index):
     """The tensor is where and what the kernel takes it to be; returns its address."""
-    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
-        _refuse(where, f"{name} {t.dtype}{list(t.shape)} on {t.device}; contiguous {dtype}{list(shape)} on {dev} expected")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _refuse(where, f"{name} {t.dtype}{list(t.shape)} on {t.device}; contiguous {dtype}{list(shape)} on cuda:{index} expected")
     return t.data_ptr()
 
 
-def _want_rows(t, where, name, shape, dtype, dev):
+def _want_rows(t, where, name, shape, dtype, index):
     """The same of rows of contiguous values a stride apart; returns their address and stride in values."""
-    if t.dtype is not dtype or t.shape != shape or t.device != dev or not (t.is_contiguous() or t.stride(1) == 1):
-        _refuse(where, f"{name} {t.dtype}{list(t.shape)} on {t.device}; rows of contiguous {dtype}{list(shape)} on {dev} expected")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not (t.is_contiguous() or t.stride(1) == 1):
+        _refuse(where, f"{name} {t.dtype}{list(t.shape)} on {t.device}; rows of contiguous {dtype}{list(shape)} on cuda:{index} expected")
     return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
 
 
@@ -239,8 +239,8 @@ def _new(shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _on(dev, stream):
-    return _raw_stream(dev.index) if stream is None else stream.cuda_stream
+def _on(index, stream):
+    return _raw_stream(index) if stream is None else stream.cuda_stream
 
 
 def rms_norm(x, weight, residual=None, eps=1e-6, quant=QUANT_NONE, out=None, stream=None):
@@ -256,9 +256,10 @@ def rms_norm(x, weight, residual=None, eps=1e-6, quant=QUANT_NONE, out=None, str
         _refuse(where, "x is not [T][H]")
     T, H = shape
     dev, dt, code = _device(x, where), x.dtype, _dtype(x, where)
-    xp, xs = _want_rows(x, where, "x", shape, dt, dev)
-    wp = _want(weight, where, "weight", (H,), dt, dev)
-    rp, rs = (None, 0) if residual is None else _want_rows(residual, where, "residual", shape, dt, dev)
+    index = dev.index
+    xp, xs = _want_rows(x, where, "x", shape, dt, index)
+    wp = _want(weight, where, "weight", (H,), dt, index)
+    rp, rs = (None, 0) if residual is None else _want_rows(residual, where, "residual", shape, dt, index)
     sc_shape, sc_dtype = None, _F32
     if quant != QUANT_NONE:
         if quant not in (QUANT_E4M3_128, QUANT_E4M3_ROW, QUANT_MXFP8):
@@ -275,21 +276,20 @@ def rms_norm(x, weight, residual=None, eps=1e-6, quant=QUANT_NONE, out=None, str
         else:
             out["q"] = _new(shape, torch.float8_e4m3fn, dev, stream)
             out["scales"] = _new(sc_shape, sc_dtype, dev, stream)
-    sp = yp = qp = cp = dp = None
-    for name, t in out.items():
-        if name == "sum":
-            sp = _want(t, where, name, shape, dt, dev)
-        elif name == "y":
-            yp = _want(t, where, name, shape, dt, dev)
-        elif name == "rstd":
-            dp = _want(t, where, name, (T,), _F32, dev)
-        elif name == "q" and sc_shape is not None:
-            qp = _want(t, where, name, shape, torch.float8_e4m3fn, dev)
-        elif name == "scales" and sc_shape is not None:
-            cp = _want(t, where, name, sc_shape, sc_dtype, dev)
-        else:
-            _refuse(where, f"no output {name!r}")
-    st = lib().moe_rms_norm(xp, xs, rp, rs, wp, T, H, code, eps, quant, sp, yp, qp, cp, dp, _on(dev, stream))
+    get = out.get
+    t_sum, t_y, t_rstd, t_q, t_scales = get("sum"), get("y"), get("rstd"), get("q"), get("scales")
+    if (t_sum is not None) + (t_y is not None) + (t_rstd is not None) + (t_q is not None) + (t_scales is not None) != len(out):
+        _refuse(where, f"outputs {sorted(out)}; sum, y, rstd, q and scales are known")
+    sp = None if t_sum is None else _want(t_sum, where, "sum", shape, dt, index)
+    yp = None if t_y is None else _want(t_y, where, "y", shape, dt, index)
+    dp = None if t_rstd is None else _want(t_rstd, where, "rstd", (T,), _F32, index)
+    qp = cp = None
+    if t_q is not None or t_scales is not None:
+        if sc_shape is None or t_q is None or t_scales is None:
+            _refuse(where, "q and scales go together, and with a quant")
+        qp = _want(t_q, where, "q", shape, torch.float8_e4m3fn, index)
+        cp = _want(t_scales, where, "scales", sc_shape, sc_dtype, index)
+    st = lib().moe_rms_norm(xp, xs, rp, rs, wp, T, H, code, eps, quant, sp, yp, qp, cp, dp, _on(index, stream))
     if st:
         raise MoeError(st, where)
     return out
@@ -306,19 +306,20 @@ def rms_norm_backward(grad_y, sum, weight, rstd, grad_sum=None, out=None, stream
         _refuse(where, "sum is not [T][H]")
     T, H = shape
     dev, dt, code = _device(sum, where), sum.dtype, _dtype(sum, where)
-    sp = _want(sum, where, "sum", shape, dt, dev)
-    yp = _want(grad_y, where, "grad_y", shape, dt, dev)
-    wp = _want(weight, where, "weight", (H,), dt, dev)
-    dp = _want(rstd, where, "rstd", (T,), _F32, dev)
-    gp = None if grad_sum is None else _want(grad_sum, where, "grad_sum", shape, dt, dev)
+    index = dev.index
+    sp = _want(sum, where, "sum", shape, dt, index)
+    yp = _want(grad_y, where, "grad_y", shape, dt, index)
+    wp = _want(weight, where, "weight", (H,), dt, index)
+    dp = _want(rstd, where, "rstd", (T,), _F32, index)
+    gp = None if grad_sum is None else _want(grad_sum, where, "grad_sum", shape, dt, index)
     if out is None:
         out = {"grad_sum": _new(shape, dt, dev, stream), "grad_w": _new((H,), _F32, dev, stream)}
-    op = _want(out["grad_sum"], where, "out grad_sum", shape, dt, dev)
-    ow = _want(out["grad_w"], where, "out grad_w", (H,), _F32, dev)
+    op = _want(out["grad_sum"], where, "out grad_sum", shape, dt, index)
+    ow = _want(out["grad_w"], where, "out grad_w", (H,), _F32, index)
     L = lib()
     n = L.moe_rms_norm_backward_workspace(T, H)
     ws = _new((n,), torch.uint8, dev, stream)
-    st = L.moe_rms_norm_backward(yp, sp, wp, dp, gp, T, H, code, op, ow, ws.data_ptr(), n, _on(dev, stream))
+    st = L.moe_rms_norm_backward(yp, sp, wp, dp, gp, T, H, code, op, ow, ws.data_ptr(), n, _on(index, stream))
     if st:
         raise MoeError(st, where)
     return out
@@ -343,27 +344,28 @@ def sort_pairs(topk_ids, num_experts, align=1, out=None, stream=None):
         _refuse(where, "topk_ids is not [T][k]")
     T, k = shape
     dev = _device(topk_ids, where)
-    ip = _want(topk_ids, where, "topk_ids", shape, _I32, dev)
+    index = dev.index
+    ip = _want(topk_ids, where, "topk_ids", shape, _I32, index)
     R = sorted_rows(T * k, num_experts, align)
     if out is None:
         out = {"expert_offsets": _new((num_experts + 1,), _I32, dev, stream), "sorted_rows": _new((R,), _I32, dev, stream),
                "pair_rows": _new(shape, _I32, dev, stream)}
-    op = _want(out["expert_offsets"], where, "out expert_offsets", (num_experts + 1,), _I32, dev)
-    rp = _want(out["sorted_rows"], where, "out sorted_rows", (R,), _I32, dev)
-    pp = _want(out["pair_rows"], where, "out pair_rows", shape, _I32, dev)
-    st = lib().moe_sort_pairs(ip, T, k, num_experts, align, R, op, rp, pp, _on(dev, stream))
+    op = _want(out["expert_offsets"], where, "out expert_offsets", (num_experts + 1,), _I32, index)
+    rp = _want(out["sorted_rows"], where, "out sorted_rows", (R,), _I32, index)
+    pp = _want(out["pair_rows"], where, "out pair_rows", shape, _I32, index)
+    st = lib().moe_sort_pairs(ip, T, k, num_experts, align, R, op, rp, pp, _on(index, stream))
     if st:
         raise MoeError(st, where)
     return out
 
 
-def _order(order, where, dev):
+def _order(order, where, index):
     """sort_pairs' result: the addresses of sorted_rows and pair_rows, the number of rows, T and k."""
     rows, inv = order["sorted_rows"], order["pair_rows"]
     if rows.dim() != 1 or inv.dim() != 2:
         _refuse(where, "order is not sort_pairs' result")
     R, (T, k) = rows.shape[0], inv.shape
-    return _want(rows, where, "sorted_rows", (R,), _I32, dev), _want(inv, where, "pair_rows", (T, k), _I32, dev), R, T, k
+    return _want(rows, where, "sorted_rows", (R,), _I32, index), _want(inv, where, "pair_rows", (T, k), _I32, index), R, T, k
 
 
 def dispatch(x, order, scales=None, out=None, stream=None):
@@ -372,25 +374,26 @@ def dispatch(x, order, scales=None, out=None, stream=None):
     Returns {"rows": [rows][H]} and, with scales [T][n], {"scales": [rows][n]}."""
     where = "moe_dispatch"
     dev = _device(x, where)
-    rp, pp, R, T, k = _order(order, where, dev)
+    index = dev.index
+    rp, pp, R, T, k = _order(order, where, index)
     if x.dim() != 2:
         _refuse(where, "x is not [T][H]")
     H, dt, es = x.shape[1], x.dtype, x.element_size()
-    xp, xs = _want_rows(x, where, "x", (T, H), dt, dev)
+    xp, xs = _want_rows(x, where, "x", (T, H), dt, index)
     cp, cn, sb = None, 0, 0
     if scales is not None:
         if scales.dim() != 2:
             _refuse(where, "scales is not [T][n]")
         cn = scales.shape[1]
-        cp, sb = _want(scales, where, "scales", (T, cn), scales.dtype, dev), cn * scales.element_size()
+        cp, sb = _want(scales, where, "scales", (T, cn), scales.dtype, index), cn * scales.element_size()
     if out is None:
         out = {"rows": _new((R, H), dt, dev, stream)}
         if scales is not None:
             out["scales"] = _new((R, cn), scales.dtype, dev, stream)
-    op, oc = _want(out["rows"], where, "out rows", (R, H), dt, dev), None
+    op, oc = _want(out["rows"], where, "out rows", (R, H), dt, index), None
     if scales is not None:
-        oc = _want(out["scales"], where, "out scales", (R, cn), scales.dtype, dev)
-    st = lib().moe_dispatch(xp, xs * es, H * es, cp, sb, T, k, rp, pp, R, op, oc, _on(dev, stream))
+        oc = _want(out["scales"], where, "out scales", (R, cn), scales.dtype, index)
+    st = lib().moe_dispatch(xp, xs * es, H * es, cp, sb, T, k, rp, pp, R, op, oc, _on(index, stream))
     if st:
         raise MoeError(st, where)
     return out
@@ -402,17 +405,18 @@ def combine(y, order, weights=None, base=None, out=None, stream=None):
     weights [T][k] fp32 (None: 1); base [T][H] is added where given.  Rows of y that hold no pair are not read."""
     where = "moe_combine"
     dev = _device(y, where)
-    rp, pp, R, T, k = _order(order, where, dev)
+    index = dev.index
+    rp, pp, R, T, k = _order(order, where, index)
     if y.dim() != 2:
         _refuse(where, "y is not [rows][H]")
     H, dt, code = y.shape[1], y.dtype, _dtype(y, where)
-    yp = _want(y, where, "y", (R, H), dt, dev)
-    wp = None if weights is None else _want(weights, where, "weights", (T, k), _F32, dev)
-    bp = None if base is None else _want(base, where, "base", (T, H), dt, dev)
+    yp = _want(y, where, "y", (R, H), dt, index)
+    wp = None if weights is None else _want(weights, where, "weights", (T, k), _F32, index)
+    bp = None if base is None else _want(base, where, "base", (T, H), dt, index)
     if out is None:
         out = _new((T, H), dt, dev, stream)
-    op = _want(out, where, "out", (T, H), dt, dev)
-    st = lib().moe_combine(yp, code, T, k, H, pp, R, wp, bp, op, _on(dev, stream))
+    op = _want(out, where, "out", (T, H), dt, index)
+    st = lib().moe_combine(yp, code, T, k, H, pp, R, wp, bp, op, _on(index, stream))
     if st:
         raise MoeError(st, where)
     return out
@@ -429,18 +433,19 @@ def combine_backward(grad_out, y, order, weights, out=None, stream=None):
     base's gradient is grad_out itself.  out["grad_y"] may be y."""
     where = "moe_combine_backward"
     dev = _device(y, where)
-    rp, pp, R, T, k = _order(order, where, dev)
+    index = dev.index
+    rp, pp, R, T, k = _order(order, where, index)
     if y.dim() != 2:
         _refuse(where, "y is not [rows][H]")
     H, dt, code = y.shape[1], y.dtype, _dtype(y, where)
-    yp = _want(y, where, "y", (R, H), dt, dev)
-    gp = _want(grad_out, where, "grad_out", (T, H), dt, dev)
-    wp = _want(weights, where, "weights", (T, k), _F32, dev)
+    yp = _want(y, where, "y", (R, H), dt, index)
+    gp = _want(grad_out, where, "grad_out", (T, H), dt, index)
+    wp = _want(weights, where, "weights", (T, k), _F32, index)
     if out is None:
         out = {"grad_y": _new((R, H), dt, dev, stream), "grad_w": _new((T, k), _F32, dev, stream)}
-    oy = _want(out["grad_y"], where, "out grad_y", (R, H), dt, dev)
-    ow = _want(out["grad_w"], where, "out grad_w", (T, k), _F32, dev)
-    st = lib().moe_combine_backward(gp, yp, code, T, k, H, rp, pp, R, wp, oy, ow, _on(dev, stream))
+    oy = _want(out["grad_y"], where, "out grad_y", (R, H), dt, index)
+    ow = _want(out["grad_w"], where, "out grad_w", (T, k), _F32, index)
+    st = lib().moe_combine_backward(gp, yp, code, T, k, H, rp, pp, R, wp, oy, ow, _on(index, stream))
     if st:
         raise MoeError(st, where)
     return out
