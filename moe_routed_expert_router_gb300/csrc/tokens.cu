@@ -67,10 +67,10 @@ struct SortArgs {
 // a match of the warp's ids 131072 pairs took 12.5 us, so 10.7).  All rows are
 // set to -1 while the ids arrive; the barrier in between orders that before the
 // placing.  Latency-bound: one read of the ids, one cluster barrier, one write
-// (4 tokens, k = 8, E = 128: 2.3 us in a graph; 16384 tokens, E = 256: 10.7 us
-// with 16 blocks), of which the placing's scattered 4-byte stores are half at
-// 131072 pairs.  Placing through a sorted copy in shared memory, for
-// neighbouring writes, measured no gain.
+// (4 tokens, k = 8, E = 128: 2.3 us in a graph; 16384 tokens, E = 256: 10.6 us
+// with 16 blocks, half of it the ranking, some 110 instructions for 32 pairs on
+// 16 SMs; the scattered stores are 0.5 us, and placing through a sorted copy in
+// shared memory, for neighbouring ones, measured no gain).
 template <bool kCluster>
 __global__ void __launch_bounds__(1024) k_sort_pairs(const SortArgs a) {
     extern __shared__ int smem[];
