@@ -322,3 +322,47 @@ def test_on_another_stream_and_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+@pytest.mark.parametrize("T,H", [(6, 512), (700, 2048)])
+def test_calls_back_to_back(T, H):
+    """Launches overlap (each starts while the one before ends): a chain of calls that nothing waits between, over
+    changing inputs and the same buffers, gives what the calls give one by one."""
+    k, E = 4, 16
+    g = torch.Generator(device="cuda").manual_seed(T)
+    xs = [torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16) for _ in range(3)]
+    ids = [torch.from_numpy(_ids(T, k, E, s, 0.1)).cuda() for s in range(3)]
+    w = (1 + 0.1 * torch.randn(H, generator=g, device="cuda")).to(torch.bfloat16)
+    p = torch.rand(T, k, generator=g, device="cuda")
+    R = moe.sorted_rows(T * k, E, 8)
+
+    def buffers():
+        i32, bf = dict(dtype=torch.int32, device="cuda"), dict(dtype=torch.bfloat16, device="cuda")
+        return dict(norm=dict(sum=torch.empty(T, H, **bf), y=torch.empty(T, H, **bf), rstd=torch.empty(T, device="cuda")),
+                    order=dict(expert_offsets=torch.empty(E + 1, **i32), sorted_rows=torch.empty(R, **i32),
+                               pair_rows=torch.empty(T, k, **i32)),
+                    rows=dict(rows=torch.empty(R, H, **bf)), out=torch.empty(T, H, **bf),
+                    back=dict(grad_y=torch.empty(R, H, **bf), grad_w=torch.empty(T, k, device="cuda")),
+                    gx=torch.empty(T, H, **bf), last=dict(grad_sum=torch.empty(T, H, **bf), grad_w=torch.empty(H, device="cuda")))
+
+    def chain(i, b, wait):
+        def step(v):
+            if wait:
+                torch.cuda.synchronize()
+            return v
+        n = step(moe.rms_norm(xs[i], w, residual=xs[(i + 1) % 3], out=b["norm"]))
+        o = step(moe.sort_pairs(ids[i], E, align=8, out=b["order"]))
+        r = step(moe.dispatch(n["y"], o, out=b["rows"]))
+        c = step(moe.combine(r["rows"], o, p, base=n["sum"], out=b["out"]))
+        back = step(moe.combine_backward(c, r["rows"], o, p, out=b["back"]))
+        gx = step(moe.dispatch_backward(back["grad_y"], o, out=b["gx"]))
+        last = step(moe.rms_norm_backward(gx, n["sum"], w, n["rstd"], grad_sum=c, out=b["last"]))
+        return [c, back["grad_w"], gx, last["grad_sum"], last["grad_w"]]
+
+    want = [[t.clone() for t in chain(i, buffers(), True)] for i in range(3)]
+    b, got = buffers(), []
+    for n in range(60):
+        got.append([t.clone() for t in chain(n % 3, b, False)])
+    torch.cuda.synchronize()
+    for n, ts in enumerate(got):
+        assert all(torch.equal(a, c) for a, c in zip(ts, want[n % 3])), n
