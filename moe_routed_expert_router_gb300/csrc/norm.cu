@@ -413,21 +413,24 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
     }
 }
 
-// grad_w[h] = sum of the blocks' partial sums: thread (i, j) adds every 32nd
-// block's from j on, four columns wide, then the 32 sums are added in order.
-// The partial sums come from L2 and the launch overlaps the end of the one
-// before, so this is latency: about 2 us behind 304 blocks of 4096 columns (a
-// thread a column and eight chains: 5 us).
-__global__ void __launch_bounds__(256) k_rms_norm_grad_w(const float *part, int blocks, int H, float *gw) {
-    __shared__ float4 s[32][8];
+// grad_w[h] = sum of the blocks' partial sums: thread (i, j) adds every 64th
+// block's from j on, four columns wide, then the 64 sums are added in order,
+// eight by eight.  The partial sums come from L2 and the launch overlaps the end
+// of the one before, so this is latency, 2 to 3 us: every thread's loads are one
+// round (1216 rows of 2048: the pass 8.5 us; 32 groups of two rounds 9.5).
+constexpr int kColumnGroups = 64;
+
+__global__ void __launch_bounds__(8 * kColumnGroups) k_rms_norm_grad_w(const float *part, int blocks, int H, float *gw) {
+    __shared__ float4 s[kColumnGroups][8];
+    __shared__ float t[8][32];
     const int i = threadIdx.x & 7, j = threadIdx.x >> 3;
     const int h = blockIdx.x * 32 + i * 4;
     pdl_wait();
     pdl_trigger();
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (h < H) {
-#pragma unroll 8
-        for (int b = j; b < blocks; b += 32) {
+#pragma unroll 5
+        for (int b = j; b < blocks; b += kColumnGroups) {
             const float4 p = *reinterpret_cast<const float4 *>(part + (int64_t)b * H + h);
             v.x += p.x;
             v.y += p.y;
@@ -437,11 +440,19 @@ __global__ void __launch_bounds__(256) k_rms_norm_grad_w(const float *part, int 
     }
     s[j][i] = v;
     __syncthreads();
-    if (threadIdx.x < 32 && blockIdx.x * 32 + threadIdx.x < H) {
-        const float *c = reinterpret_cast<const float *>(s) + threadIdx.x;
+    const float *c = reinterpret_cast<const float *>(s) + (threadIdx.x & 31);
+    const int w = threadIdx.x >> 5;
+    if (w < 8) {
         float sum = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) sum += c[k * 32];
+        for (int k = 0; k < kColumnGroups / 8; ++k) sum += c[(w * (kColumnGroups / 8) + k) * 32];
+        t[w][threadIdx.x & 31] = sum;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32 && blockIdx.x * 32 + threadIdx.x < H) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum += t[k][threadIdx.x];
         gw[blockIdx.x * 32 + threadIdx.x] = sum;
     }
 }
@@ -624,7 +635,7 @@ moe_status moe_rms_norm_backward(const void *grad_y, const void *sum, const void
         default: e = launch_norm_grad<MOE_DTYPE_F16>(a, g, s); break;
     }
     if (e != cudaSuccess) return MOE_ERR_CUDA;
-    return cuda_status(launch_pdl(k_rms_norm_grad_w, dim3((H + 31) / 32), dim3(256), 0, s, (const float *)a.part, g.blocks,
+    return cuda_status(launch_pdl(k_rms_norm_grad_w, dim3((H + 31) / 32), dim3(8 * kColumnGroups), 0, s, (const float *)a.part, g.blocks,
                                   (int)H, grad_w));
 }
 
