@@ -318,8 +318,8 @@ def rms_norm_backward(grad_y, sum, weight, rstd, grad_sum=None, out=None, stream
     ow = _want(out["grad_w"], where, "out grad_w", (H,), _F32, index)
     L = lib()
     n = L.moe_rms_norm_backward_workspace(T, H)
-    ws = _new((n,), torch.uint8, dev, stream)
-    st = L.moe_rms_norm_backward(yp, sp, wp, dp, gp, T, H, code, op, ow, ws.data_ptr(), n, _on(index, stream))
+    ws = _new((n,), torch.uint8, dev, stream) if n else None
+    st = L.moe_rms_norm_backward(yp, sp, wp, dp, gp, T, H, code, op, ow, ws.data_ptr() if n else None, n, _on(index, stream))
     if st:
         raise MoeError(st, where)
     return out

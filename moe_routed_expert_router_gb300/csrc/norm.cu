@@ -388,6 +388,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
         if constexpr (R == 2) slot ^= 1;
     }
     float *sums = kWarp ? reinterpret_cast<float *>(smem) + group * a.H : a.part + (int64_t)blockIdx.x * a.H;
+    const bool vectors = (reinterpret_cast<uintptr_t>(sums) & 15u) == 0;   // grad_w itself may be less aligned
     if constexpr (kWarp) {
         copy_wait<0>();
         __syncthreads();                              // the ring is free: the warps' sums, [8][H]
@@ -398,9 +399,15 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
         for (int h = 0; h < kWords; ++h) {
             if (col(i, h) >= a.H) continue;
 #pragma unroll
-            for (int e = 0; e < kWord; e += 4)
-                *reinterpret_cast<float4 *>(sums + col(i, h) + e) =
-                    make_float4(gw[i][h * kWord + e], gw[i][h * kWord + e + 1], gw[i][h * kWord + e + 2], gw[i][h * kWord + e + 3]);
+            for (int e = 0; e < kWord; e += 4) {
+                float *at = sums + col(i, h) + e, *v = &gw[i][h * kWord + e];
+                if (kWarp || vectors) {
+                    *reinterpret_cast<float4 *>(at) = make_float4(v[0], v[1], v[2], v[3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) at[k] = v[k];
+                }
+            }
         }
     if constexpr (kWarp) {
         __syncthreads();
@@ -524,7 +531,11 @@ template <int DT> cudaError_t launch_norm(const NormArgs &a, int quant, int T, c
 // rows of 1024, bf16: 25.7 us against 65 us a block a row), longer ones a
 // block.  Blocks an SM: 512 threads' worth, two to four (16384 rows: H = 2048
 // 46.0 us with four, 58.1 with two; H = 6144 133 us with two, 171 with three,
-// whose third waits); every block writes a row of partial sums.
+// whose third waits); every block writes a row of partial sums.  What one block
+// does in two rounds is one block's, whose sums are the result: no workspace and
+// no second launch (2 rows of 4096 3.1 us against 3.8, 4 rows would be 4.7; 16
+// rows of 512 2.8 against 3.2, 32 would be 4.4; host 7 us a call against 15).
+constexpr int kOneBlockRounds = 2;
 struct GradShape { RowShape row; bool warp; int blocks; };
 GradShape grad_shape(int T, int H, int dtype) {
     const int n8 = H / kChunk;
@@ -533,9 +544,12 @@ GradShape grad_shape(int T, int H, int dtype) {
     g.row = g.warp ? RowShape{32, warp_pieces(n8)} : row_shape(n8, false, 512);
     const int an_sm = std::max(2, std::min(4, 512 / (g.warp ? 32 * kWarpRows : g.row.threads)));
     const int groups = g.warp ? (T - 1) / kWarpRows + 1 : T;          // rows, or eights of them
-    g.blocks = std::min(groups, an_sm * kSms);
+    g.blocks = groups <= kOneBlockRounds ? 1 : std::min(groups, an_sm * kSms);
     return g;
 }
+
+// Bytes of the blocks' partial sums; one block's are the result.
+size_t grad_workspace(const GradShape &g, int H) { return g.blocks == 1 ? 0 : sizeof(float) * (size_t)g.blocks * (size_t)H; }
 
 template <int DT, int V, int R, bool kWarp>
 cudaError_t launch_norm_grad_v(const NormGradArgs &a, int blocks, int threads, size_t stage, cudaStream_t st) {
@@ -608,9 +622,7 @@ moe_status moe_rms_norm(const void *x, int64_t x_stride, const void *residual, i
 
 size_t moe_rms_norm_backward_workspace(int32_t T, int32_t H) {
     if (T <= 0 || H <= 0) return 0;
-    size_t blocks = 0;
-    for (int dtype : {MOE_DTYPE_F32, MOE_DTYPE_BF16}) blocks = std::max(blocks, (size_t)grad_shape(T, H, dtype).blocks);
-    return sizeof(float) * blocks * (size_t)H;
+    return std::max(grad_workspace(grad_shape(T, H, MOE_DTYPE_F32), H), grad_workspace(grad_shape(T, H, MOE_DTYPE_BF16), H));
 }
 
 moe_status moe_rms_norm_backward(const void *grad_y, const void *sum, const void *weight, const float *rstd,
@@ -619,22 +631,23 @@ moe_status moe_rms_norm_backward(const void *grad_y, const void *sum, const void
     moe_status st = check_rows(T, H, dtype);
     if (st != MOE_OK) return st;
     if (!grad_w) return MOE_ERR_INVALID_ARG;
-    if (T > 0 && (!grad_y || !sum || !weight || !rstd || !grad_in || !workspace)) return MOE_ERR_INVALID_ARG;
-    if (workspace_bytes < moe_rms_norm_backward_workspace(T, H)) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!grad_y || !sum || !weight || !rstd || !grad_in)) return MOE_ERR_INVALID_ARG;
+    const size_t need = moe_rms_norm_backward_workspace(T, H);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_INVALID_ARG;
     if (!aligned_to(grad_y, 16) || !aligned_to(sum, 16) || !aligned_to(weight, 16) || !aligned_to(rstd, 4) ||
         !aligned_to(grad_sum, 16) || !aligned_to(grad_in, 16) || !aligned_to(grad_w, 4) || !aligned_to(workspace, 16))
         return MOE_ERR_MISALIGNED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (T == 0) return cuda_status(cudaMemsetAsync(grad_w, 0, sizeof(float) * H, s));
     const GradShape g = grad_shape(T, H, dtype);
-    const NormGradArgs a{grad_y, sum, weight, grad_sum, rstd, T, H, grad_in, static_cast<float *>(workspace)};
+    const NormGradArgs a{grad_y, sum, weight, grad_sum, rstd, T, H, grad_in, g.blocks == 1 ? grad_w : static_cast<float *>(workspace)};
     cudaError_t e;
     switch (dtype) {
         case MOE_DTYPE_F32: e = launch_norm_grad<MOE_DTYPE_F32>(a, g, s); break;
         case MOE_DTYPE_BF16: e = launch_norm_grad<MOE_DTYPE_BF16>(a, g, s); break;
         default: e = launch_norm_grad<MOE_DTYPE_F16>(a, g, s); break;
     }
-    if (e != cudaSuccess) return MOE_ERR_CUDA;
+    if (e != cudaSuccess || g.blocks == 1) return cuda_status(e);
     return cuda_status(launch_pdl(k_rms_norm_grad_w, dim3((H + 31) / 32), dim3(8 * kColumnGroups), 0, s, (const float *)a.part, g.blocks,
                                   (int)H, grad_w));
 }

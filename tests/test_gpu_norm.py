@@ -71,7 +71,7 @@ def _check_quant(n, q, scales, quant, rel):
 SHAPES = [(1, 8), (1, 256), (3, 136), (5, 1840), (2, 2056), (4, 4096), (7, 7168), (3, 16384), (300, 520),
           (310, 8), (310, 136), (2050, 264), (310, 520), (2050, 776), (2049, 1000), (333, 1032), (320, 4104), (310, 16384)]
 # several rows a block in the backward pass, in each of its splits
-LONG = [(5000, 264), (5001, 1000), (2500, 1024), (1300, 2056), (650, 4104), (640, 7176), (620, 16384)]
+LONG = [(8, 1000), (16, 264), (17, 264), (2, 4104), (3, 4104), (5000, 264), (5001, 1000), (2500, 1024), (1300, 2056), (650, 4104), (640, 7176), (620, 16384)]
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
@@ -248,6 +248,20 @@ def test_norm_backward_against_differences():
         # fp32 gradients: 70 u of each term; the difference: h^2 of third derivatives and 2^-52 / h of the loss
         size = abs(loss(s.double(), w.double())) + terms.abs().sum().item()
         assert abs(num - terms.sum().item()) <= 70 * U * 4 * terms.abs().sum().item() + (h * h * 100 + 2.0 ** -50 / h) * size
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_norm_backward_into_part_of_a_gradient_buffer(dtype):
+    """grad_w aligned to its element only, for one row, a few and many."""
+    for T, H in ((1, 1032), (4, 4104), (8, 264), (700, 2056)):
+        s, gy, gs, w = _grads(T, H, DTYPES[dtype], T, True)
+        rstd = moe.rms_norm(s, w)["rstd"]
+        want = moe.rms_norm_backward(gy, s, w, rstd, grad_sum=gs)
+        flat = torch.full((H + 8,), 7.0, device="cuda")
+        out = dict(grad_sum=torch.empty_like(s), grad_w=flat[3:3 + H])
+        moe.rms_norm_backward(gy, s, w, rstd, grad_sum=gs, out=out)
+        assert torch.equal(out["grad_w"], want["grad_w"]) and torch.equal(out["grad_sum"], want["grad_sum"])
+        assert (flat[:3] == 7).all() and (flat[3 + H:] == 7).all()
 
 
 def test_norm_backward_in_place():

@@ -27,7 +27,7 @@ def test_norm(kw, want):
     assert norm(**kw) == want
 
 
-def norm_back(gy=A, s=A, w=A, rstd=A, gs=NULL, T=4, H=256, dt=moe.DTYPE_BF16, gi=A, gw=A, ws=A, n=1 << 30):
+def norm_back(gy=A, s=A, w=A, rstd=A, gs=NULL, T=400, H=256, dt=moe.DTYPE_BF16, gi=A, gw=A, ws=A, n=1 << 30):
     return moe.lib().moe_rms_norm_backward(gy, s, w, rstd, gs, T, H, dt, gi, gw, ws, n, None)
 
 
@@ -43,7 +43,8 @@ def test_norm_backward(kw, want):
 def test_norm_backward_workspace():
     n = moe.lib().moe_rms_norm_backward_workspace
     assert n(0, 256) == 0 and n(-1, 256) == 0
-    assert n(4, 256) > 0 and norm_back(n=n(4, 256) - 1) == INV
+    assert n(400, 256) > 0 and norm_back(n=n(400, 256) - 1) == INV
+    assert n(1, 256) == 0 and n(1, 4096) == 0           # one block's sums are the result
     assert n(1 << 20, 16384) == n(1 << 30, 16384)
 
 
