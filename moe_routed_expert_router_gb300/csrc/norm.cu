@@ -278,8 +278,8 @@ struct NormGradArgs {
 
 // Backward: block b takes rows b, b + blocks, ...; a thread keeps its columns'
 // weight gradient in registers over all of them, so the column sums cost one
-// [blocks][H] store at the end.  Bound by HBM (8192 x 4096 bf16 42.8 us of the
-// pass's 45.0, whose floor is 39.7; the rest adds up the blocks' sums).  With
+// [blocks][H] store at the end.  Bound by HBM (8192 x 4096 bf16 42 us of the
+// pass's 44.4, whose floor is 39.7; the rest adds up the blocks' sums).  With
 // R = 2 the next row is on its way into shared memory while one is worked on
 // (cp.async; a thread copies the pieces that it will use itself and overwrites
 // only what it has used, so its own copies are all that it waits for); R = 1 is
