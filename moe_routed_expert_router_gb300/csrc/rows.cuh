@@ -79,7 +79,7 @@ template <int DT> __device__ __forceinline__ void store8(typename RowType<DT>::T
 
 // Two fp32 operations in one instruction (f32x2), each rounded as the scalar
 // one is: a *= b;  c += a * b.
-__device__ __forceinline__ void mul2(float (&a)[8], int i, float b0, float b1) {
+template <int N> __device__ __forceinline__ void mul2(float (&a)[N], int i, float b0, float b1) {
     asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tmul.rn.f32x2 x, x, y;\n\t"
         "mov.b64 {%0, %1}, x;\n\t}"
         : "+f"(a[i]), "+f"(a[i + 1]) : "f"(b0), "f"(b1));
@@ -136,6 +136,28 @@ template <int DT> __device__ __forceinline__ Raw8<DT> narrow8(const float (&v)[8
         r.a = make_uint4(u[0], u[1], u[2], u[3]);
     }
     return r;
+}
+
+// A 16-byte piece of a row: eight 16-bit values or four fp32 ones, so that
+// neighbouring lanes always touch neighbouring 16 bytes.
+template <int DT> constexpr int kPieceValues = DT == MOE_DTYPE_F32 ? 4 : 8;
+
+template <int DT> __device__ __forceinline__ void widen_piece(const uint4 &r, float (&v)[kPieceValues<DT>]) {
+    if constexpr (DT == MOE_DTYPE_F32) {
+        v[0] = __uint_as_float(r.x);
+        v[1] = __uint_as_float(r.y);
+        v[2] = __uint_as_float(r.z);
+        v[3] = __uint_as_float(r.w);
+    } else {
+        widen8<DT>(Raw8<DT>{r}, v);
+    }
+}
+
+template <int DT> __device__ __forceinline__ uint4 narrow_piece(const float (&v)[kPieceValues<DT>]) {
+    if constexpr (DT == MOE_DTYPE_F32)
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    else
+        return narrow8<DT>(v).a;
 }
 
 inline bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

@@ -296,26 +296,26 @@ __global__ void __launch_bounds__(256) k_dispatch(const char *x, int64_t xs, int
 // The registers are held to what lets an SM keep its blocks (4096 x 7168, k = 8,
 // bf16: 77.1 us at 64 registers, 101 % of the measured copy bandwidth; 80.8 us
 // at 66, with a block less; the rows passed between lanes by shuffles 87.9 us).
+// A piece is 16 bytes in every type: with eight fp32 values a thread a warp's
+// access had holes (4096 x 4096, k = 10, fp32, backward: 208 us against 238).
 constexpr int pair_pieces(int kb) { return kb == 5 ? 2 : 8 / kb; }
 constexpr int kCombineThreads = 128;
-constexpr int combine_blocks(int dt, int kb) {
-    const bool wide = kb == 2 || kb == 5;      // more registers for the sums
-    return dt == MOE_DTYPE_F32 ? (wide ? 4 : 5) : (wide ? 6 : 8);
-}
+constexpr int combine_blocks(int kb) { return kb == 2 || kb == 5 ? 6 : 8; }   // two or more pieces' sums take registers
 
 template <int DT, int KB, int PP>
-__global__ void __launch_bounds__(kCombineThreads, combine_blocks(DT, KB))
+__global__ void __launch_bounds__(kCombineThreads, combine_blocks(KB))
 k_combine(const typename RowType<DT>::T *y, int T, int k, int H, const int32_t *inv, int64_t R, const float *w,
           const typename RowType<DT>::T *base, typename RowType<DT>::T *out) {
+    constexpr int N = kPieceValues<DT>;
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     pdl_wait();
     pdl_trigger();
     if (t >= T) return;
-    const int c0 = (blockIdx.y * PP * blockDim.x + threadIdx.x) * kChunk, dc = blockDim.x * kChunk;
+    const int c0 = (blockIdx.y * PP * blockDim.x + threadIdx.x) * N, dc = blockDim.x * N;
     if (c0 >= H) return;
-    float acc[PP][8] = {};
+    float acc[PP][N] = {};
     for (int j0 = 0; j0 < k; j0 += KB) {
-        Raw8<DT> v[KB][PP];
+        uint4 v[KB][PP];
         int row[KB];
 #pragma unroll
         for (int j = 0; j < KB; ++j) {
@@ -323,7 +323,7 @@ k_combine(const typename RowType<DT>::T *y, int T, int k, int H, const int32_t *
             if (row[j] >= R) row[j] = -1;
 #pragma unroll
             for (int i = 0; i < PP; ++i)
-                if (row[j] >= 0 && c0 + i * dc < H) v[j][i] = load8<DT>(y + (int64_t)row[j] * H + c0 + i * dc);
+                if (row[j] >= 0 && c0 + i * dc < H) v[j][i] = ld16(y + (int64_t)row[j] * H + c0 + i * dc);
         }
 #pragma unroll
         for (int j = 0; j < KB; ++j) {
@@ -332,10 +332,10 @@ k_combine(const typename RowType<DT>::T *y, int T, int k, int H, const int32_t *
 #pragma unroll
             for (int i = 0; i < PP; ++i) {
                 if (c0 + i * dc >= H) continue;
-                float f[8];
-                widen8<DT>(v[j][i], f);
+                float f[N];
+                widen_piece<DT>(v[j][i], f);
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) fma2(acc[i][e], acc[i][e + 1], f[e], f[e + 1], wj, wj);
+                for (int e = 0; e < N; e += 2) fma2(acc[i][e], acc[i][e + 1], f[e], f[e + 1], wj, wj);
             }
         }
     }
@@ -344,12 +344,12 @@ k_combine(const typename RowType<DT>::T *y, int T, int k, int H, const int32_t *
         const int c = c0 + i * dc;
         if (c >= H) continue;
         if (base) {
-            float f[8];
-            widen8<DT>(load8<DT>(base + t * H + c), f);
+            float f[N];
+            widen_piece<DT>(ld16(base + t * H + c), f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[i][e] += f[e];
+            for (int e = 0; e < N; ++e) acc[i][e] += f[e];
         }
-        store8<DT>(out + t * H + c, narrow8<DT>(acc[i]));
+        st16(out + t * H + c, narrow_piece<DT>(acc[i]));
     }
 }
 
@@ -359,13 +359,12 @@ k_combine(const typename RowType<DT>::T *y, int T, int k, int H, const int32_t *
 // written once, the dot products reduced over the block; or a token a warp and
 // eight of them a block (short rows, no block barrier: 16384 x 256, k = 8 24.7 us
 // against 105 us).  Later blocks write zeros to the rows without a pair.
-constexpr int combine_backward_blocks(int dt) { return dt == MOE_DTYPE_F32 ? 2 : 3; }
-
 template <int DT, int KB, int PP, bool kWarp>
-__global__ void __launch_bounds__(256, combine_backward_blocks(DT))
+__global__ void __launch_bounds__(256, 3)
 k_combine_backward(const typename RowType<DT>::T *go, const typename RowType<DT>::T *y, int T, int k, int kb, int H,
                    const int32_t *rows, const int32_t *inv, int64_t R, const float *w, typename RowType<DT>::T *gy,
                    float *gw, int token_blocks, int parts, int zero_rows) {
+    constexpr int N = kPieceValues<DT>;
     __shared__ float red[8][KB];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     pdl_wait();
@@ -379,7 +378,7 @@ k_combine_backward(const typename RowType<DT>::T *go, const typename RowType<DT>
     const int part = blockIdx.x % parts;
     const int64_t t = kWarp ? (int64_t)(blockIdx.x / parts) * 8 + warp : blockIdx.x / parts;
     if (kWarp && t >= T) return;
-    const int tid = kWarp ? lane : threadIdx.x, dc = (kWarp ? 32 : blockDim.x) * kChunk;
+    const int tid = kWarp ? lane : threadIdx.x, dc = (kWarp ? 32 : blockDim.x) * N;
     const int j0 = part * kb;
     int row[KB];
     float wj[KB], dot[KB];
@@ -391,35 +390,35 @@ k_combine_backward(const typename RowType<DT>::T *go, const typename RowType<DT>
         wj[j] = row[j] >= 0 ? w[t * k + j0 + j] : 0.0f;
         dot[j] = 0.0f;
     }
-    for (int c0 = tid * kChunk; c0 < H; c0 += PP * dc) {
-        Raw8<DT> g[PP], v[KB][PP];
+    for (int c0 = tid * N; c0 < H; c0 += PP * dc) {
+        uint4 g[PP], v[KB][PP];
 #pragma unroll
         for (int i = 0; i < PP; ++i)
-            if (c0 + i * dc < H) g[i] = load8<DT>(go + t * H + c0 + i * dc);
+            if (c0 + i * dc < H) g[i] = ld16(go + t * H + c0 + i * dc);
 #pragma unroll
         for (int j = 0; j < KB; ++j)
 #pragma unroll
             for (int i = 0; i < PP; ++i)
-                if (row[j] >= 0 && c0 + i * dc < H) v[j][i] = load8<DT>(y + (int64_t)row[j] * H + c0 + i * dc);
+                if (row[j] >= 0 && c0 + i * dc < H) v[j][i] = ld16(y + (int64_t)row[j] * H + c0 + i * dc);
 #pragma unroll
         for (int i = 0; i < PP; ++i) {
             if (c0 + i * dc >= H) continue;
-            float gf[8];
-            widen8<DT>(g[i], gf);
+            float gf[N];
+            widen_piece<DT>(g[i], gf);
 #pragma unroll
             for (int j = 0; j < KB; ++j) {
                 if (row[j] < 0) continue;
-                float f[8], d1 = 0.0f;
-                widen8<DT>(v[j][i], f);
+                float f[N], d1 = 0.0f;
+                widen_piece<DT>(v[j][i], f);
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
+                for (int e = 0; e < N; e += 2) {
                     fma2(dot[j], d1, f[e], f[e + 1], gf[e], gf[e + 1]);
                     f[e] = gf[e];
                     f[e + 1] = gf[e + 1];
                     mul2(f, e, wj[j], wj[j]);
                 }
                 dot[j] += d1;
-                store8<DT>(gy + (int64_t)row[j] * H + c0 + i * dc, narrow8<DT>(f));
+                st16(gy + (int64_t)row[j] * H + c0 + i * dc, narrow_piece<DT>(f));
             }
         }
     }
@@ -443,12 +442,11 @@ k_combine_backward(const typename RowType<DT>::T *go, const typename RowType<DT>
 
 // Pairs a thread loads together, of k: 8, 5 (two pieces: 5, 9 and 10 pairs; 4096 x
 // 8192, k = 10, bf16: 109 us against 113 with 8 and 2), 4 or 2; few tokens have
-// too few threads for more than one piece each, and fp32 has no registers for
-// two pieces of five (4096 x 4096, k = 10, backward: 287 us against 239).
-int pair_batch(int k, bool few, int dtype) {
+// too few threads for more than one piece each.
+int pair_batch(int k, bool few) {
     if (few) return 8;
     if (k <= 4) return k <= 2 ? 2 : 4;
-    return dtype != MOE_DTYPE_F32 && (k == 5 || k == 9 || k == 10) ? 5 : 8;
+    return k == 5 || k == 9 || k == 10 ? 5 : 8;
 }
 int even_batch(int k, int most) { const int n = (k + most - 1) / most; return (k + n - 1) / n; }
 constexpr int kFewTokens = 2 * 152;
@@ -461,7 +459,7 @@ cudaError_t launch_combine_k(const void *y, int T, int k, int H, const int32_t *
                              const void *base, void *out, cudaStream_t st) {
     using E = typename RowType<DT>::T;
     constexpr int PP = pair_pieces(KB);
-    const int n = (H / kChunk + PP - 1) / PP;                       // threads that a row can use
+    const int n = (H / kPieceValues<DT> + PP - 1) / PP;                       // threads that a row can use
     const int tx = std::min(kCombineThreads, (n + 31) / 32 * 32), ty = kCombineThreads / tx;
     return launch_pdl(k_combine<DT, KB, PP>, dim3((T + ty - 1) / ty, (n + tx - 1) / tx), dim3(tx, ty), 0, st,
                       static_cast<const E *>(y), T, k, H, inv, R, w, static_cast<const E *>(base),
@@ -471,10 +469,10 @@ cudaError_t launch_combine_k(const void *y, int T, int k, int H, const int32_t *
 template <int DT>
 cudaError_t launch_combine(const void *y, int T, int k, int H, const int32_t *inv, int64_t R, const float *w,
                            const void *base, void *out, cudaStream_t st) {
-    switch (pair_batch(k, T <= kFewTokens, DT)) {
+    switch (pair_batch(k, T <= kFewTokens)) {
         case 2: return launch_combine_k<DT, 2>(y, T, k, H, inv, R, w, base, out, st);
         case 4: return launch_combine_k<DT, 4>(y, T, k, H, inv, R, w, base, out, st);
-        case 5: return launch_combine_k<DT, DT == MOE_DTYPE_F32 ? 8 : 5>(y, T, k, H, inv, R, w, base, out, st);
+        case 5: return launch_combine_k<DT, 5>(y, T, k, H, inv, R, w, base, out, st);
         default: return launch_combine_k<DT, 8>(y, T, k, H, inv, R, w, base, out, st);
     }
 }
@@ -485,9 +483,9 @@ cudaError_t launch_combine_backward_k(const void *go, const void *y, int T, int 
                                       cudaStream_t st) {
     using E = typename RowType<DT>::T;
     constexpr int PP = pair_pieces(KB);
-    const bool few = T <= kFewBackward, warp = !few && H / kChunk <= 32 * (KB > 4 ? 4 : 8);
+    const bool few = T <= kFewBackward, warp = !few && H / kPieceValues<DT> <= 32 * (KB > 4 ? 4 : 8);
     const int kb = few ? 1 : even_batch(k, KB);
-    const int pieces = (H / kChunk + PP - 1) / PP;                  // threads that a row can use
+    const int pieces = (H / kPieceValues<DT> + PP - 1) / PP;                  // threads that a row can use
     const int threads = warp ? 256 : std::max(few ? 128 : 32, std::min(256, (pieces + 31) / 32 * 32));
     const int parts = (k + kb - 1) / kb;
     const int64_t token_blocks = (int64_t)(warp ? (T + 7) / 8 : T) * parts;
@@ -504,10 +502,10 @@ template <int DT>
 cudaError_t launch_combine_backward(const void *go, const void *y, int T, int k, int H, const int32_t *rows,
                                     const int32_t *inv, int64_t R, const float *w, void *gy, float *gw,
                                     cudaStream_t st) {
-    switch (T <= kFewBackward ? 2 : pair_batch(k, false, DT)) {
+    switch (T <= kFewBackward ? 2 : pair_batch(k, false)) {
         case 2: return launch_combine_backward_k<DT, 2>(go, y, T, k, H, rows, inv, R, w, gy, gw, st);
         case 4: return launch_combine_backward_k<DT, 4>(go, y, T, k, H, rows, inv, R, w, gy, gw, st);
-        case 5: return launch_combine_backward_k<DT, DT == MOE_DTYPE_F32 ? 8 : 5>(go, y, T, k, H, rows, inv, R, w, gy, gw, st);
+        case 5: return launch_combine_backward_k<DT, 5>(go, y, T, k, H, rows, inv, R, w, gy, gw, st);
         default: return launch_combine_backward_k<DT, 8>(go, y, T, k, H, rows, inv, R, w, gy, gw, st);
     }
 }
