@@ -469,7 +469,8 @@ __global__ void __launch_bounds__(8 * kColumnGroups) k_rms_norm_grad_w(const flo
 // and four above `two` pieces a row.  Forward 400 (bf16, 8 bits out, 8192 rows of
 // 4096 without residual 20.1 us against 23.8 with two pieces, with residual 4096
 // rows 20.1 against 19.7; 2048 wide, one piece and 256 threads 39.5 us against
-// 36.7 at 16384 rows), backward 512 (four pieces need the registers).
+// 36.7 at 16384 rows), backward 512 (four pieces need the registers), in fp32
+// 1024 (8192 rows of 4528 118 us against 140 us with four).
 struct RowShape { int threads, v; };
 RowShape row_shape(int n8, bool few, int two) {
     const int v = few ? (n8 <= 512 ? 1 : n8 <= 1024 ? 2 : 4) : (n8 <= 128 ? 1 : n8 <= two ? 2 : 4);
@@ -531,18 +532,24 @@ template <int DT> cudaError_t launch_norm(const NormArgs &a, int quant, int T, c
 // rows of 1024, bf16: 25.7 us against 65 us a block a row), longer ones a
 // block.  Blocks an SM: 512 threads' worth, two to four (16384 rows: H = 2048
 // 46.0 us with four, 58.1 with two; H = 6144 133 us with two, 171 with three,
-// whose third waits); every block writes a row of partial sums.  What one block
-// does in two rounds is one block's, whose sums are the result: no workspace and
-// no second launch (2 rows of 4096 3.1 us against 3.8, 4 rows would be 4.7; 16
-// rows of 512 2.8 against 3.2, 32 would be 4.4; host 7 us a call against 15).
+// whose third waits), no more than its shared memory takes (1216 rows of 16384:
+// 32.4 us with one, 36.8 with two); every block writes a row of partial sums.
+// What one block does in two rounds is one block's, whose sums are the result:
+// no workspace and no second launch (2 rows of 4096 3.1 us against 3.8, 4 rows
+// would be 4.7; 16 rows of 512 2.8 against 3.2, 32 would be 4.4; host 7 us a call
+// against 15).
 constexpr int kOneBlockRounds = 2;
 struct GradShape { RowShape row; bool warp; int blocks; };
 GradShape grad_shape(int T, int H, int dtype) {
     const int n8 = H / kChunk;
+    const bool f32 = dtype == MOE_DTYPE_F32;
     GradShape g;
-    g.warp = n8 <= (dtype == MOE_DTYPE_F32 ? kWarpPieces / 2 : kWarpPieces);   // a warp's ring of fp32 rows is twice as large
-    g.row = g.warp ? RowShape{32, warp_pieces(n8)} : row_shape(n8, false, 512);
-    const int an_sm = std::max(2, std::min(4, 512 / (g.warp ? 32 * kWarpRows : g.row.threads)));
+    g.warp = n8 <= (f32 ? kWarpPieces / 2 : kWarpPieces);              // a warp's ring of fp32 rows is twice as large
+    g.row = g.warp ? RowShape{32, warp_pieces(n8)} : row_shape(n8, false, f32 ? 1024 : 512);
+    const int threads = g.warp ? 32 * kWarpRows : g.row.threads;
+    const size_t rings = 2 * 3 * (f32 ? 32 : 16) * (size_t)g.row.v * threads;
+    const int fit = (int)std::max<size_t>(1, kSmemSm / (rings + 2048));
+    const int an_sm = std::min(fit, std::max(2, std::min(4, 512 / threads)));
     const int groups = g.warp ? (T - 1) / kWarpRows + 1 : T;          // rows, or eights of them
     g.blocks = groups <= kOneBlockRounds ? 1 : std::min(groups, an_sm * kSms);
     return g;
