@@ -537,7 +537,7 @@ template <int DT> cudaError_t launch_norm(const NormArgs &a, int quant, int T, c
 // What one block does in two rounds is one block's, whose sums are the result:
 // no workspace and no second launch (2 rows of 4096 3.1 us against 3.8, 4 rows
 // would be 4.7; 16 rows of 512 2.8 against 3.2, 32 would be 4.4; host 7 us a call
-// against 15).
+// against 12).
 constexpr int kOneBlockRounds = 2;
 struct GradShape { RowShape row; bool warp; int blocks; };
 GradShape grad_shape(int T, int H, int dtype) {
