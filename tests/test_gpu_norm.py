@@ -300,3 +300,28 @@ def test_norm_on_another_stream_and_in_a_graph():
     assert torch.equal(got["sum"], torch.roll(want["sum"], 1, 0))
     assert torch.equal(got["q"].view(torch.uint8), torch.roll(want["q"].view(torch.uint8), 1, 0))
     assert torch.equal(gback["grad_sum"], torch.roll(back["grad_sum"], 1, 0))
+
+
+def test_norm_backward_workspaces_do_not_meet():
+    """The call's workspace inside a graph, under eager allocations between replays, and on two streams at once."""
+    T, H = 700, 2048
+    s, gy, gs, w = _grads(T, H, torch.bfloat16, 41, True)
+    rstd = moe.rms_norm(s, w)["rstd"]
+    want = moe.rms_norm_backward(gy, s, w, rstd, grad_sum=gs)
+    again = moe.rms_norm_backward(want["grad_sum"], s, w, rstd)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        one = moe.rms_norm_backward(gy, s, w, rstd, grad_sum=gs)
+        between = torch.zeros(1 << 22, device="cuda") + 5
+        two = moe.rms_norm_backward(one["grad_sum"], s, w, rstd)
+    for _ in range(10):
+        graph.replay()
+        torch.full((1 << 20,), 3.0, device="cuda")
+    torch.cuda.synchronize()
+    assert (between == 5).all()
+    for a, b in ((one, want), (two, again)):
+        assert torch.equal(a["grad_w"], b["grad_w"]) and torch.equal(a["grad_sum"], b["grad_sum"])
+    side = torch.cuda.Stream()
+    got = [moe.rms_norm_backward(gy, s, w, rstd, grad_sum=gs, stream=st) for _ in range(30) for st in (None, side)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a["grad_w"], want["grad_w"]) for a in got)
