@@ -335,8 +335,9 @@ typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2 } moe_dt
  *   E4M3_ROW: one group a row, fp32 scales [T].
  *             For both: a = max(amax of |n| in the group, 2^-100), scale =
  *             a / 448, code = E4M3_rne_sat(n * 448 / a), where n * 448 / a is
- *             (s * weight) * (448 / amax |s * weight|).  A NaN makes its group
- *             NaN.
+ *             (s * weight) * (448 / amax |s * weight|), but n * (448 / a) in
+ *             groups with amax |n| or amax |s * weight| of 2^-100 or less.  A
+ *             NaN makes its group NaN.
  *   MXFP8:    groups of 32, E8M0 scales uint8[T][ceil(H/32)]: byte =
  *             clamp(floor(log2(amax)) - 8 + 127, 0, 254) (0 for an all-zero
  *             group), code = E4M3_rne_sat(n * 2^(127 - byte)); a group whose

@@ -38,7 +38,12 @@ struct NormArgs {
     float *rstd;
 };
 
-// Maximum that keeps a NaN; of magnitudes, three at a time.
+// Minimum and maximum that keep a NaN; the maximum of magnitudes, three at a time.
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -117,13 +122,15 @@ template <int DT> __device__ __forceinline__ void product8(float (&f)[8], const 
 
 // A group's scale, and the factor that takes its products to its codes: with top
 // = amax p * rstd and a = max(top, 2^-100) a code is that of p * rstd * 448 / a,
-// which is p * (448 / amax p) but for groups at the bound (or with a NaN), whose
-// products are taken times rstd first: rstd * 448 / 2^-100 may leave fp32.
-__device__ __forceinline__ float e4m3_factor(float amax_p, float top) {
-    return __fdiv_rn(448.0f, top > kMinAmax ? amax_p : kMinAmax);
+// which is p * (448 / amax p).  Groups with top or amax p at the bound or below it
+// (or with a NaN) take their products times rstd first, and then 448 / a: rstd *
+// 448 / 2^-100 may leave fp32, and so may 448 / amax p, from 2^-119.2 down, where
+// rstd is large.  `low` is min(amax p, top).
+__device__ __forceinline__ float e4m3_factor(float amax_p, float top, float low) {
+    return __fdiv_rn(448.0f, low > kMinAmax ? amax_p : max_nan(top, kMinAmax));
 }
-__device__ __forceinline__ void at_the_bound(float (&p)[8], float top, float rstd) {
-    if (top > kMinAmax) return;
+__device__ __forceinline__ void at_the_bound(float (&p)[8], float low, float rstd) {
+    if (low > kMinAmax) return;
 #pragma unroll
     for (int e = 0; e < 8; e += 2) mul2(p, e, rstd, rstd);
 }
@@ -182,7 +189,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
             if (a.r) u[i] = load8<DT>(static_cast<const T *>(a.r) + t * a.rs + c * kChunk);
         }
     }
-    float p[V][8], s0 = 0.0f, s1 = 0.0f, row_mul = 0.0f, row_top = 0.0f;
+    float p[V][8], s0 = 0.0f, s1 = 0.0f, row_mul = 0.0f, row_low = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = tid + i * n;
@@ -203,9 +210,10 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
     const float rstd = row_rstd(sum, a.inv_h, a.eps);
     if (a.rstd && tid == 0) a.rstd[t] = rstd;
     if constexpr (Q == MOE_QUANT_E4M3_ROW) {
-        row_top = __fmul_rn(row_mul, rstd);
-        row_mul = e4m3_factor(row_mul, row_top);
-        if (tid == 0) static_cast<float *>(a.scales)[t] = e4m3_scale(row_top);
+        const float top = __fmul_rn(row_mul, rstd);
+        row_low = min_nan(row_mul, top);
+        row_mul = e4m3_factor(row_mul, top, row_low);
+        if (tid == 0) static_cast<float *>(a.scales)[t] = e4m3_scale(top);
     }
     constexpr int kLanes = Q == MOE_QUANT_MXFP8 ? 4 : 16;      // of a group
     const int64_t group0 = t * ((n8 + kLanes - 1) / kLanes);
@@ -216,18 +224,18 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
     };
     // E4M3_128: lane i of a group's 16 does the divisions of its piece i, all
     // pieces' at once
-    float top[V], factor = row_mul;
+    float low[V], factor = row_mul;
     if constexpr (Q == MOE_QUANT_E4M3_128) {
         const int mine = threadIdx.x & 15;
-        float m = 0.0f, own = 0.0f;
+        float m = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            top[i] = group_max(amax8(p[i], 0.0f));
-            if (mine == i) m = top[i];
-            top[i] = __fmul_rn(top[i], rstd);
-            if (mine == i) own = top[i];
+            const float amax_p = group_max(amax8(p[i], 0.0f));
+            low[i] = min_nan(amax_p, __fmul_rn(amax_p, rstd));
+            if (mine == i) m = amax_p;
         }
-        factor = e4m3_factor(m, own);
+        const float own = __fmul_rn(m, rstd);
+        factor = e4m3_factor(m, own, min_nan(m, own));
         const int c = (tid & ~15) + mine * n;
         if (mine < V && c < n8) static_cast<float *>(a.scales)[group0 + c / 16] = e4m3_scale(own);
     }
@@ -244,10 +252,10 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
         }
         if constexpr (Q == MOE_QUANT_NONE) continue;
         float mul = factor;
-        if constexpr (Q == MOE_QUANT_E4M3_ROW) at_the_bound(p[i], row_top, rstd);
+        if constexpr (Q == MOE_QUANT_E4M3_ROW) at_the_bound(p[i], row_low, rstd);
         if constexpr (Q == MOE_QUANT_E4M3_128) {
             mul = __shfl_sync(0xffffffffu, factor, (threadIdx.x & 16) + i);
-            at_the_bound(p[i], top[i], rstd);
+            at_the_bound(p[i], low[i], rstd);
         }
         if constexpr (Q == MOE_QUANT_MXFP8) {
 #pragma unroll
