@@ -320,7 +320,8 @@ moe_status moe_route_static(const void *x_bf16, int32_t T, int32_t hidden, const
  * their own (8-bit or bf16 products, training): the layer's norm, the sort of
  * the (token, slot) pairs by expert, rows to expert order and back, and the
  * gradients.  These entry points need no plan, allocate nothing, keep nothing
- * between calls and replay from CUDA graphs.  Rows (x, residual, sum, y, q,
+ * between calls and replay from CUDA graphs.  They launch on the current device,
+ * which has to be the stream's and the arrays'.  Rows (x, residual, sum, y, q,
  * their gradients, weight) are 16-byte aligned, every other array is aligned to
  * its element.  Row counts, row offsets and strides may pass 32 bits in bytes.
  * ====================================================================== */

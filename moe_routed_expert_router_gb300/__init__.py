@@ -125,6 +125,7 @@ def _stream(stream=None):
 # The current stream's handle: 0.1 us a call where torch has it, 2.9 us through a Stream object.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _check(status: int, where: str):
@@ -193,6 +194,7 @@ def convert_f32(src: torch.Tensor, fmt: int, out: torch.Tensor | None = None, st
 #
 # A decode step makes these calls for a few microseconds of work each, so the checks are written
 # to cost little when they pass: one expression an argument, the text of a refusal only when one is due.
+# A call runs on its tensors' device, whichever is current, on `stream` or else on that device's current stream.
 
 _DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
 _GROUP = {QUANT_E4M3_128: 128, QUANT_MXFP8: 32}
@@ -239,8 +241,21 @@ def _new(shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _on(index, stream):
-    return _raw_stream(index) if stream is None else stream.cuda_stream
+def _on(where, index, stream):
+    """The handle of the stream that the call runs on: the given one, or the current one of the tensors' device."""
+    if stream is None:
+        return _raw_stream(index)
+    if stream.device_index != index:
+        _refuse(where, f"stream of cuda:{stream.device_index}, tensors on cuda:{index}")
+    return stream.cuda_stream
+
+
+def _there(index, function):
+    """The library launches on the current device: its function, with the tensors' device current for the call."""
+    def call(*args):
+        with torch.cuda.device(index):
+            return function(*args)
+    return call
 
 
 def rms_norm(x, weight, residual=None, eps=1e-6, quant=QUANT_NONE, out=None, stream=None):
@@ -289,7 +304,10 @@ def rms_norm(x, weight, residual=None, eps=1e-6, quant=QUANT_NONE, out=None, str
             _refuse(where, "q and scales go together, and with a quant")
         qp = _want(t_q, where, "q", shape, torch.float8_e4m3fn, index)
         cp = _want(t_scales, where, "scales", sc_shape, sc_dtype, index)
-    st = lib().moe_rms_norm(xp, xs, rp, rs, wp, T, H, code, eps, quant, sp, yp, qp, cp, dp, _on(index, stream))
+    call = lib().moe_rms_norm
+    if _current_device() != index:
+        call = _there(index, call)
+    st = call(xp, xs, rp, rs, wp, T, H, code, eps, quant, sp, yp, qp, cp, dp, _on(where, index, stream))
     if st:
         raise MoeError(st, where)
     return out
@@ -318,11 +336,13 @@ def rms_norm_backward(grad_y, sum, weight, rstd, grad_sum=None, out=None, stream
     ow = _want(out["grad_w"], where, "out grad_w", (H,), _F32, index)
     L = lib()
     n = L.moe_rms_norm_backward_workspace(T, H)
-    handle = _on(index, stream)
+    call, handle = L.moe_rms_norm_backward, _on(where, index, stream)
+    if _current_device() != index:
+        call = _there(index, call)
     # plain memory of the call's stream, given back to it behind the launches (a tensor for it costs 2.4 us more)
     ws = torch.cuda.caching_allocator_alloc(n, index, handle) if n else None
     try:
-        st = L.moe_rms_norm_backward(yp, sp, wp, dp, gp, T, H, code, op, ow, ws, n, handle)
+        st = call(yp, sp, wp, dp, gp, T, H, code, op, ow, ws, n, handle)
     finally:
         if ws is not None:
             torch.cuda.caching_allocator_delete(ws)
@@ -359,7 +379,10 @@ def sort_pairs(topk_ids, num_experts, align=1, out=None, stream=None):
     op = _want(out["expert_offsets"], where, "out expert_offsets", (num_experts + 1,), _I32, index)
     rp = _want(out["sorted_rows"], where, "out sorted_rows", (R,), _I32, index)
     pp = _want(out["pair_rows"], where, "out pair_rows", shape, _I32, index)
-    st = lib().moe_sort_pairs(ip, T, k, num_experts, align, R, op, rp, pp, _on(index, stream))
+    call = lib().moe_sort_pairs
+    if _current_device() != index:
+        call = _there(index, call)
+    st = call(ip, T, k, num_experts, align, R, op, rp, pp, _on(where, index, stream))
     if st:
         raise MoeError(st, where)
     return out
@@ -399,7 +422,10 @@ def dispatch(x, order, scales=None, out=None, stream=None):
     op, oc = _want(out["rows"], where, "out rows", (R, H), dt, index), None
     if scales is not None:
         oc = _want(out["scales"], where, "out scales", (R, cn), scales.dtype, index)
-    st = lib().moe_dispatch(xp, xs * es, H * es, cp, sb, T, k, rp, pp, R, op, oc, _on(index, stream))
+    call = lib().moe_dispatch
+    if _current_device() != index:
+        call = _there(index, call)
+    st = call(xp, xs * es, H * es, cp, sb, T, k, rp, pp, R, op, oc, _on(where, index, stream))
     if st:
         raise MoeError(st, where)
     return out
@@ -422,7 +448,10 @@ def combine(y, order, weights=None, base=None, out=None, stream=None):
     if out is None:
         out = _new((T, H), dt, dev, stream)
     op = _want(out, where, "out", (T, H), dt, index)
-    st = lib().moe_combine(yp, code, T, k, H, pp, R, wp, bp, op, _on(index, stream))
+    call = lib().moe_combine
+    if _current_device() != index:
+        call = _there(index, call)
+    st = call(yp, code, T, k, H, pp, R, wp, bp, op, _on(where, index, stream))
     if st:
         raise MoeError(st, where)
     return out
@@ -451,7 +480,10 @@ def combine_backward(grad_out, y, order, weights, out=None, stream=None):
         out = {"grad_y": _new((R, H), dt, dev, stream), "grad_w": _new((T, k), _F32, dev, stream)}
     oy = _want(out["grad_y"], where, "out grad_y", (R, H), dt, index)
     ow = _want(out["grad_w"], where, "out grad_w", (T, k), _F32, index)
-    st = lib().moe_combine_backward(gp, yp, code, T, k, H, rp, pp, R, wp, oy, ow, _on(index, stream))
+    call = lib().moe_combine_backward
+    if _current_device() != index:
+        call = _there(index, call)
+    st = call(gp, yp, code, T, k, H, rp, pp, R, wp, oy, ow, _on(where, index, stream))
     if st:
         raise MoeError(st, where)
     return out
