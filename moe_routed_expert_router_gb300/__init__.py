@@ -195,6 +195,9 @@ def convert_f32(src: torch.Tensor, fmt: int, out: torch.Tensor | None = None, st
 # A decode step makes these calls for a few microseconds of work each, so the checks are written
 # to cost little when they pass: one expression an argument, the text of a refusal only when one is due.
 # A call runs on its tensors' device, whichever is current, on `stream` or else on that device's current stream.
+# Where `stream` is given the caller orders it behind the work that fills the tensors and, as with any work on another
+# stream, the work that uses the results behind it; new results belong to that stream, and the memory of what is given
+# is held until it has passed the call.
 
 _DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
 _GROUP = {QUANT_E4M3_128: 128, QUANT_MXFP8: 32}
@@ -241,12 +244,14 @@ def _new(shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _on(where, index, stream):
-    """The handle of the stream that the call runs on: the given one, or the current one of the tensors' device."""
-    if stream is None:
-        return _raw_stream(index)
+def _given(where, index, stream, *tensors):
+    """The handle of a stream that the caller names; what the call reads and writes is held for it, because torch
+    would give memory that is freed meanwhile to the stream it came from."""
     if stream.device_index != index:
         _refuse(where, f"stream of cuda:{stream.device_index}, tensors on cuda:{index}")
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
     return stream.cuda_stream
 
 
@@ -304,10 +309,12 @@ def rms_norm(x, weight, residual=None, eps=1e-6, quant=QUANT_NONE, out=None, str
             _refuse(where, "q and scales go together, and with a quant")
         qp = _want(t_q, where, "q", shape, torch.float8_e4m3fn, index)
         cp = _want(t_scales, where, "scales", sc_shape, sc_dtype, index)
+    handle = _raw_stream(index) if stream is None else _given(
+        where, index, stream, x, weight, residual, t_sum, t_y, t_rstd, t_q, t_scales)
     call = lib().moe_rms_norm
     if _current_device() != index:
         call = _there(index, call)
-    st = call(xp, xs, rp, rs, wp, T, H, code, eps, quant, sp, yp, qp, cp, dp, _on(where, index, stream))
+    st = call(xp, xs, rp, rs, wp, T, H, code, eps, quant, sp, yp, qp, cp, dp, handle)
     if st:
         raise MoeError(st, where)
     return out
@@ -336,7 +343,9 @@ def rms_norm_backward(grad_y, sum, weight, rstd, grad_sum=None, out=None, stream
     ow = _want(out["grad_w"], where, "out grad_w", (H,), _F32, index)
     L = lib()
     n = L.moe_rms_norm_backward_workspace(T, H)
-    call, handle = L.moe_rms_norm_backward, _on(where, index, stream)
+    handle = _raw_stream(index) if stream is None else _given(
+        where, index, stream, grad_y, sum, weight, rstd, grad_sum, out["grad_sum"], out["grad_w"])
+    call = L.moe_rms_norm_backward
     if _current_device() != index:
         call = _there(index, call)
     # plain memory of the call's stream, given back to it behind the launches (a tensor for it costs 2.4 us more)
@@ -379,10 +388,12 @@ def sort_pairs(topk_ids, num_experts, align=1, out=None, stream=None):
     op = _want(out["expert_offsets"], where, "out expert_offsets", (num_experts + 1,), _I32, index)
     rp = _want(out["sorted_rows"], where, "out sorted_rows", (R,), _I32, index)
     pp = _want(out["pair_rows"], where, "out pair_rows", shape, _I32, index)
+    handle = _raw_stream(index) if stream is None else _given(
+        where, index, stream, topk_ids, out["expert_offsets"], out["sorted_rows"], out["pair_rows"])
     call = lib().moe_sort_pairs
     if _current_device() != index:
         call = _there(index, call)
-    st = call(ip, T, k, num_experts, align, R, op, rp, pp, _on(where, index, stream))
+    st = call(ip, T, k, num_experts, align, R, op, rp, pp, handle)
     if st:
         raise MoeError(st, where)
     return out
@@ -422,10 +433,13 @@ def dispatch(x, order, scales=None, out=None, stream=None):
     op, oc = _want(out["rows"], where, "out rows", (R, H), dt, index), None
     if scales is not None:
         oc = _want(out["scales"], where, "out scales", (R, cn), scales.dtype, index)
+    handle = _raw_stream(index) if stream is None else _given(
+        where, index, stream, x, scales, order["sorted_rows"], order["pair_rows"], out["rows"],
+        None if scales is None else out["scales"])
     call = lib().moe_dispatch
     if _current_device() != index:
         call = _there(index, call)
-    st = call(xp, xs * es, H * es, cp, sb, T, k, rp, pp, R, op, oc, _on(where, index, stream))
+    st = call(xp, xs * es, H * es, cp, sb, T, k, rp, pp, R, op, oc, handle)
     if st:
         raise MoeError(st, where)
     return out
@@ -448,10 +462,12 @@ def combine(y, order, weights=None, base=None, out=None, stream=None):
     if out is None:
         out = _new((T, H), dt, dev, stream)
     op = _want(out, where, "out", (T, H), dt, index)
+    handle = _raw_stream(index) if stream is None else _given(
+        where, index, stream, y, order["pair_rows"], weights, base, out)
     call = lib().moe_combine
     if _current_device() != index:
         call = _there(index, call)
-    st = call(yp, code, T, k, H, pp, R, wp, bp, op, _on(where, index, stream))
+    st = call(yp, code, T, k, H, pp, R, wp, bp, op, handle)
     if st:
         raise MoeError(st, where)
     return out
@@ -480,10 +496,12 @@ def combine_backward(grad_out, y, order, weights, out=None, stream=None):
         out = {"grad_y": _new((R, H), dt, dev, stream), "grad_w": _new((T, k), _F32, dev, stream)}
     oy = _want(out["grad_y"], where, "out grad_y", (R, H), dt, index)
     ow = _want(out["grad_w"], where, "out grad_w", (T, k), _F32, index)
+    handle = _raw_stream(index) if stream is None else _given(
+        where, index, stream, grad_out, y, order["sorted_rows"], order["pair_rows"], weights, out["grad_y"], out["grad_w"])
     call = lib().moe_combine_backward
     if _current_device() != index:
         call = _there(index, call)
-    st = call(gp, yp, code, T, k, H, rp, pp, R, wp, oy, ow, _on(where, index, stream))
+    st = call(gp, yp, code, T, k, H, rp, pp, R, wp, oy, ow, handle)
     if st:
         raise MoeError(st, where)
     return out

@@ -128,3 +128,15 @@ def test_a_stream_of_another_device_is_refused(world, which):
     with pytest.raises(moe.MoeError) as e:
         call()
     assert e.value.status == moe.ERR_INVALID_ARG and not world.calls
+
+
+@pytest.mark.parametrize("which", range(7))
+def test_memory_of_the_tensors_is_held_for_a_given_stream(world, which):
+    """What a call on another stream reads and writes is recorded there: torch gives freed memory away otherwise."""
+    _, call, tensors = every_call(0)[which]
+    call()
+    assert not any(t.streams for t in tensors)           # the current stream: nothing to record
+    stream = Stream(0)
+    _, call, tensors = every_call(0, stream)[which]
+    call()
+    assert all(t.streams == [stream] for t in tensors)
