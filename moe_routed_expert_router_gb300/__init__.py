@@ -126,6 +126,7 @@ def _stream(stream=None):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_devices = 0    # of this process; 0 until the first call asks
 
 
 def _check(status: int, where: str):
@@ -255,6 +256,14 @@ def _given(where, index, stream, *tensors):
     return stream.cuda_stream
 
 
+def _elsewhere(index):
+    """Whether another device than the tensors' is current."""
+    global _devices
+    if _devices == 0:
+        _devices = torch.cuda.device_count()
+    return _devices != 1 and _current_device() != index
+
+
 def _there(index, function):
     """The library launches on the current device: its function, with the tensors' device current for the call."""
     def call(*args):
@@ -312,7 +321,7 @@ def rms_norm(x, weight, residual=None, eps=1e-6, quant=QUANT_NONE, out=None, str
     handle = _raw_stream(index) if stream is None else _given(
         where, index, stream, x, weight, residual, t_sum, t_y, t_rstd, t_q, t_scales)
     call = lib().moe_rms_norm
-    if _current_device() != index:
+    if _devices != 1 and _elsewhere(index):
         call = _there(index, call)
     st = call(xp, xs, rp, rs, wp, T, H, code, eps, quant, sp, yp, qp, cp, dp, handle)
     if st:
@@ -346,7 +355,7 @@ def rms_norm_backward(grad_y, sum, weight, rstd, grad_sum=None, out=None, stream
     handle = _raw_stream(index) if stream is None else _given(
         where, index, stream, grad_y, sum, weight, rstd, grad_sum, out["grad_sum"], out["grad_w"])
     call = L.moe_rms_norm_backward
-    if _current_device() != index:
+    if _devices != 1 and _elsewhere(index):
         call = _there(index, call)
     # plain memory of the call's stream, given back to it behind the launches (a tensor for it costs 2.4 us more)
     ws = torch.cuda.caching_allocator_alloc(n, index, handle) if n else None
@@ -391,7 +400,7 @@ def sort_pairs(topk_ids, num_experts, align=1, out=None, stream=None):
     handle = _raw_stream(index) if stream is None else _given(
         where, index, stream, topk_ids, out["expert_offsets"], out["sorted_rows"], out["pair_rows"])
     call = lib().moe_sort_pairs
-    if _current_device() != index:
+    if _devices != 1 and _elsewhere(index):
         call = _there(index, call)
     st = call(ip, T, k, num_experts, align, R, op, rp, pp, handle)
     if st:
@@ -437,7 +446,7 @@ def dispatch(x, order, scales=None, out=None, stream=None):
         where, index, stream, x, scales, order["sorted_rows"], order["pair_rows"], out["rows"],
         None if scales is None else out["scales"])
     call = lib().moe_dispatch
-    if _current_device() != index:
+    if _devices != 1 and _elsewhere(index):
         call = _there(index, call)
     st = call(xp, xs * es, H * es, cp, sb, T, k, rp, pp, R, op, oc, handle)
     if st:
@@ -465,7 +474,7 @@ def combine(y, order, weights=None, base=None, out=None, stream=None):
     handle = _raw_stream(index) if stream is None else _given(
         where, index, stream, y, order["pair_rows"], weights, base, out)
     call = lib().moe_combine
-    if _current_device() != index:
+    if _devices != 1 and _elsewhere(index):
         call = _there(index, call)
     st = call(yp, code, T, k, H, pp, R, wp, bp, op, handle)
     if st:
@@ -499,7 +508,7 @@ def combine_backward(grad_out, y, order, weights, out=None, stream=None):
     handle = _raw_stream(index) if stream is None else _given(
         where, index, stream, grad_out, y, order["sorted_rows"], order["pair_rows"], weights, out["grad_y"], out["grad_w"])
     call = lib().moe_combine_backward
-    if _current_device() != index:
+    if _devices != 1 and _elsewhere(index):
         call = _there(index, call)
     st = call(gp, yp, code, T, k, H, rp, pp, R, wp, oy, ow, handle)
     if st:

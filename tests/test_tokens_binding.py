@@ -68,6 +68,7 @@ class World:
         fake = Lib()
         monkeypatch.setattr(moe, "lib", lambda: fake)
         monkeypatch.setattr(moe, "_raw_stream", lambda index: 1000 + index)
+        monkeypatch.setattr(moe, "_devices", 2, raising=False)
         monkeypatch.setattr(moe, "_current_device", lambda: self.current, raising=False)
         monkeypatch.setattr(torch.cuda, "device", device)
         monkeypatch.setattr(torch.cuda, "current_device", lambda: self.current)
