@@ -209,6 +209,11 @@ def _refuse(where: str, what: str, status: int = ERR_INVALID_ARG):
     raise MoeError(status, f"{where} ({what})")
 
 
+def _too_large(where, *sizes):
+    """The entry points take sizes of 32 bits; ctypes would pass on the lower 32 of a larger one."""
+    _refuse(where, f"sizes {list(sizes)}; 2^31 - 1 is the largest", ERR_UNSUPPORTED_SHAPE)
+
+
 def _dtype(t, where):
     d = _DTYPES.get(t.dtype)
     if d is None:
@@ -284,6 +289,8 @@ def rms_norm(x, weight, residual=None, eps=1e-6, quant=QUANT_NONE, out=None, str
     if len(shape) != 2:
         _refuse(where, "x is not [T][H]")
     T, H = shape
+    if (T | H) >> 31:
+        _too_large(where, T, H)
     dev, dt, code = _device(x, where), x.dtype, _dtype(x, where)
     index = dev.index
     xp, xs = _want_rows(x, where, "x", shape, dt, index)
@@ -339,6 +346,8 @@ def rms_norm_backward(grad_y, sum, weight, rstd, grad_sum=None, out=None, stream
     if len(shape) != 2:
         _refuse(where, "sum is not [T][H]")
     T, H = shape
+    if (T | H) >> 31:
+        _too_large(where, T, H)
     dev, dt, code = _device(sum, where), sum.dtype, _dtype(sum, where)
     index = dev.index
     sp = _want(sum, where, "sum", shape, dt, index)
@@ -371,7 +380,7 @@ def rms_norm_backward(grad_y, sum, weight, rstd, grad_sum=None, out=None, stream
 
 def sorted_rows(pairs: int, num_experts: int, align: int = 1) -> int:
     """Rows of the sorted layout, whatever the routing (moe_sorted_rows)."""
-    n = lib().moe_sorted_rows(pairs, num_experts, align)
+    n = -1 if (pairs | num_experts | align) >> 31 else lib().moe_sorted_rows(pairs, num_experts, align)
     if n < 0:
         _refuse("moe_sorted_rows", f"{pairs} pairs, {num_experts} experts, align {align}", ERR_UNSUPPORTED_SHAPE)
     return n
@@ -414,6 +423,8 @@ def _order(order, where, index):
     if rows.dim() != 1 or inv.dim() != 2:
         _refuse(where, "order is not sort_pairs' result")
     R, (T, k) = rows.shape[0], inv.shape
+    if (R | T | k) >> 31:
+        _too_large(where, R, T, k)
     return _want(rows, where, "sorted_rows", (R,), _I32, index), _want(inv, where, "pair_rows", (T, k), _I32, index), R, T, k
 
 
@@ -435,6 +446,8 @@ def dispatch(x, order, scales=None, out=None, stream=None):
             _refuse(where, "scales is not [T][n]")
         cn = scales.shape[1]
         cp, sb = _want(scales, where, "scales", (T, cn), scales.dtype, index), cn * scales.element_size()
+        if sb >> 31:
+            _too_large(where, sb)
     if out is None:
         out = {"rows": _new((R, H), dt, dev, stream)}
         if scales is not None:
@@ -465,6 +478,8 @@ def combine(y, order, weights=None, base=None, out=None, stream=None):
     if y.dim() != 2:
         _refuse(where, "y is not [rows][H]")
     H, dt, code = y.shape[1], y.dtype, _dtype(y, where)
+    if H >> 31:
+        _too_large(where, H)
     yp = _want(y, where, "y", (R, H), dt, index)
     wp = None if weights is None else _want(weights, where, "weights", (T, k), _F32, index)
     bp = None if base is None else _want(base, where, "base", (T, H), dt, index)
@@ -498,6 +513,8 @@ def combine_backward(grad_out, y, order, weights, out=None, stream=None):
     if y.dim() != 2:
         _refuse(where, "y is not [rows][H]")
     H, dt, code = y.shape[1], y.dtype, _dtype(y, where)
+    if H >> 31:
+        _too_large(where, H)
     yp = _want(y, where, "y", (R, H), dt, index)
     gp = _want(grad_out, where, "grad_out", (T, H), dt, index)
     wp = _want(weights, where, "weights", (T, k), _F32, index)

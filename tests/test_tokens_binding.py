@@ -141,3 +141,37 @@ def test_memory_of_the_tensors_is_held_for_a_given_stream(world, which):
     _, call, tensors = every_call(0, stream)[which]
     call()
     assert all(t.streams == [stream] for t in tensors)
+
+
+# --------------------------------- sizes that the entry points' 32-bit arguments cannot hold
+
+@pytest.mark.parametrize("size", [dict(T=(1 << 32) + 6), dict(H=(1 << 32) + 64), dict(T=1 << 31)])
+@pytest.mark.parametrize("which", range(7))
+def test_sizes_past_32_bits_are_refused(world, which, size):
+    name, call, _ = every_call(**size)[which]
+    if name == "moe_sort_pairs" and "H" in size:
+        pytest.skip("no H")
+    with pytest.raises(moe.MoeError) as e:
+        call()
+    assert e.value.status == moe.ERR_UNSUPPORTED_SHAPE and not world.calls
+
+
+def test_pairs_a_token_and_scales_past_32_bits_are_refused(world):
+    many = (1 << 32) + 2
+    order = dict(sorted_rows=Tensor((R,), I32), pair_rows=Tensor((T, many), I32))
+    good = dict(sorted_rows=Tensor((R,), I32), pair_rows=Tensor((T, K), I32))
+    for call in (lambda: moe.combine(Tensor((R, H), BF), order, out=Tensor((T, H), BF)),
+                 lambda: moe.dispatch(Tensor((T, H), BF), order, out=dict(rows=Tensor((R, H), BF))),
+                 lambda: moe.dispatch(Tensor((T, H), BF), good, scales=Tensor((T, 1 << 30), F32),
+                                      out=dict(rows=Tensor((R, H), BF), scales=Tensor((R, 1 << 30), F32)))):
+        with pytest.raises(moe.MoeError) as e:
+            call()
+        assert e.value.status == moe.ERR_UNSUPPORTED_SHAPE and not world.calls
+
+
+@pytest.mark.parametrize("args", [(10, (1 << 32) + 8), (10, 8 - (1 << 32)), (10, 8, (1 << 32) + 1), (10, 8, 1 - (1 << 32)),
+                                  ((1 << 64) + 10, 8)])
+def test_sorted_rows_of_sizes_past_32_bits(args):
+    with pytest.raises(moe.MoeError) as e:
+        moe.sorted_rows(*args)
+    assert e.value.status == moe.ERR_UNSUPPORTED_SHAPE
