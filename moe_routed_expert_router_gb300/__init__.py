@@ -199,6 +199,8 @@ def convert_f32(src: torch.Tensor, fmt: int, out: torch.Tensor | None = None, st
 # Where `stream` is given the caller orders it behind the work that fills the tensors and, as with any work on another
 # stream, the work that uses the results behind it; new results belong to that stream, and the memory of what is given
 # is held until it has passed the call.
+# Autograd does not see the calls.  The forward ones refuse tensors that require a gradient while it is on; a training
+# program calls the gradients' entry points itself, or from the backward() of an autograd.Function.
 
 _DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
 _GROUP = {QUANT_E4M3_128: 128, QUANT_MXFP8: 32}
@@ -212,6 +214,13 @@ def _refuse(where: str, what: str, status: int = ERR_INVALID_ARG):
 def _too_large(where, *sizes):
     """The entry points take sizes of 32 bits; ctypes would pass on the lower 32 of a larger one."""
     _refuse(where, f"sizes {list(sizes)}; 2^31 - 1 is the largest", ERR_UNSUPPORTED_SHAPE)
+
+
+def _followed(where):
+    """The call's results would be cut from the graph that autograd keeps of its tensors."""
+    if torch.is_grad_enabled():
+        _refuse(where, "a tensor requires grad and the result has no history: call it under torch.no_grad() or in an "
+                       "autograd.Function, and the gradient's own entry point for the way back")
 
 
 def _dtype(t, where):
@@ -296,6 +305,8 @@ def rms_norm(x, weight, residual=None, eps=1e-6, quant=QUANT_NONE, out=None, str
     xp, xs = _want_rows(x, where, "x", shape, dt, index)
     wp = _want(weight, where, "weight", (H,), dt, index)
     rp, rs = (None, 0) if residual is None else _want_rows(residual, where, "residual", shape, dt, index)
+    if x.requires_grad or weight.requires_grad or (residual is not None and residual.requires_grad):
+        _followed(where)
     sc_shape, sc_dtype = None, _F32
     if quant != QUANT_NONE:
         if quant not in (QUANT_E4M3_128, QUANT_E4M3_ROW, QUANT_MXFP8):
@@ -440,6 +451,8 @@ def dispatch(x, order, scales=None, out=None, stream=None):
         _refuse(where, "x is not [T][H]")
     H, dt, es = x.shape[1], x.dtype, x.element_size()
     xp, xs = _want_rows(x, where, "x", (T, H), dt, index)
+    if x.requires_grad or (scales is not None and scales.requires_grad):
+        _followed(where)
     cp, cn, sb = None, 0, 0
     if scales is not None:
         if scales.dim() != 2:
@@ -483,6 +496,8 @@ def combine(y, order, weights=None, base=None, out=None, stream=None):
     yp = _want(y, where, "y", (R, H), dt, index)
     wp = None if weights is None else _want(weights, where, "weights", (T, k), _F32, index)
     bp = None if base is None else _want(base, where, "base", (T, H), dt, index)
+    if y.requires_grad or (weights is not None and weights.requires_grad) or (base is not None and base.requires_grad):
+        _followed(where)
     if out is None:
         out = _new((T, H), dt, dev, stream)
     op = _want(out, where, "out", (T, H), dt, index)

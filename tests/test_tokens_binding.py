@@ -175,3 +175,21 @@ def test_sorted_rows_of_sizes_past_32_bits(args):
     with pytest.raises(moe.MoeError) as e:
         moe.sorted_rows(*args)
     assert e.value.status == moe.ERR_UNSUPPORTED_SHAPE
+
+
+# --------------------------------- tensors that autograd follows
+
+@pytest.mark.parametrize("which,names", [(0, 3), (3, 2), (4, 3), (5, 1)])
+def test_tensors_that_require_a_gradient_are_not_taken_in_silence(world, which, names):
+    """The results have no history: the forward calls refuse what autograd would follow, unless it is switched off."""
+    for i in range(names):
+        name, call, tensors = every_call()[which]
+        tensors[i].requires_grad = True
+        with pytest.raises(moe.MoeError) as e:
+            call()
+        assert e.value.status == moe.ERR_INVALID_ARG and "no_grad" in str(e.value) and not world.calls
+        with torch.no_grad():
+            call()
+        (got, _, _), = world.calls
+        assert got == name
+        world.calls.clear()
