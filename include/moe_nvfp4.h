@@ -376,10 +376,13 @@ moe_status moe_rms_norm(const void *x, int64_t x_stride, const void *residual, i
  * grad_y, sum, grad_sum (NULL: none), grad_in: [T][H] of `dtype`; grad_in may
  * be grad_y's or grad_sum's memory.  weight [H] of `dtype`, rstd [T], grad_w
  * [H] fp32 (written, not added to).  workspace: device memory of at least
- * moe_rms_norm_backward_workspace(T, H) bytes (0 for a few rows: NULL then),
- * 16-byte aligned, used during the call only.  Rows are added in a fixed order: the same inputs on the same
- * device give the same bits.  T = 0 writes grad_w = 0. */
+ * moe_rms_norm_backward_workspace_for(T, H, dtype) bytes (0 for a few rows:
+ * NULL then; moe_rms_norm_backward_workspace(T, H) is enough for any type),
+ * 16-byte aligned, used during the call only.  Rows are added in a fixed
+ * order: the same inputs on the same device give the same bits.  T = 0 writes
+ * grad_w = 0. */
 size_t moe_rms_norm_backward_workspace(int32_t T, int32_t H);
+size_t moe_rms_norm_backward_workspace_for(int32_t T, int32_t H, int32_t dtype);
 moe_status moe_rms_norm_backward(const void *grad_y, const void *sum, const void *weight, const float *rstd,
                                  const void *grad_sum, int32_t T, int32_t H, int32_t dtype, void *grad_in,
                                  float *grad_w, void *workspace, size_t workspace_bytes, void *stream);

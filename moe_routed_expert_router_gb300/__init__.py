@@ -32,6 +32,7 @@ EXPORTS = ["moe_plan_create", "moe_plan_destroy", "moe_route", "moe_forward", "m
            "moe_plan_set_profiling", "moe_plan_read_profile", "moe_plan_set_path", "moe_plan_check_timeout",
            "moe_route_static", "moe_convert_f32", "moe_quantize_mxfp4", "moe_plan_keep_h", "moe_status_string",
            "moe_version", "moe_rms_norm", "moe_rms_norm_backward", "moe_rms_norm_backward_workspace",
+           "moe_rms_norm_backward_workspace_for",
            "moe_sorted_rows", "moe_sort_pairs", "moe_dispatch", "moe_combine", "moe_combine_backward"]
 FMT_E4M3, FMT_E2M1 = 0, 1
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
@@ -91,6 +92,7 @@ def lib():
         L.moe_rms_norm.argtypes = [P, I64, P, I64, P, I32, I32, I32, ctypes.c_float, I32, P, P, P, P, P, P]
         L.moe_rms_norm_backward.argtypes = [P, P, P, P, P, I32, I32, I32, P, P, P, SZ, P]
         L.moe_rms_norm_backward_workspace.argtypes = [I32, I32]
+        L.moe_rms_norm_backward_workspace_for.argtypes = [I32, I32, I32]
         L.moe_sorted_rows.argtypes = [I64, I32, I32]
         L.moe_sort_pairs.argtypes = [P, I32, I32, I32, I32, I64, P, P, P, P]
         L.moe_dispatch.argtypes = [P, I64, I64, P, I32, I32, I32, P, P, I64, P, P, P]
@@ -102,7 +104,7 @@ def lib():
         for n in EXPORTS:
             if n not in ("moe_status_string", "moe_version"):
                 getattr(L, n).restype = I32
-        L.moe_rms_norm_backward_workspace.restype = SZ
+        L.moe_rms_norm_backward_workspace.restype = L.moe_rms_norm_backward_workspace_for.restype = SZ
         L.moe_sorted_rows.restype = I64
         _lib = L
     return _lib
@@ -371,7 +373,7 @@ def rms_norm_backward(grad_y, sum, weight, rstd, grad_sum=None, out=None, stream
     op = _want(out["grad_sum"], where, "out grad_sum", shape, dt, index)
     ow = _want(out["grad_w"], where, "out grad_w", (H,), _F32, index)
     L = lib()
-    n = L.moe_rms_norm_backward_workspace(T, H)
+    n = L.moe_rms_norm_backward_workspace_for(T, H, code)
     handle = _raw_stream(index) if stream is None else _given(
         where, index, stream, grad_y, sum, weight, rstd, grad_sum, out["grad_sum"], out["grad_w"])
     call = L.moe_rms_norm_backward

@@ -635,9 +635,13 @@ moe_status moe_rms_norm(const void *x, int64_t x_stride, const void *residual, i
     }
 }
 
+size_t moe_rms_norm_backward_workspace_for(int32_t T, int32_t H, int32_t dtype) {
+    return T > 0 && H > 0 && known_dtype(dtype) ? grad_workspace(grad_shape(T, H, dtype), H) : 0;
+}
+
 size_t moe_rms_norm_backward_workspace(int32_t T, int32_t H) {
-    if (T <= 0 || H <= 0) return 0;
-    return std::max(grad_workspace(grad_shape(T, H, MOE_DTYPE_F32), H), grad_workspace(grad_shape(T, H, MOE_DTYPE_BF16), H));
+    return std::max(moe_rms_norm_backward_workspace_for(T, H, MOE_DTYPE_F32),
+                    moe_rms_norm_backward_workspace_for(T, H, MOE_DTYPE_BF16));   // f16's is bf16's
 }
 
 moe_status moe_rms_norm_backward(const void *grad_y, const void *sum, const void *weight, const float *rstd,
@@ -647,7 +651,7 @@ moe_status moe_rms_norm_backward(const void *grad_y, const void *sum, const void
     if (st != MOE_OK) return st;
     if (!grad_w) return MOE_ERR_INVALID_ARG;
     if (T > 0 && (!grad_y || !sum || !weight || !rstd || !grad_in)) return MOE_ERR_INVALID_ARG;
-    const size_t need = moe_rms_norm_backward_workspace(T, H);
+    const size_t need = moe_rms_norm_backward_workspace_for(T, H, dtype);
     if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_INVALID_ARG;
     if (!aligned_to(grad_y, 16) || !aligned_to(sum, 16) || !aligned_to(weight, 16) || !aligned_to(rstd, 4) ||
         !aligned_to(grad_sum, 16) || !aligned_to(grad_in, 16) || !aligned_to(grad_w, 4) || !aligned_to(workspace, 16))
