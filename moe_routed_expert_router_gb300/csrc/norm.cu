@@ -508,7 +508,7 @@ template <auto Kernel> cudaError_t allow_smem() {
 
 template <int DT, int Q, bool kWarp>
 cudaError_t launch_norm_v(const NormArgs &a, int T, int threads, int v, cudaStream_t st) {
-    const dim3 grid(kWarp ? (T + kWarpRows - 1) / kWarpRows : T), block(kWarp ? 32 * kWarpRows : threads);
+    const dim3 grid(kWarp ? blocks_of(T, kWarpRows) : T), block(kWarp ? 32 * kWarpRows : threads);
     if (v == 1) return launch_pdl(k_rms_norm<DT, Q, 1, kWarp>, grid, block, 0, st, a, (int64_t)T);
     if (v == 2) return launch_pdl(k_rms_norm<DT, Q, 2, kWarp>, grid, block, 0, st, a, (int64_t)T);
     return launch_pdl(k_rms_norm<DT, Q, 4, kWarp>, grid, block, 0, st, a, (int64_t)T);
@@ -558,7 +558,7 @@ GradShape grad_shape(int T, int H, int dtype) {
     const size_t rings = 2 * 3 * (f32 ? 32 : 16) * (size_t)g.row.v * threads;
     const int fit = (int)std::max<size_t>(1, kSmemSm / (rings + 2048));
     const int an_sm = std::min(fit, std::max(2, std::min(4, 512 / threads)));
-    const int groups = g.warp ? (T - 1) / kWarpRows + 1 : T;          // rows, or eights of them
+    const int groups = g.warp ? blocks_of(T, kWarpRows) : T;          // rows, or eights of them
     g.blocks = groups <= kOneBlockRounds ? 1 : std::min(groups, an_sm * kSms);
     return g;
 }

@@ -160,6 +160,9 @@ template <int DT> __device__ __forceinline__ uint4 narrow_piece(const float (&v)
         return narrow8<DT>(v).a;
 }
 
+// Blocks for n rows, `each` of them a block; n may be the largest int.
+inline int blocks_of(int n, int each) { return n > 0 ? (n - 1) / each + 1 : 0; }
+
 inline bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline bool known_dtype(int32_t d) { return d == MOE_DTYPE_F32 || d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F16; }
 

@@ -461,7 +461,7 @@ cudaError_t launch_combine_k(const void *y, int T, int k, int H, const int32_t *
     constexpr int PP = pair_pieces(KB);
     const int n = (H / kPieceValues<DT> + PP - 1) / PP;                       // threads that a row can use
     const int tx = std::min(kCombineThreads, (n + 31) / 32 * 32), ty = kCombineThreads / tx;
-    return launch_pdl(k_combine<DT, KB, PP>, dim3((T + ty - 1) / ty, (n + tx - 1) / tx), dim3(tx, ty), 0, st,
+    return launch_pdl(k_combine<DT, KB, PP>, dim3(blocks_of(T, ty), (n + tx - 1) / tx), dim3(tx, ty), 0, st,
                       static_cast<const E *>(y), T, k, H, inv, R, w, static_cast<const E *>(base),
                       static_cast<E *>(out));
 }
@@ -488,7 +488,7 @@ cudaError_t launch_combine_backward_k(const void *go, const void *y, int T, int 
     const int pieces = (H / kPieceValues<DT> + PP - 1) / PP;                  // threads that a row can use
     const int threads = warp ? 256 : std::max(few ? 128 : 32, std::min(256, (pieces + 31) / 32 * 32));
     const int parts = (k + kb - 1) / kb;
-    const int64_t token_blocks = (int64_t)(warp ? (T + 7) / 8 : T) * parts;
+    const int64_t token_blocks = (int64_t)(warp ? blocks_of(T, 8) : T) * parts;
     const int zero_rows = zero_rows_a_warp(H * (int)sizeof(E) / 16), block_rows = threads / 32 * zero_rows;
     const int64_t blocks = token_blocks + (R + block_rows - 1) / block_rows;
     if (blocks > kMaxRows) return cudaErrorInvalidValue;
@@ -593,7 +593,7 @@ moe_status moe_dispatch(const void *x, int64_t x_stride_bytes, int64_t row_bytes
     const int n = (int)(row_bytes / 16);
     const int tx = std::min(256, ((n + kCopyPieces - 1) / kCopyPieces + 31) / 32 * 32), ty = 256 / tx;
     const int parts = (n + tx * kCopyPieces - 1) / (tx * kCopyPieces);
-    const int64_t token_blocks = (int64_t)((T + ty - 1) / ty) * parts;
+    const int64_t token_blocks = (int64_t)blocks_of(T, ty) * parts;
     const int zero_rows = zero_rows_a_warp(n), block_rows = tx * ty / 32 * zero_rows;
     const int64_t blocks = token_blocks + (rows + block_rows - 1) / block_rows;
     if (blocks > kMaxRows) return MOE_ERR_UNSUPPORTED_SHAPE;
