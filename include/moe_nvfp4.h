@@ -402,7 +402,9 @@ int64_t moe_sorted_rows(int64_t pairs, int32_t num_experts, int32_t align);
  *   pair_rows      [T][k] int32: the row of a pair, -1 where it is dropped
  * rows = moe_sorted_rows(T*k, E, align), at most 2^31 - 1; align a power of
  * two up to 256; k up to 32; E up to 1024.  With align = 1 and no pair dropped,
- * expert_offsets and sorted_rows are moe_route's.  T = 0 writes zero offsets. */
+ * expert_offsets and sorted_rows are moe_route's.  T = 0 writes zero offsets.
+ * More than 4096 pairs take a cluster of 16 blocks: MOE_ERR_CUDA on a partition
+ * of a device that cannot hold one. */
 moe_status moe_sort_pairs(const int32_t *topk_ids, int32_t T, int32_t k, int32_t num_experts, int32_t align,
                           int64_t rows, int32_t *expert_offsets, int32_t *sorted_rows, int32_t *pair_rows,
                           void *stream);

@@ -3,9 +3,9 @@
 //
 // A block takes a row and keeps it in registers over the reduction, so every
 // input is read once and every output written once.  Bound by HBM (4096 x 7168
-// bf16 with residual and E4M3_128 output 32.9 us, 93 % of the measured copy
-// bandwidth; without the residual, three bytes a value, by instructions: 8192 x
-// 7168 36 us, 72 %).  What keeps it there is that the loads of the next row do
+// bf16 with residual and E4M3_128 output 32.4 us, 94 % of the measured copy
+// bandwidth; without the residual, three bytes a value, 8192 x 7168 37.2 us, 71 %,
+// with 69 % of the issue slots taken).  What keeps it there is that the loads of the next row do
 // not wait for the reduction of the present one: other blocks' in the forward
 // pass, a ring in shared memory in the backward pass.  (A ring in the forward
 // pass too: 33.7 against 34.3 us at 4096 x 7168, 20.8 against 20.1 at 4096 x 4096.)

@@ -70,7 +70,8 @@ struct SortArgs {
 // (4 tokens, k = 8, E = 128: 2.3 us in a graph; 16384 tokens, E = 256: 10.6 us
 // with 16 blocks, half of it the ranking, some 110 instructions for 32 pairs on
 // 16 SMs; the scattered stores are 0.5 us, and placing through a sorted copy in
-// shared memory, for neighbouring ones, measured no gain).
+// shared memory, for neighbouring ones, measured no gain).  A cluster of 16 is more
+// than every device has to hold; a whole GB300 does.
 template <bool kCluster>
 __global__ void __launch_bounds__(1024) k_sort_pairs(const SortArgs a) {
     extern __shared__ int smem[];
@@ -294,8 +295,9 @@ __global__ void __launch_bounds__(256) k_dispatch(const char *x, int64_t xs, int
 // (KB x PP = 8), so that a token of two pairs asks for as much as one of eight
 // (16384 tokens of 4096, k = 2, bf16: 59 us against 99 us with one piece).
 // The registers are held to what lets an SM keep its blocks (4096 x 7168, k = 8,
-// bf16: 77.1 us at 64 registers, 101 % of the measured copy bandwidth; 80.8 us
-// at 66, with a block less; the rows passed between lanes by shuffles 87.9 us).
+// bf16: 77.1 us at 64 registers, 80.8 us at 66, with a block less; the rows passed
+// between lanes by shuffles 87.9 us; over changing inputs 80 us, 98 % of the
+// measured copy bandwidth).
 // A piece is 16 bytes in every type: with eight fp32 values a thread a warp's
 // access had holes (4096 x 4096, k = 10, fp32, backward: 208 us against 238).
 constexpr int pair_pieces(int kb) { return kb == 5 ? 2 : 8 / kb; }
@@ -511,8 +513,6 @@ cudaError_t launch_combine_backward(const void *go, const void *y, int T, int k,
 }
 
 // ----------------------------------------------------------------- checks
-
-
 
 moe_status check_pairs(int32_t T, int32_t k, int64_t rows) {
     if (T < 0 || rows < 0) return MOE_ERR_INVALID_ARG;
