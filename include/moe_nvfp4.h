@@ -444,6 +444,55 @@ moe_status moe_combine_backward(const void *grad_out, const void *y, int32_t dty
                                 const int32_t *sorted_rows, const int32_t *pair_rows, int64_t rows,
                                 const float *weights, void *grad_y, float *grad_weights, void *stream);
 
+/* ======================================================================
+ * Around attention and in a decode step: the norm of query and key heads with
+ * the position rotation, its gradients, products of a few tokens with a 4-bit
+ * weight, and the whole layer of a few tokens with experts that are not
+ * quantised.  As the entry points above: no plan, no allocation, nothing kept
+ * between calls, graph replay, the current device.
+ * ====================================================================== */
+
+/* Root-mean-square norm of every query and key head, then the rotation by the
+ * token's position.  Of a head row x of D values:
+ *   n = (x * weight) / sqrt(mean(x^2) + eps)   in fp32,
+ *   the first R values of n turn in R/2 planes: (a, b) -> (a cos - b sin,
+ *   b cos + a sin), plane i being values i and i + R/2, or 2i and 2i + 1 where
+ *   interleaved is 1; the other D - R values stay; rounded once.
+ * The angle of plane i at position p is p * turns[i] / 2^64 of a whole turn, the
+ * product taken modulo 2^64: turns[i] = floor(frequency_i / (2 pi) * 2^64)
+ * modulo 2^64 for a frequency in radians a position.  Far and negative positions are exact.
+ *   q [T][q_heads][D], k [T][k_heads][D]: the heads of a token lie behind one
+ *     another, tokens q_stride and k_stride values apart (so both may be parts
+ *     of the rows of one product)
+ *   q_weight, k_weight [D], all of `dtype`; positions [T] int32; turns [R/2]
+ *     (both unused and possibly NULL for R = 0)
+ *   q_out, k_out: as q and k, with strides of their own; each may be its input
+ *     in place (the same address and stride), and overlaps nothing else
+ * D: a multiple of 16 up to 512; R: a multiple of 16 up to D; heads: up to 1024;
+ * strides: multiples of 8, at least heads * D; eps > 0 and finite. */
+moe_status moe_head_norm(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *q_weight,
+                         const void *k_weight, const int32_t *positions, const uint64_t *turns, int32_t T,
+                         int32_t q_heads, int32_t k_heads, int32_t D, int32_t R, int32_t interleaved, int32_t dtype,
+                         float eps, void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride, void *stream);
+
+/* Gradients of moe_head_norm.  With g = grad turned back and n = x * rstd:
+ *   grad_in = rstd * (g * weight - n * mean(g * weight * n)),
+ *   grad_weight = sum over tokens and heads of g * n   (fp32, written)
+ * rstd is computed again from q and k.  grad_q, grad_k, q, k as above with
+ * strides; grad_q_in [T][q_heads][D] and grad_k_in [T][k_heads][D] without;
+ * each may be the memory of its grad or of its input where that one has no
+ * stride either.  workspace: moe_head_norm_backward_workspace bytes (0 for a few
+ * rows: NULL then), 16-byte aligned, used during the call only.  Sums are taken
+ * in a fixed order.  T = 0 writes zeros to grad_qw and grad_kw. */
+size_t moe_head_norm_backward_workspace(int32_t T, int32_t q_heads, int32_t k_heads, int32_t D, int32_t R);
+moe_status moe_head_norm_backward(const void *grad_q, int64_t grad_q_stride, const void *grad_k, int64_t grad_k_stride,
+                                  const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                  const void *q_weight, const void *k_weight, const int32_t *positions,
+                                  const uint64_t *turns, int32_t T, int32_t q_heads, int32_t k_heads, int32_t D,
+                                  int32_t R, int32_t interleaved, int32_t dtype, float eps, void *grad_q_in,
+                                  void *grad_k_in, float *grad_qw, float *grad_kw, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
 /* Text of a status code (static storage). */
 const char *moe_status_string(moe_status s);
 

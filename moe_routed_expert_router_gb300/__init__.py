@@ -8,6 +8,7 @@ the library cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -33,7 +34,8 @@ EXPORTS = ["moe_plan_create", "moe_plan_destroy", "moe_route", "moe_forward", "m
            "moe_route_static", "moe_convert_f32", "moe_quantize_mxfp4", "moe_plan_keep_h", "moe_status_string",
            "moe_version", "moe_rms_norm", "moe_rms_norm_backward", "moe_rms_norm_backward_workspace",
            "moe_rms_norm_backward_workspace_for",
-           "moe_sorted_rows", "moe_sort_pairs", "moe_dispatch", "moe_combine", "moe_combine_backward"]
+           "moe_sorted_rows", "moe_sort_pairs", "moe_dispatch", "moe_combine", "moe_combine_backward",
+           "moe_head_norm", "moe_head_norm_backward", "moe_head_norm_backward_workspace"]
 FMT_E4M3, FMT_E2M1 = 0, 1
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 QUANT_NONE, QUANT_E4M3_128, QUANT_E4M3_ROW, QUANT_MXFP8 = 0, 1, 2, 3
@@ -98,6 +100,10 @@ def lib():
         L.moe_dispatch.argtypes = [P, I64, I64, P, I32, I32, I32, P, P, I64, P, P, P]
         L.moe_combine.argtypes = [P, I32, I32, I32, I32, P, I64, P, P, P, P]
         L.moe_combine_backward.argtypes = [P, P, I32, I32, I32, I32, P, P, I64, P, P, P, P]
+        head = [P, P, P, P, I32, I32, I32, I32, I32, I32, I32, ctypes.c_float]   # weights, positions, turns; sizes
+        L.moe_head_norm.argtypes = [P, I64, P, I64, *head, P, I64, P, I64, P]
+        L.moe_head_norm_backward.argtypes = [P, I64, P, I64, P, I64, P, I64, *head, P, P, P, P, P, SZ, P]
+        L.moe_head_norm_backward_workspace.argtypes = [I32, I32, I32, I32, I32]
         L.moe_status_string.argtypes = [I32]
         L.moe_status_string.restype = ctypes.c_char_p
         L.moe_version.restype = ctypes.c_char_p
@@ -105,6 +111,7 @@ def lib():
             if n not in ("moe_status_string", "moe_version"):
                 getattr(L, n).restype = I32
         L.moe_rms_norm_backward_workspace.restype = L.moe_rms_norm_backward_workspace_for.restype = SZ
+        L.moe_head_norm_backward_workspace.restype = SZ
         L.moe_sorted_rows.restype = I64
         _lib = L
     return _lib
@@ -545,6 +552,109 @@ def combine_backward(grad_out, y, order, weights, out=None, stream=None):
     if _devices != 1 and _elsewhere(index):
         call = _there(index, call)
     st = call(gp, yp, code, T, k, H, rp, pp, R, wp, oy, ow, handle)
+    if st:
+        raise MoeError(st, where)
+    return out
+
+
+# ------------------------------------------------ around attention and in a decode step
+
+def rotary_turns(dim, base=10000.0, frequencies=None, device="cuda"):
+    """What head_norm keeps of a rotation of `dim` values: int64 [dim / 2], a plane's frequency as a fraction of a turn a
+    position in units of 2^-64.  Frequencies are base ** (-2 i / dim) radians a position, or the `frequencies` given
+    (dim / 2 finite numbers, of a scaled rotation for instance)."""
+    where = "rotary_turns"
+    if dim < 0 or dim % 16:
+        _refuse(where, f"dim {dim}; a multiple of 16 expected", ERR_UNSUPPORTED_SHAPE)
+    freqs = [base ** (-2.0 * i / dim) for i in range(dim // 2)] if frequencies is None else [float(f) for f in frequencies]
+    if len(freqs) != dim // 2 or not all(math.isfinite(f) for f in freqs):
+        _refuse(where, f"{len(freqs)} frequencies for dim {dim}; dim / 2 finite numbers expected")
+    turns = [math.floor(f / (2 * math.pi) * 2.0 ** 64) % 2 ** 64 for f in freqs]
+    return torch.tensor([t - 2 ** 64 if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
+
+
+def _want_heads(t, where, name, shape, dtype, index):
+    """Heads of contiguous values behind one another, tokens a stride apart; returns their address and stride in values."""
+    T, n, D = shape
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not (
+            t.is_contiguous() or (t.stride(2) == 1 and (n == 1 or t.stride(1) == D))):
+        _refuse(where, f"{name} {t.dtype}{list(t.shape)} on {t.device}; heads of contiguous {dtype}{list(shape)} on cuda:{index} expected")
+    return t.data_ptr(), t.stride(0) if T > 1 else n * D
+
+
+def _heads(q, k, q_weight, k_weight, positions, turns, where):
+    """The checks that both directions of head_norm share."""
+    if len(q.shape) != 3 or len(k.shape) != 3 or len(turns.shape) != 1:
+        _refuse(where, "q, k are not [T][heads][D] or turns is not [R / 2]")
+    T, nq, D = q.shape
+    nk, R = k.shape[1], 2 * turns.shape[0]
+    if (T | nq | nk | D | R) >> 31:
+        _too_large(where, T, nq, nk, D, R)
+    dev, dt, code = _device(q, where), q.dtype, _dtype(q, where)
+    index = dev.index
+    qp, qs = _want_heads(q, where, "q", (T, nq, D), dt, index)
+    kp, ks = _want_heads(k, where, "k", (T, nk, D), dt, index)
+    small = (_want(q_weight, where, "q_weight", (D,), dt, index), _want(k_weight, where, "k_weight", (D,), dt, index),
+             _want(positions, where, "positions", (T,), _I32, index) if R else None,
+             _want(turns, where, "turns", (R // 2,), torch.int64, index) if R else None)
+    return dev, index, dt, code, (qp, qs, kp, ks), small, (T, nq, nk, D, R)
+
+
+def head_norm(q, k, q_weight, k_weight, positions, turns, interleaved=False, eps=1e-6, out=None, stream=None):
+    """Root-mean-square norm of every head of q [T][heads][D] and k [T][heads][D] and the rotation of its first
+    2 * len(turns) values by the token's position (int32 [T]); turns is rotary_turns' tensor (an empty one: no rotation).
+
+    The planes of the rotation are values i and i + R / 2, or 2 i and 2 i + 1 where interleaved.  A token's heads lie
+    behind one another and tokens may be strided, as in parts of one product's rows.  Returns {"q", "k"}: new tensors, or
+    `out`'s, which may be strided as well and may be q and k themselves."""
+    where = "moe_head_norm"
+    dev, index, dt, code, given, small, sizes = _heads(q, k, q_weight, k_weight, positions, turns, where)
+    if q.requires_grad or k.requires_grad or q_weight.requires_grad or k_weight.requires_grad:
+        _followed(where)
+    if out is None:
+        out = {"q": _new(q.shape, dt, dev, stream), "k": _new(k.shape, dt, dev, stream)}
+    op, os_ = _want_heads(out["q"], where, "out q", q.shape, dt, index)
+    pp, ps = _want_heads(out["k"], where, "out k", k.shape, dt, index)
+    handle = _raw_stream(index) if stream is None else _given(
+        where, index, stream, q, k, q_weight, k_weight, positions, turns, out["q"], out["k"])
+    call = lib().moe_head_norm
+    if _devices != 1 and _elsewhere(index):
+        call = _there(index, call)
+    st = call(*given, *small, *sizes, int(interleaved), code, eps, op, os_, pp, ps, handle)
+    if st:
+        raise MoeError(st, where)
+    return out
+
+
+def head_norm_backward(grad_q, grad_k, q, k, q_weight, k_weight, positions, turns, interleaved=False, eps=1e-6, out=None,
+                       stream=None):
+    """Gradients of head_norm: {"grad_q", "grad_k" as q and k, contiguous; "grad_qw", "grad_kw": [D] fp32}.
+
+    q and k are head_norm's inputs.  out's "grad_q" and "grad_k" may be the given gradients or inputs where those are
+    contiguous."""
+    where = "moe_head_norm_backward"
+    dev, index, dt, code, given, small, sizes = _heads(q, k, q_weight, k_weight, positions, turns, where)
+    gp, gs = _want_heads(grad_q, where, "grad_q", q.shape, dt, index)
+    hp, hs = _want_heads(grad_k, where, "grad_k", k.shape, dt, index)
+    D = sizes[3]
+    if out is None:
+        out = {"grad_q": _new(q.shape, dt, dev, stream), "grad_k": _new(k.shape, dt, dev, stream),
+               "grad_qw": _new((D,), _F32, dev, stream), "grad_kw": _new((D,), _F32, dev, stream)}
+    outs = (_want(out["grad_q"], where, "out grad_q", q.shape, dt, index), _want(out["grad_k"], where, "out grad_k", k.shape, dt, index),
+            _want(out["grad_qw"], where, "out grad_qw", (D,), _F32, index), _want(out["grad_kw"], where, "out grad_kw", (D,), _F32, index))
+    L = lib()
+    n = L.moe_head_norm_backward_workspace(*sizes)
+    handle = _raw_stream(index) if stream is None else _given(
+        where, index, stream, grad_q, grad_k, q, k, q_weight, k_weight, positions, turns, *out.values())
+    call = L.moe_head_norm_backward
+    if _devices != 1 and _elsewhere(index):
+        call = _there(index, call)
+    ws = torch.cuda.caching_allocator_alloc(n, index, handle) if n else None
+    try:
+        st = call(gp, gs, hp, hs, *given, *small, *sizes, int(interleaved), code, eps, *outs, ws, n, handle)
+    finally:
+        if ws is not None:
+            torch.cuda.caching_allocator_delete(ws)
     if st:
         raise MoeError(st, where)
     return out

@@ -428,48 +428,11 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) k_rms_no
     }
 }
 
-// grad_w[h] = sum of the blocks' partial sums: thread (i, j) adds every 64th
-// block's from j on, four columns wide, then the 64 sums are added in order,
-// eight by eight.  The partial sums come from L2 and the launch overlaps the end
-// of the one before, so this is latency, 2 to 3 us: every thread's loads are one
-// round (1216 rows of 2048: the pass 8.5 us; 32 groups of two rounds 9.5).
-constexpr int kColumnGroups = 64;
-
+// The second launch of the backward pass overlaps the end of the first: latency, 2 to 3 us.
 __global__ void __launch_bounds__(8 * kColumnGroups) k_rms_norm_grad_w(const float *part, int blocks, int H, float *gw) {
-    __shared__ float4 s[kColumnGroups][8];
-    __shared__ float t[8][32];
-    const int i = threadIdx.x & 7, j = threadIdx.x >> 3;
-    const int h = blockIdx.x * 32 + i * 4;
     pdl_wait();
     pdl_trigger();
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (h < H) {
-#pragma unroll 5
-        for (int b = j; b < blocks; b += kColumnGroups) {
-            const float4 p = *reinterpret_cast<const float4 *>(part + (int64_t)b * H + h);
-            v.x += p.x;
-            v.y += p.y;
-            v.z += p.z;
-            v.w += p.w;
-        }
-    }
-    s[j][i] = v;
-    __syncthreads();
-    const float *c = reinterpret_cast<const float *>(s) + (threadIdx.x & 31);
-    const int w = threadIdx.x >> 5;
-    if (w < 8) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kColumnGroups / 8; ++k) sum += c[(w * (kColumnGroups / 8) + k) * 32];
-        t[w][threadIdx.x & 31] = sum;
-    }
-    __syncthreads();
-    if (threadIdx.x < 32 && blockIdx.x * 32 + threadIdx.x < H) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sum += t[k][threadIdx.x];
-        gw[blockIdx.x * 32 + threadIdx.x] = sum;
-    }
+    column_sums(part, blocks, H, gw);
 }
 
 // Threads and pieces a thread for a row of n8 pieces.  Few rows: as many threads
