@@ -35,7 +35,8 @@ EXPORTS = ["moe_plan_create", "moe_plan_destroy", "moe_route", "moe_forward", "m
            "moe_version", "moe_rms_norm", "moe_rms_norm_backward", "moe_rms_norm_backward_workspace",
            "moe_rms_norm_backward_workspace_for",
            "moe_sorted_rows", "moe_sort_pairs", "moe_dispatch", "moe_combine", "moe_combine_backward",
-           "moe_head_norm", "moe_head_norm_backward", "moe_head_norm_backward_workspace"]
+           "moe_head_norm", "moe_head_norm_backward", "moe_head_norm_backward_workspace",
+           "moe_linear_fp4", "moe_linear_fp4_workspace"]
 FMT_E4M3, FMT_E2M1 = 0, 1
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 QUANT_NONE, QUANT_E4M3_128, QUANT_E4M3_ROW, QUANT_MXFP8 = 0, 1, 2, 3
@@ -104,6 +105,8 @@ def lib():
         L.moe_head_norm.argtypes = [P, I64, P, I64, *head, P, I64, P, I64, P]
         L.moe_head_norm_backward.argtypes = [P, I64, P, I64, P, I64, P, I64, *head, P, P, P, P, P, SZ, P]
         L.moe_head_norm_backward_workspace.argtypes = [I32, I32, I32, I32, I32]
+        L.moe_linear_fp4.argtypes = [P, I64, ctypes.POINTER(Nvfp4), I32, I32, I32, I32, I32, I32, P, P, SZ, P]
+        L.moe_linear_fp4_workspace.argtypes = [I32, I32, I32]
         L.moe_status_string.argtypes = [I32]
         L.moe_status_string.restype = ctypes.c_char_p
         L.moe_version.restype = ctypes.c_char_p
@@ -111,7 +114,7 @@ def lib():
             if n not in ("moe_status_string", "moe_version"):
                 getattr(L, n).restype = I32
         L.moe_rms_norm_backward_workspace.restype = L.moe_rms_norm_backward_workspace_for.restype = SZ
-        L.moe_head_norm_backward_workspace.restype = SZ
+        L.moe_head_norm_backward_workspace.restype = L.moe_linear_fp4_workspace.restype = SZ
         L.moe_sorted_rows.restype = I64
         _lib = L
     return _lib
@@ -652,6 +655,65 @@ def head_norm_backward(grad_q, grad_k, q, k, q_weight, k_weight, positions, turn
     ws = torch.cuda.caching_allocator_alloc(n, index, handle) if n else None
     try:
         st = call(gp, gs, hp, hs, *given, *small, *sizes, int(interleaved), code, eps, *outs, ws, n, handle)
+    finally:
+        if ws is not None:
+            torch.cuda.caching_allocator_delete(ws)
+    if st:
+        raise MoeError(st, where)
+    return out
+
+
+_U8 = torch.uint8
+
+
+def linear_fp4(x, weight: NvfpTensor, out=None, out_dtype=None, stream=None):
+    """x [T][K] (bfloat16 or float16; rows may be strided) times the transpose of one 4-bit weight [N][K], as
+    quantize_nvfp4 and quantize_mxfp4 give it: [T][N] in x's type, or in float32 with out_dtype=torch.float32.
+
+    Made for the few tokens of a decode step: the weight is read once for every 64."""
+    where = "moe_linear_fp4"
+    codes, scales, ts = weight.codes, weight.scales, weight.ts
+    shape, rows = x.shape, codes.shape[-2:]
+    if len(shape) != 2 or len(rows) != 2 or len(scales.shape) < 2:
+        _refuse(where, "x is not [T][K] or the weight's codes are not [N][K / 2]")
+    T, K = shape
+    N = rows[0]
+    if (T | K | N) >> 31:
+        _too_large(where, T, K, N)
+    dev, dt = _device(x, where), x.dtype
+    index = dev.index
+    code = DTYPE_BF16 if dt is torch.bfloat16 else DTYPE_F16 if dt is torch.float16 else _refuse(where, f"{dt} rows; bfloat16 or float16 expected")
+    xp, xs = _want_rows(x, where, "x", shape, dt, index)
+    lead = codes.shape[:-2]
+    if lead != () and lead != (1,):
+        _refuse(where, f"codes {list(codes.shape)}; one weight expected")
+    wp = _want(codes, where, "codes", (*lead, N, K // 2), _U8, index)
+    fmt = WEIGHTS_MXFP4 if ts is None else WEIGHTS_NVFP4
+    sp = _want(scales, where, "scales", (*lead, N, K // (32 if ts is None else 16)), _U8, index)
+    tp = None
+    if ts is not None:
+        if ts.numel() != 1:
+            _refuse(where, f"tensor scale {list(ts.shape)}; one value expected")
+        tp = _want(ts, where, "tensor scale", ts.shape, _F32, index)
+    if x.requires_grad:
+        _followed(where)
+    if out is None:
+        out = _new((T, N), dt if out_dtype is None else out_dtype, dev, stream)
+    elif out_dtype is not None and out.dtype is not out_dtype:
+        _refuse(where, f"out {out.dtype}; {out_dtype} asked for")
+    to = out.dtype
+    if to is not dt and to is not _F32:
+        _refuse(where, f"out {to}; {dt} or float32 expected")
+    op = _want(out, where, "out", (T, N), to, index)
+    L = lib()
+    n = L.moe_linear_fp4_workspace(T, K, code)
+    handle = _raw_stream(index) if stream is None else _given(where, index, stream, x, codes, scales, ts, out)
+    call = L.moe_linear_fp4
+    if _devices != 1 and _elsewhere(index):
+        call = _there(index, call)
+    ws = torch.cuda.caching_allocator_alloc(n, index, handle) if n else None
+    try:
+        st = call(xp, xs, ctypes.byref(Nvfp4(wp, sp, tp)), fmt, T, N, K, code, DTYPE_F32 if to is _F32 else code, op, ws, n, handle)
     finally:
         if ws is not None:
             torch.cuda.caching_allocator_delete(ws)

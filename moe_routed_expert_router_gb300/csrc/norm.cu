@@ -12,7 +12,6 @@
 #include <math.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "rows.cuh"
 
@@ -452,23 +451,6 @@ RowShape row_shape(int n8, bool few, int two) {
 int warp_pieces(int n8) { return n8 <= 32 ? 1 : n8 <= 64 ? 2 : 4; }
 
 constexpr int kSms = 152;
-constexpr size_t kSmemSm = 227 * 1024;   // shared memory of an SM that its blocks share
-
-// The kernel's dynamic shared-memory limit, set once a device.
-template <auto Kernel> cudaError_t allow_smem() {
-    static std::mutex mu;
-    static bool done[kMaxDevices] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    std::lock_guard<std::mutex> lock(mu);
-    if (done[dev]) return cudaSuccess;
-    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemSm - 2048);
-    if (e == cudaSuccess) done[dev] = true;
-    return e;
-}
-
 template <int DT, int Q, bool kWarp>
 cudaError_t launch_norm_v(const NormArgs &a, int T, int threads, int v, cudaStream_t st) {
     const dim3 grid(kWarp ? blocks_of(T, kWarpRows) : T), block(kWarp ? 32 * kWarpRows : threads);

@@ -2,6 +2,8 @@
 // dispatch / combine kernels: eight values at a time, widened to fp32.
 #pragma once
 
+#include <mutex>
+
 #include "moe_internal.cuh"
 
 namespace moe {
@@ -200,6 +202,23 @@ __device__ __forceinline__ void column_sums(const float *part, int blocks, int H
         for (int k = 0; k < 8; ++k) sum += t[k][threadIdx.x];
         gw[blockIdx.x * 32 + threadIdx.x] = sum;
     }
+}
+
+constexpr size_t kSmemSm = 227 * 1024;   // shared memory of an SM that its blocks share
+
+// The kernel's dynamic shared-memory limit, set once a device.
+template <auto Kernel> cudaError_t allow_smem() {
+    static std::mutex mu;
+    static bool done[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (done[dev]) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemSm - 2048);
+    if (e == cudaSuccess) done[dev] = true;
+    return e;
 }
 
 // Blocks for n rows, `each` of them a block; n may be the largest int.
