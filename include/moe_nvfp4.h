@@ -514,6 +514,37 @@ moe_status moe_linear_fp4(const void *x, int64_t x_stride, const moe_nvfp4 *weig
                           int32_t N, int32_t K, int32_t dtype, int32_t out_dtype, void *out, void *workspace,
                           size_t workspace_bytes, void *stream);
 
+/* The whole mixture-of-experts layer of up to 16 tokens with experts that are not
+ * quantised, in two launches:
+ *   out[t] = round(base[t] + sum over j of topk_w[t][j] * FFN_{topk_ids[t][j]}(x_t) + FFN_shared(x_t))
+ * with the FFN of moe_forward, everything between x and out in fp32 (the SwiGLU
+ * output is not rounded).  Logits, top-k and weights are moe_route's, in the same
+ * order of sums, so both choose the same experts; an expert whose logit is NaN is
+ * chosen after all others.
+ *   x        [T][hidden] of `dtype` (moe_dtype), as the experts, base and out are
+ *   router_w [E][hidden] fp32 or bf16 words (moe_router_dtype); router_bias [E] fp32 or NULL
+ *   gate, up [E][inter][hidden], down [E][hidden][inter]
+ *   shared_* the shared expert's [shared_inter][hidden] and [hidden][shared_inter],
+ *            or NULL with shared_inter = 0
+ *   base     NULL, or [T][hidden] added to the sum (the residual stream)
+ *   out      [T][hidden]; may be base's or x's memory
+ *   topk_ids [T][k] int32, topk_w [T][k] fp32: written
+ *   workspace: moe_decode_layer_workspace bytes, 16-byte aligned, used during the
+ *            call only
+ * Sums are taken in a fixed order: equal inputs on the same device give equal
+ * bits.  The second launch waits inside for its own first half, for a second at
+ * most; if that ever runs out, out is NaN.
+ * T: 0 to 16 (0 is a no-op); hidden, inter, shared_inter: multiples of 8 up to
+ * 16384; E: 1 to 1024; k: 1 to min(E, 32).  x, router_w and the experts are
+ * 16-byte aligned, the other arrays to their element. */
+size_t moe_decode_layer_workspace(int32_t T, int32_t num_experts, int32_t inter, int32_t top_k, int32_t shared_inter);
+moe_status moe_decode_layer(const void *x, int32_t dtype, int32_t T, int32_t hidden, const void *router_w,
+                            int32_t router_dtype, const float *router_bias, int32_t num_experts, int32_t top_k,
+                            int32_t router, int32_t renormalize, const void *gate, const void *up, const void *down,
+                            int32_t inter, const void *shared_gate, const void *shared_up, const void *shared_down,
+                            int32_t shared_inter, const void *base, void *out, int32_t *topk_ids, float *topk_w,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
 /* Text of a status code (static storage). */
 const char *moe_status_string(moe_status s);
 

@@ -36,7 +36,7 @@ EXPORTS = ["moe_plan_create", "moe_plan_destroy", "moe_route", "moe_forward", "m
            "moe_rms_norm_backward_workspace_for",
            "moe_sorted_rows", "moe_sort_pairs", "moe_dispatch", "moe_combine", "moe_combine_backward",
            "moe_head_norm", "moe_head_norm_backward", "moe_head_norm_backward_workspace",
-           "moe_linear_fp4", "moe_linear_fp4_workspace"]
+           "moe_linear_fp4", "moe_linear_fp4_workspace", "moe_decode_layer", "moe_decode_layer_workspace"]
 FMT_E4M3, FMT_E2M1 = 0, 1
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 QUANT_NONE, QUANT_E4M3_128, QUANT_E4M3_ROW, QUANT_MXFP8 = 0, 1, 2, 3
@@ -107,6 +107,8 @@ def lib():
         L.moe_head_norm_backward_workspace.argtypes = [I32, I32, I32, I32, I32]
         L.moe_linear_fp4.argtypes = [P, I64, ctypes.POINTER(Nvfp4), I32, I32, I32, I32, I32, I32, P, P, SZ, P]
         L.moe_linear_fp4_workspace.argtypes = [I32, I32, I32]
+        L.moe_decode_layer.argtypes = [P, I32, I32, I32, P, I32, P, I32, I32, I32, I32, P, P, P, I32, P, P, P, I32, P, P, P, P, P, SZ, P]
+        L.moe_decode_layer_workspace.argtypes = [I32, I32, I32, I32, I32]
         L.moe_status_string.argtypes = [I32]
         L.moe_status_string.restype = ctypes.c_char_p
         L.moe_version.restype = ctypes.c_char_p
@@ -115,6 +117,7 @@ def lib():
                 getattr(L, n).restype = I32
         L.moe_rms_norm_backward_workspace.restype = L.moe_rms_norm_backward_workspace_for.restype = SZ
         L.moe_head_norm_backward_workspace.restype = L.moe_linear_fp4_workspace.restype = SZ
+        L.moe_decode_layer_workspace.restype = SZ
         L.moe_sorted_rows.restype = I64
         _lib = L
     return _lib
@@ -714,6 +717,74 @@ def linear_fp4(x, weight: NvfpTensor, out=None, out_dtype=None, stream=None):
     ws = torch.cuda.caching_allocator_alloc(n, index, handle) if n else None
     try:
         st = call(xp, xs, ctypes.byref(Nvfp4(wp, sp, tp)), fmt, T, N, K, code, DTYPE_F32 if to is _F32 else code, op, ws, n, handle)
+    finally:
+        if ws is not None:
+            torch.cuda.caching_allocator_delete(ws)
+    if st:
+        raise MoeError(st, where)
+    return out
+
+
+def _ffn(where, name, weights, lead, H, dtype, index):
+    """An expert set's gate, up and down: their addresses and the intermediate size."""
+    gate, up, down = weights
+    if len(gate.shape) != len(lead) + 2:
+        _refuse(where, f"{name}gate {list(gate.shape)}; {len(lead) + 2} dimensions expected")
+    I = gate.shape[-2]
+    return (_want(gate, where, name + "gate", (*lead, I, H), dtype, index), _want(up, where, name + "up", (*lead, I, H), dtype, index),
+            _want(down, where, name + "down", (*lead, H, I), dtype, index)), I
+
+
+def decode_layer(x, router_w, gate, up, down, top_k, router_bias=None, router=ROUTER_SOFTMAX, renormalize=True, shared=None, base=None,
+                 out=None, stream=None):
+    """The whole mixture-of-experts layer of a decode step's tokens, x [T][H] with T up to 16: router [E][H] (float32 or
+    bfloat16), gate and up [E][I][H] and down [E][H][I] in x's type, and where given the shared expert's (gate, up, down)
+    and base [T][H], which is added.
+
+    Returns {"out": [T][H], "topk_ids": [T][k] int32, "topk_w": [T][k] fp32}; the ids are Plan.route's.  out's "out" may
+    be x or base."""
+    where = "moe_decode_layer"
+    shape = x.shape
+    if len(shape) != 2 or len(gate.shape) != 3 or len(router_w.shape) != 2:
+        _refuse(where, "x is not [T][H], gate not [E][I][H] or router_w not [E][H]")
+    T, H = shape
+    E = gate.shape[0]
+    dev, dt, code = _device(x, where), x.dtype, _dtype(x, where)
+    index = dev.index
+    xp = _want(x, where, "x", shape, dt, index)
+    rt = router_w.dtype
+    if rt is not _F32 and rt is not torch.bfloat16:
+        _refuse(where, f"router_w {rt}; float32 or bfloat16 expected")
+    rp = _want(router_w, where, "router_w", (E, H), rt, index)
+    ep, I = _ffn(where, "", (gate, up, down), (E,), H, dt, index)
+    if (T | H | E | I | top_k) >> 31:
+        _too_large(where, T, H, E, I, top_k)
+    bp = None if router_bias is None else _want(router_bias, where, "router_bias", (E,), _F32, index)
+    sp, Is = (None, None, None), 0
+    if shared is not None:
+        sp, Is = _ffn(where, "shared ", shared, (), H, dt, index)
+        if Is == 0 or Is >> 31:
+            _refuse(where, f"a shared expert of {Is} features", ERR_UNSUPPORTED_SHAPE)
+    ap = None if base is None else _want(base, where, "base", shape, dt, index)
+    given = (x, router_w, gate, up, down, router_bias, base, *(shared or ()))
+    if torch.is_grad_enabled():
+        for t in given:
+            if t is not None and t.requires_grad:
+                _followed(where)
+    if out is None:
+        out = {"out": _new(shape, dt, dev, stream), "topk_ids": _new((T, top_k), _I32, dev, stream), "topk_w": _new((T, top_k), _F32, dev, stream)}
+    op = _want(out["out"], where, "out", shape, dt, index)
+    ip, wp = _want(out["topk_ids"], where, "topk_ids", (T, top_k), _I32, index), _want(out["topk_w"], where, "topk_w", (T, top_k), _F32, index)
+    L = lib()
+    n = L.moe_decode_layer_workspace(T, E, I, top_k, Is)
+    handle = _raw_stream(index) if stream is None else _given(where, index, stream, *given, out["out"], out["topk_ids"], out["topk_w"])
+    call = L.moe_decode_layer
+    if _devices != 1 and _elsewhere(index):
+        call = _there(index, call)
+    ws = torch.cuda.caching_allocator_alloc(n, index, handle) if n else None
+    try:
+        st = call(xp, code, T, H, rp, ROUTER_F32 if rt is _F32 else ROUTER_BF16, bp, E, top_k, router, int(bool(renormalize)), *ep, I, *sp, Is, ap,
+                  op, ip, wp, ws, n, handle)
     finally:
         if ws is not None:
             torch.cuda.caching_allocator_delete(ws)
