@@ -500,19 +500,16 @@ moe_status moe_head_norm_backward(const void *grad_q, int64_t grad_q_stride, con
  *   weight host struct: codes [N][K/2], scales [N][K/16] or [N][K/32],
  *          tensor_scale one fp32 (NVFP4; ignored for MXFP4)
  *   out    [T][N] of out_dtype: `dtype` or MOE_DTYPE_F32
- *   workspace: moe_linear_fp4_workspace bytes (0 for f16: NULL then), 16-byte
- *          aligned, used during the call only
  * W is not rounded (a value has at most six significant bits and the tensor
  * scale is applied to the sum); f16 rows are taken as they are, bf16 ones to
- * within 2^-32 of their largest finite magnitude.  A row that holds an infinity
- * or a NaN gives what fp32 arithmetic gives and leaves the other rows alone.
+ * within 2^-32 of the largest finite magnitude of each of their blocks of 256 (128
+ * for more than 16 tokens) values.  A row that holds an infinity or a NaN gives
+ * what fp32 arithmetic gives and leaves the other rows alone.
  * K: a multiple of 128 up to 65536; x_stride: a multiple of 8, at least K; T: up
- * to 2^20, made for up to 64 (every 64 tokens read the weight once).  T = 0 is a
+ * to 2^20, made for up to 64 (every 32 tokens read the weight once, the later ones from cache).  T = 0 is a
  * no-op. */
-size_t moe_linear_fp4_workspace(int32_t T, int32_t K, int32_t dtype);
 moe_status moe_linear_fp4(const void *x, int64_t x_stride, const moe_nvfp4 *weight, int32_t weight_format, int32_t T,
-                          int32_t N, int32_t K, int32_t dtype, int32_t out_dtype, void *out, void *workspace,
-                          size_t workspace_bytes, void *stream);
+                          int32_t N, int32_t K, int32_t dtype, int32_t out_dtype, void *out, void *stream);
 
 /* The whole mixture-of-experts layer of up to 16 tokens with experts that are not
  * quantised, in two launches:

@@ -10,14 +10,17 @@
 // shuffled.  f16 holds E2M1 * E4M3 exactly (six significant bits, 2^-10 to 2688);
 // E8M0 scales go past f16, so MXFP4 multiplies the fp32 sum of every 32 values.
 //
-// bf16 tokens become f16 in a launch of their own, each row times a power of two
-// that brings its largest magnitude to [2^7, 2^8): a bf16 value is exact in f16
+// bf16 tokens become f16, times a power of two that brings the largest finite
+// magnitude of a token's 256 values to [2^7, 2^8): a bf16 value is exact in f16
 // down to 2^-17, and what is smaller is off by at most 2^-25, that is 2^-32 of the
-// row's largest.  f16 tokens are used where they lie.
+// largest.  The power is taken back from the sum.
 //
-// A block takes 16 * MT rows of the weight; its warps share K in stages of 256
-// values, each with a cp.async ring of its own (no barriers between warps until
-// the sums of a tile are joined).  The ring runs on into the block's next tile.
+// One block an SM takes an even share of the weight's rows, so all SMs read
+// equally much.  Its warps share K in stages of 256 values: a warp holds a stage's
+// tokens in registers (turned into f16 there) and runs down the block's rows, 16 at
+// a time, with a cp.async ring of its own, so that neither tokens nor weights pass
+// between warps and no barrier stops the stream.  The warps' sums of a pass over
+// the rows are joined in shared memory in a fixed order.
 #include <algorithm>
 
 #include "rows.cuh"
@@ -26,28 +29,55 @@ namespace {
 
 using namespace moe;
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kStageK = 256;               // values of K a stage
-constexpr int kCodeBytes = kStageK / 2;    // a row's codes in a stage
-constexpr int kScaleBytes = 16;            // a row's scales in a stage (MXFP4 uses 8)
-constexpr int kRing = 4;
+// Values of K a stage: 256, and half of it where 32 tokens have to share the registers.
+template <int NT> constexpr int kStageK = NT >= 4 ? 128 : 256;
+constexpr int kScaleBytes = 16;            // a row's place for a stage's scales (MXFP4 uses half)
+constexpr int kCodePad = 16;               // behind a row's codes: eight rows' equal words lie in different banks
+constexpr int kRows = 16;                  // rows a tile (32: 53.1 us for 1 x 100003 x 4096 against 47.1, the ring too short beside the sums)
+// Warps of a block: what the tokens' registers leave room for.
+template <int NT> constexpr int kWarps = NT == 1 ? 16 : 12;
 constexpr int kSms = 152;
 constexpr int kMaxK = 1 << 16, kMaxTokens = 1 << 20;
+constexpr int kMaxRing = 6;
+constexpr size_t kSmem = kSmemSm - 1024;   // a block's
+
+// Bytes of a warp's stage of a tile.
+template <int NT> constexpr int kStageBytes = kRows * (kStageK<NT> / 2 + kCodePad + kScaleBytes);
 
 struct LinearArgs {
     const uint8_t *codes, *scales;
     const float *ts;                       // tensor scale or null
-    const __half *x;                       // [T] rows, x_stride apart
-    const float *x_scale;                  // [T] or null for 1
+    const void *x;                         // [T] rows, x_stride values apart
     int64_t x_stride;
     void *out;
-    int T, N, K, tiles, slices;            // tiles of rows; warps that share a tile's K
-    int dtype, early;                      // out's type; whether the weight may be read before the launch before has ended
+    int T, N, K, dtype;                    // out's type
+    int bf16;                              // x's type
+    int base, extra;                       // rows of a block: base, and one more in the first `extra` blocks
+    int passes, pass_rows, tile_rows;      // over a block's rows; rows a pass and a tile
+    int wk, wm, tiles;                     // warps that share K; groups of them, which share a pass's tiles; tiles a group
+    int ring;                              // stages of a warp's ring
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same from zero.
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// Two scales of a word each: E4M3 bytes (a, a, b, b) as f16 pairs (a, a) and (b, b); E8M0 bytes (a, b, ., .) as the
+// bf16 pair (a, b), exact: 2^-127 is one of its subnormals and byte 255 a NaN.
+__device__ __forceinline__ void scales_e4m3(uint32_t w, uint32_t &first, uint32_t &second) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(first), "=r"(second) : "r"(w));
+}
+__device__ __forceinline__ void scales_e8m0(uint32_t w, uint32_t &first, uint32_t &second) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.bf16x2.ue8m0x2 %0, l;\n\tcvt.rn.bf16x2.ue8m0x2 %1, h;\n\t}"
+        : "=r"(first), "=r"(second) : "r"(w));
 }
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -63,205 +93,307 @@ template <int B> __device__ __forceinline__ void copy_small(void *dst, const voi
 
 __device__ __forceinline__ uint32_t lds32(const uint8_t *p) { return *reinterpret_cast<const uint32_t *>(p); }
 
-// Places for a tile's sums: with two, the next tile's need not wait for the reading of the last one's.
-template <int MT, int NT> constexpr int join_buffers() { return MT * NT <= 4 ? 2 : 1; }
+// The power of two that brings values whose largest finite magnitude has exponent e to [2^7, 2^8), in two factors, and
+// what undoes it; e is -127 where all are subnormals or zeros.
+__device__ __forceinline__ int exponent_of(float amax) { return (int)(__float_as_uint(amax) >> 23) - 127; }
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }    // -126 to 127
+__device__ __forceinline__ float scale_up(int e) { return power_of_two(min(7 - e, 127)); }
+__device__ __forceinline__ float scale_more(int e) { return power_of_two(max(0, 7 - e - 127)); }
+__device__ __forceinline__ float scale_down(int e) { return power_of_two(max(e - 7, -126)) * power_of_two(min(0, e - 7 + 126)); }
 
-template <bool MX, int MT, int NT>
-__global__ void __launch_bounds__(kThreads) k_linear(LinearArgs a) {
-    constexpr int kRows = 16 * MT;
-    constexpr int kStage = kRows * (kCodeBytes + kScaleBytes), kBufs = join_buffers<MT, NT>();
+// Largest magnitude of bf16 values, NaNs aside: pairs, then the larger of the two.
+__device__ __forceinline__ uint32_t amax_pair(uint32_t m, uint32_t pair) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(pair & 0x7FFF7FFFu));
+    return r;
+}
+__device__ __forceinline__ uint32_t amax8(const uint4 &p, uint32_t m) { return amax_pair(amax_pair(m, p.x), amax_pair(amax_pair(amax_pair(0u, p.y), p.z), p.w)); }
+__device__ __forceinline__ float amax_of(uint32_t m) { return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u)); }
+// The same of the finite ones, where an infinity is among them.
+__device__ __noinline__ float finite_amax8(uint4 p, float m) {
+    const uint32_t u[4] = {p.x, p.y, p.z, p.w};
+    for (int i = 0; i < 8; ++i) {
+        const float v = fabsf(__uint_as_float(i & 1 ? u[i >> 1] & 0xFFFF0000u : u[i >> 1] << 16));
+        if (v < INFINITY) m = fmaxf(m, v);
+    }
+    return m;
+}
+__device__ __forceinline__ uint4 scaled8(const uint4 &piece, float up, float more) {
+    float v[8];
+    widen8<MOE_DTYPE_BF16>(Raw8<MOE_DTYPE_BF16>{piece}, v);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) mul2(v, i, up, up);
+    if (more != 1.0f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= more;
+    }
+    return narrow8<MOE_DTYPE_F16>(v).a;
+}
+
+// The warps that share a group's K wait for one another.
+__device__ __forceinline__ void group_sync(int group, int warps) {
+    if (warps == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(32 * warps) : "memory");
+}
+
+template <bool MX, int NT>
+__global__ void __launch_bounds__(32 * kWarps<NT>, 1) k_linear(LinearArgs a) {
+    constexpr int SK = kStageK<NT>;
+    constexpr int kUnits = SK / 32, kCodePitch = SK / 2 + kCodePad, kStage = kStageBytes<NT>;   // a unit: 32 values of K
     extern __shared__ __align__(16) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
-    const int wk = warp % a.slices, wm = warp / a.slices, groups = kWarps / a.slices;
-    const int token0 = blockIdx.y * (8 * NT);
-    uint8_t *ring = smem + warp * kRing * kStage;
-    float4 *red = reinterpret_cast<float4 *>(smem + kWarps * kRing * kStage);   // [kBufs][warp][MT][NT][lane]
-    const int stages = (a.K + kStageK - 1) / kStageK;
+    const int wm = warp / a.wk, wk = warp - wm * a.wk;
+    const int token0 = blockIdx.y * (8 * NT), tokens = min(8 * NT, a.T - token0);
+    const int row0 = (int)blockIdx.x * a.base + min((int)blockIdx.x, a.extra), row1 = row0 + a.base + ((int)blockIdx.x < a.extra);
+    uint8_t *ring = smem + warp * a.ring * kStage;
+    float4 *red = reinterpret_cast<float4 *>(smem + a.wk * a.wm * a.ring * kStage);   // [warp][tile][NT][lane]
+    const int stages = (a.K + SK - 1) / SK;
     const int64_t code_row = a.K / 2, scale_row = a.K / (MX ? 32 : 16);
 
-    // one stage of the rows of a tile, into slot `slot`
-    auto load = [&](int tile, int stage, int slot) {
-        const int n0 = (tile * groups + wm) * kRows, k0 = stage * kStageK;
-        uint8_t *to = ring + slot * kStage;
-#pragma unroll
-        for (int i = 0; i < 4 * MT; ++i) {
-            const int id = i * 32 + lane, row = id >> 3, u = id & 7;
-            const bool on = n0 + row < a.N && k0 + 32 * u < a.K;
-            copy16(to + row * kCodeBytes + ((u ^ (row & 7)) << 4), a.codes + (on ? (n0 + row) * code_row + (k0 >> 1) + 16 * u : 0), on);
-        }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int id = i * 32 + lane, row = id >> 1, half = id & 1;
-            const bool on = n0 + row < a.N && k0 + 128 * half < a.K;
-            constexpr int B = MX ? 4 : 8;
-            copy_small<B>(to + kRows * kCodeBytes + row * kScaleBytes + half * B,
-                          a.scales + (on ? (n0 + row) * scale_row + (int64_t)stage * (2 * B) + half * B : 0), on);
-        }
+    // rows of this warp's j-th tile in a pass: first and end
+    auto tile_rows = [&](int pass, int j, int &n0, int &n1) {
+        const int end = min(row0 + (pass + 1) * a.pass_rows, row1);
+        n0 = min(row0 + pass * a.pass_rows + (wm * a.tiles + j) * a.tile_rows, end);
+        n1 = min(n0 + a.tile_rows, end);
     };
-    // the stages of this warp, tile after tile
-    int lt = blockIdx.x, ls = wk, slot = 0;
-    auto load_next = [&](int to) {
-        while (lt < a.tiles && ls >= stages) {
-            lt += gridDim.x;
-            ls = wk;
-            if (wk >= stages) lt = a.tiles;
-        }
-        if (lt < a.tiles) {
-            load(lt, ls, to);
-            ls += a.slices;
+    // The stream of this warp: pass, stage, tile.  A lane copies one 16-byte unit of every kLoadRows-th row and a piece of
+    // a row's scales; rows that are not there are left out, for no result that is stored uses them.
+    constexpr int kLoadRows = 32 / kUnits, kScalePiece = MX ? 4 : 8, kPieces = kUnits / 4;
+    const int load_row = lane / kUnits, load_unit = lane % kUnits, scale_lane_row = lane / kPieces, scale_piece = lane % kPieces;
+    const bool last_half = a.K % SK != 0;  // of the last stage
+    const int64_t code_step = kLoadRows * code_row;
+    int lp = 0, ls = wk, lj = 0, fill = 0, left = 0;                         // rows left in the warp's share of the pass
+    const uint8_t *code_at = nullptr, *scale_at = nullptr;
+    auto stream_at = [&]() {               // the first tile of pass lp and stage ls
+        int n0, n1;
+        tile_rows(lp, 0, n0, n1);
+        left = min(row0 + (lp + 1) * a.pass_rows, row1) - n0;
+        code_at = a.codes + (n0 + load_row) * code_row + ls * (SK / 2) + 16 * load_unit;
+        scale_at = a.scales + (n0 + scale_lane_row) * scale_row + ls * (kPieces * kScalePiece) + scale_piece * kScalePiece;
+    };
+    auto load_next = [&]() {
+        if (lp < a.passes) {
+            uint8_t *to = ring + fill * kStage;
+            uint8_t *code_to = to + load_row * kCodePitch + 16 * load_unit;
+            uint8_t *scale_to = to + kRows * kCodePitch + scale_lane_row * kScaleBytes + scale_piece * kScalePiece;
+            const int here = min(left, a.tile_rows), rows = here - load_row, scale_rows = scale_lane_row < kRows ? here - scale_lane_row : 0;
+            if (last_half && ls == stages - 1) {                             // zeros behind K
+                const bool code_on = load_unit < kUnits / 2, scale_on = scale_piece == 0;
+#pragma unroll
+                for (int i = 0; i < kRows / kLoadRows; ++i)
+                    if (i * kLoadRows < rows) copy16(code_to + i * kLoadRows * kCodePitch, code_on ? code_at + i * code_step : a.codes, code_on);
+                if (scale_rows > 0) copy_small<kScalePiece>(scale_to, scale_on ? scale_at : a.scales, scale_on);
+            } else {
+                const uint8_t *at = code_at;
+#pragma unroll
+                for (int i = 0; i < kRows / kLoadRows; ++i, at += code_step)
+                    if (i * kLoadRows < rows) copy16(code_to + i * kLoadRows * kCodePitch, at, true);
+                if (scale_rows > 0) copy_small<kScalePiece>(scale_to, scale_at, true);
+            }
+            if (++lj < a.tiles) {
+                left -= a.tile_rows;
+                code_at += a.tile_rows * code_row;
+                scale_at += a.tile_rows * scale_row;
+            } else {
+                lj = 0;
+                ls += a.wk;
+                if (ls >= stages) {
+                    ls = wk;
+                    ++lp;
+                }
+                stream_at();
+            }
         }
         copy_commit();
+        if (++fill == a.ring) fill = 0;
     };
-    if (!a.early) pdl_wait();
-#pragma unroll
-    for (int i = 0; i < kRing - 1; ++i) load_next(i);
-    if (a.early) pdl_wait();
-    pdl_trigger();
+    auto wait_oldest = [&]() {             // all but the ring - 1 latest stages are there
+        switch (a.ring) {
+            case 2: copy_wait<1>(); break;
+            case 3: copy_wait<2>(); break;
+            case 4: copy_wait<3>(); break;
+            case 5: copy_wait<4>(); break;
+            default: copy_wait<kMaxRing - 1>(); break;
+        }
+        __syncwarp();
+    };
 
+    // A stage's tokens: unit u's values 8 t .. 8 t + 7 of token 8 n + g (a column without one takes the last: its sums are
+    // not stored), and the scales of the sums' columns 2 t and 2 t + 1.
+    uint4 x[NT][kUnits];
+    float undo[NT][2];
+    auto take_tokens = [&](int stage) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const uint16_t *row = static_cast<const uint16_t *>(a.x) + (token0 + min(8 * n + g, tokens - 1)) * a.x_stride + stage * SK + 8 * t;
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) x[n][u] = stage * SK + 32 * u < a.K ? ld16_shared(row + 32 * u) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            undo[n][0] = undo[n][1] = 1.0f;
+            if (a.bf16) {
+                uint32_t pairs = 0u;
+#pragma unroll
+                for (int u = 0; u < kUnits; ++u) pairs = amax8(x[n][u], pairs);
+                float m = amax_of(pairs);
+                if (m == INFINITY) {
+                    m = 0.0f;
+#pragma unroll
+                    for (int u = 0; u < kUnits; ++u) m = finite_amax8(x[n][u], m);
+                }
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                const int e = exponent_of(m);
+                const float up = scale_up(e), more = scale_more(e), down = scale_down(e);
+#pragma unroll
+                for (int u = 0; u < kUnits; ++u) x[n][u] = scaled8(x[n][u], up, more);
+                undo[n][0] = __shfl_sync(0xffffffffu, down, 8 * t);
+                undo[n][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+            }
+        }
+    };
+
+    stream_at();
+    pdl_wait();
+    for (int i = 0; i < a.ring - 1; ++i) load_next();
+    pdl_trigger();
+    take_tokens(wk);
     float ts = 1.0f;
     if (a.ts) ts = *a.ts;
-    int buf = 0;
-    for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
-        float acc[MT][NT][4] = {};
-        for (int stage = wk; stage < stages; stage += a.slices) {
-            load_next((slot + kRing - 1) % kRing);
-            copy_wait<kRing - 1>();
-            __syncwarp();
-            const uint8_t *from = ring + slot * kStage;
-            uint4 sc[MT][2];               // the stage's scales of rows g and g + 8
+    const uint32_t scale_bytes = t >> 1 ? 0x3311 : 0x2200;
+    float4 *mine = red + warp * a.tiles * (NT * 32) + lane;
+    const bool one_stage = wk + a.wk >= stages;
+    int slot = 0;
+    for (int pass = 0; pass < a.passes; ++pass) {
+        for (int stage = wk; stage < stages; stage += a.wk) {
+            if (!one_stage && (pass > 0 || stage > wk)) take_tokens(stage);
+            for (int j = 0; j < a.tiles; ++j) {
+                load_next();
+                wait_oldest();
+                const uint8_t *from = ring + slot * kStage;
+                if (++slot == a.ring) slot = 0;
+                float acc[NT][4] = {};
+                // the stage's scales of rows g and g + 8: per two units a word of E4M3 bytes, or a pair of bf16 values
+                uint32_t sc[2][kUnits / 2];
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+                for (int h = 0; h < 2; ++h) {
+                    const uint8_t *p = from + kRows * kCodePitch + (8 * h + g) * kScaleBytes;
+                    uint32_t raw[4];
+                    if constexpr (MX && kUnits == 4) raw[0] = *reinterpret_cast<const uint32_t *>(p);
+                    else if constexpr (MX || kUnits == 4) *reinterpret_cast<uint2 *>(raw) = *reinterpret_cast<const uint2 *>(p);
+                    else *reinterpret_cast<uint4 *>(raw) = *reinterpret_cast<const uint4 *>(p);
+                    if constexpr (MX) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    sc[m][h] = *reinterpret_cast<const uint4 *>(from + kRows * kCodeBytes + (16 * m + 8 * h + g) * kScaleBytes);
+                        for (int i = 0; i < kUnits / 4; ++i) scales_e8m0(raw[i], sc[h][2 * i], sc[h][2 * i + 1]);
+                    } else {
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int k = stage * kStageK + 32 * u + 8 * t;
-                uint4 xb[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int token = token0 + 8 * n + g;
-                    xb[n] = make_uint4(0, 0, 0, 0);
-                    if (token < a.T && k < a.K) xb[n] = ld16_shared(a.x + token * a.x_stride + k);
+                        for (int i = 0; i < kUnits / 2; ++i) sc[h][i] = raw[i];
+                    }
                 }
+                const uint8_t *codes = from + g * kCodePitch + 4 * t;
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    uint32_t w[2][4];
+                for (int p = 0; p < kUnits / 2; ++p) { // two units
+                    uint32_t w[2][2][4];               // [unit][row half]
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        e2m1x8_to_f16x8(lds32(from + (16 * m + 8 * h + g) * kCodeBytes + ((u ^ g) << 4) + 4 * t), w[h]);
-                        if constexpr (!MX) {
-                            // the scale of values 8 t .. 8 t + 7 of the unit: byte 2 u + (t >> 1), twice
-                            const uint32_t word = (&sc[m][h].x)[u >> 1];
-                            const uint32_t two = __byte_perm(word, 0, (t >> 1) * 0x11 + ((u & 1) ? 0x22 : 0));
-                            const uint32_t s = e4m3x2_to_f16x2(two & 0xFFFFu);
+                        uint32_t s[2];
+                        // the scale of values 8 t .. 8 t + 7 of a unit: byte t >> 1 of its two, twice
+                        if constexpr (!MX) scales_e4m3(__byte_perm(sc[h][p], 0, scale_bytes), s[0], s[1]);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) w[h][j] = hmul2(w[h][j], s);
-                        }
-                    }
+                        for (int v = 0; v < 2; ++v) {
+                            e2m1x8_to_f16x8(lds32(codes + 8 * h * kCodePitch + 16 * (2 * p + v)), w[v][h]);
+                            if constexpr (!MX) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if constexpr (MX) {
-                            float d[4] = {};
-                            mma16816(d, w[0][0], w[1][0], w[0][1], w[1][1], xb[n].x, xb[n].y);
-                            mma16816(d, w[0][2], w[1][2], w[0][3], w[1][3], xb[n].z, xb[n].w);
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const float s = e8m0_to_f32((&sc[m][h].x)[u >> 2] >> (8 * (u & 3)));
-                                acc[m][n][2 * h] = fmaf(d[2 * h], s, acc[m][n][2 * h]);
-                                acc[m][n][2 * h + 1] = fmaf(d[2 * h + 1], s, acc[m][n][2 * h + 1]);
+                                for (int i = 0; i < 4; ++i) w[v][h][i] = hmul2(w[v][h][i], s[v]);
                             }
-                        } else {
-                            mma16816(acc[m][n], w[0][0], w[1][0], w[0][1], w[1][1], xb[n].x, xb[n].y);
-                            mma16816(acc[m][n], w[0][2], w[1][2], w[0][3], w[1][3], xb[n].z, xb[n].w);
                         }
                     }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int v = 0; v < 2; ++v) {
+                            const uint4 &b = x[n][2 * p + v];
+                            if constexpr (MX) {
+                                float d[4];
+                                mma16816_zero(d, w[v][0][0], w[v][1][0], w[v][0][1], w[v][1][1], b.x, b.y);
+                                mma16816(d, w[v][0][2], w[v][1][2], w[v][0][3], w[v][1][3], b.z, b.w);
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const float s = __uint_as_float(v ? sc[h][p] & 0xFFFF0000u : sc[h][p] << 16);
+                                    acc[n][2 * h] = fmaf(d[2 * h], s, acc[n][2 * h]);
+                                    acc[n][2 * h + 1] = fmaf(d[2 * h + 1], s, acc[n][2 * h + 1]);
+                                }
+                            } else {
+                                mma16816(acc[n], w[v][0][0], w[v][1][0], w[v][0][1], w[v][1][1], b.x, b.y);
+                                mma16816(acc[n], w[v][0][2], w[v][1][2], w[v][0][3], w[v][1][3], b.z, b.w);
+                            }
+                        }
                 }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float4 *at = mine + (j * NT + n) * 32;
+                    float4 s = stage > wk ? *at : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    s.x = fmaf(acc[n][0], undo[n][0], s.x);
+                    s.y = fmaf(acc[n][1], undo[n][1], s.y);
+                    s.z = fmaf(acc[n][2], undo[n][0], s.z);
+                    s.w = fmaf(acc[n][3], undo[n][1], s.w);
+                    *at = s;
+                }
+                __syncwarp();
             }
-            __syncwarp();
-            slot = (slot + 1) % kRing;
         }
-        // join the slices' sums in order
-        float4 *mine = red + buf * (kWarps * MT * NT * 32);
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                mine[((warp * MT + m) * NT + n) * 32 + lane] = make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
-        __syncthreads();
-        const float *all = reinterpret_cast<const float *>(mine);
-        const int outs = groups * kRows * 8 * NT;
-        for (int i = threadIdx.x; i < outs; i += kThreads) {
-            const int row = i % kRows, j = i / kRows, tok = j % (8 * NT), grp = j / (8 * NT);
-            const int n = (tile * groups + grp) * kRows + row, token = token0 + tok;
-            if (n >= a.N || token >= a.T) continue;
-            const int from = ((((row >> 4) * NT + (tok >> 3)) * 32 + (row & 7) * 4 + ((tok & 7) >> 1)) << 2) + ((row >> 3) & 1) * 2 + (tok & 1);
+        // join the sums of the group's warps in order
+        group_sync(wm, a.wk);
+        const float *all = reinterpret_cast<const float *>(red + wm * a.wk * a.tiles * (NT * 32));
+        for (int i = wk * 32 + lane; i < a.tiles * kRows * tokens; i += 32 * a.wk) {
+            const int row = i % kRows, tok = i / kRows % tokens, j = i / kRows / tokens;
+            int n0, n1;
+            tile_rows(pass, j, n0, n1);
+            if (n0 + row >= n1) continue;
+            const float *p = all + ((j * NT + (tok >> 3)) * 32 + (row & 7) * 4 + ((tok & 7) >> 1)) * 4 + (row >> 3) * 2 + (tok & 1);
             float s = 0.0f;
-            for (int w = 0; w < a.slices; ++w) s += all[(grp * a.slices + w) * (MT * NT * 128) + from];
-            s = s * ts;
-            if (a.x_scale) s *= a.x_scale[token];
-            const int64_t at = (int64_t)token * a.N + n;
+#pragma unroll 4
+            for (int w = 0; w < a.wk; ++w) s += p[w * a.tiles * (NT * 128)];
+            s *= ts;
+            const int64_t at = (int64_t)(token0 + tok) * a.N + n0 + row;
             if (a.dtype == MOE_DTYPE_F32) static_cast<float *>(a.out)[at] = s;
             else if (a.dtype == MOE_DTYPE_BF16) static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(s);
             else static_cast<__half *>(a.out)[at] = __float2half_rn(s);
         }
-        if constexpr (kBufs == 1) __syncthreads();
-        else buf ^= 1;
+        if (pass + 1 < a.passes) group_sync(wm, a.wk);
     }
-}
-
-// bf16 rows as f16 times a power of two (see the top), and what undoes it.
-constexpr int kXThreads = 256;
-__global__ void __launch_bounds__(kXThreads) k_linear_x(const __nv_bfloat16 *x, int64_t stride, int K, __half *out, float *scale) {
-    __shared__ float top[kXThreads / 32];
-    const int64_t row = blockIdx.x;
-    pdl_wait();
-    pdl_trigger();
-    float amax = 0.0f;
-    for (int k = 8 * threadIdx.x; k < K; k += 8 * kXThreads) {
-        float v[8];
-        widen8<MOE_DTYPE_BF16>(load8_shared<MOE_DTYPE_BF16>(x + row * stride + k), v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, isfinite(v[i]) ? fabsf(v[i]) : 0.0f);
-    }
-    amax = warp_max(amax);
-    if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = amax;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kXThreads / 32; ++i) amax = fmaxf(amax, top[i]);
-    const int e = (int)(__float_as_uint(amax) >> 23) - 127;      // -127 for a row of subnormals or zeros
-    const float up = ldexpf(1.0f, min(7 - e, 127)), more = ldexpf(1.0f, max(0, 7 - e - 127));   // 2^(7 - e) in two factors
-    for (int k = 8 * threadIdx.x; k < K; k += 8 * kXThreads) {
-        float v[8];
-        widen8<MOE_DTYPE_BF16>(load8_shared<MOE_DTYPE_BF16>(x + row * stride + k), v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] * up * more;
-        store8<MOE_DTYPE_F16>(out + row * K + k, narrow8<MOE_DTYPE_F16>(v));
-    }
-    if (threadIdx.x == 0) scale[row] = ldexpf(1.0f, e - 7);
 }
 
 // ------------------------------------------------------------ host side
 
-template <bool MX, int MT, int NT> cudaError_t launch(LinearArgs a, cudaStream_t st) {
-    constexpr size_t smem = kWarps * (kRing * 16 * MT * (kCodeBytes + kScaleBytes) + join_buffers<MT, NT>() * MT * NT * 32 * sizeof(float4));
-    static_assert(smem <= kSmemSm - 2048);
-    const cudaError_t e = allow_smem<k_linear<MX, MT, NT>>();
+template <bool MX, int NT> cudaError_t launch(LinearArgs a, cudaStream_t st) {
+    const cudaError_t e = allow_smem<k_linear<MX, NT>>();
     if (e != cudaSuccess) return e;
-    const int stages = (a.K + kStageK - 1) / kStageK;
-    a.slices = stages >= 8 ? 8 : stages >= 4 ? 4 : stages >= 2 ? 2 : 1;
-    a.tiles = blocks_of(a.N, 16 * MT * (kWarps / a.slices));
-    constexpr int an_sm = (int)std::max<size_t>(1, std::min<size_t>(2, 227 * 1024 / (smem + 1024)));
-    const dim3 grid(std::min(a.tiles, kSms * an_sm), blocks_of(a.T, 8 * NT));
-    return launch_pdl(k_linear<MX, MT, NT>, grid, dim3(kThreads), smem, st, a);
+    constexpr size_t stage = kStageBytes<NT>, join = NT * 512;     // a tile's sums of a warp
+    constexpr int ring = 2;                                        // stages at least
+    const int stages = blocks_of(a.K, kStageK<NT>), groups = blocks_of(a.T, 8 * NT);
+    const int blocks = std::min(std::max(1, kSms / groups), a.N);
+    const int rows = blocks_of(a.N, blocks);
+    a.base = a.N / blocks;
+    a.extra = a.N % blocks;
+    a.wk = blocks_of(stages, blocks_of(stages, kWarps<NT>));           // no more warps than the longest share of K needs
+    a.wm = std::min(kWarps<NT> / a.wk, blocks_of(rows, kRows));
+    const int warps = a.wk * a.wm;
+    const int most = (int)((kSmem / warps - ring * stage) / join); // tiles of a warp in a pass
+    a.passes = blocks_of(rows, a.wm * most * kRows);
+    a.pass_rows = blocks_of(rows, a.passes);
+    a.tiles = blocks_of(a.pass_rows, a.wm * kRows);
+    a.tile_rows = blocks_of(a.pass_rows, a.wm * a.tiles);
+    a.ring = (int)std::min<size_t>(kMaxRing, (kSmem / warps - a.tiles * join) / stage);
+    return launch_pdl(k_linear<MX, NT>, dim3(blocks, groups), dim3(32 * warps), warps * (a.ring * stage + a.tiles * join), st, a);
 }
 
 template <bool MX> cudaError_t launch_format(const LinearArgs &a, cudaStream_t st) {
-    if (a.T <= 8) return launch<MX, 1, 1>(a, st);
-    if (a.T <= 16) return launch<MX, 2, 2>(a, st);
-    if (a.T <= 32) return launch<MX, 2, 4>(a, st);
-    return launch<MX, 2, 8>(a, st);
+    if (a.T <= 8) return launch<MX, 1>(a, st);
+    if (a.T <= 16) return launch<MX, 2>(a, st);
+    return launch<MX, 4>(a, st);
 }
 
 moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
@@ -270,14 +402,8 @@ moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_E
 
 extern "C" {
 
-size_t moe_linear_fp4_workspace(int32_t T, int32_t K, int32_t dtype) {
-    if (T < 1 || K < 1 || dtype != MOE_DTYPE_BF16) return 0;
-    return (size_t)T * K * sizeof(__half) + ((size_t)T * sizeof(float) + 15) / 16 * 16;
-}
-
 moe_status moe_linear_fp4(const void *x, int64_t x_stride, const moe_nvfp4 *weight, int32_t weight_format, int32_t T,
-                          int32_t N, int32_t K, int32_t dtype, int32_t out_dtype, void *out, void *workspace,
-                          size_t workspace_bytes, void *stream) {
+                          int32_t N, int32_t K, int32_t dtype, int32_t out_dtype, void *out, void *stream) {
     if (T < 0 || (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F16) || (out_dtype != dtype && out_dtype != MOE_DTYPE_F32) ||
         (weight_format != MOE_WEIGHTS_NVFP4 && weight_format != MOE_WEIGHTS_MXFP4) || !weight)
         return MOE_ERR_INVALID_ARG;
@@ -286,36 +412,22 @@ moe_status moe_linear_fp4(const void *x, int64_t x_stride, const moe_nvfp4 *weig
     if (T == 0) return MOE_OK;
     const bool mx = weight_format == MOE_WEIGHTS_MXFP4;
     if (!x || !out || !weight->codes || !weight->scales || (!mx && !weight->tensor_scale)) return MOE_ERR_INVALID_ARG;
-    const size_t need = moe_linear_fp4_workspace(T, K, dtype);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_INVALID_ARG;
     if (!aligned_to(x, 16) || !aligned_to(weight->codes, 16) || !aligned_to(weight->scales, 16) ||
-        !aligned_to(mx ? nullptr : weight->tensor_scale, 4) || !aligned_to(out, out_dtype == MOE_DTYPE_F32 ? 4 : 2) ||
-        !aligned_to(workspace, 16))
+        !aligned_to(mx ? nullptr : weight->tensor_scale, 4) || !aligned_to(out, out_dtype == MOE_DTYPE_F32 ? 4 : 2))
         return MOE_ERR_MISALIGNED;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     LinearArgs a{};
     a.codes = weight->codes;
     a.scales = weight->scales;
     a.ts = mx ? nullptr : weight->tensor_scale;
+    a.x = x;
+    a.x_stride = x_stride;
     a.out = out;
     a.T = T;
     a.N = N;
     a.K = K;
     a.dtype = out_dtype;
-    if (dtype == MOE_DTYPE_BF16) {
-        __half *x16 = static_cast<__half *>(workspace);
-        float *scale = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + (size_t)T * K * sizeof(__half));
-        const cudaError_t e = launch_pdl(k_linear_x, dim3(T), dim3(kXThreads), 0, s, static_cast<const __nv_bfloat16 *>(x), x_stride, (int)K,
-                                         x16, scale);
-        if (e != cudaSuccess) return MOE_ERR_CUDA;
-        a.x = x16;
-        a.x_scale = scale;
-        a.x_stride = K;
-        a.early = 1;                       // k_linear_x starts no dependents before all that came before it has ended
-    } else {
-        a.x = static_cast<const __half *>(x);
-        a.x_stride = x_stride;
-    }
+    a.bf16 = dtype == MOE_DTYPE_BF16;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
     return cuda_status(mx ? launch_format<true>(a, s) : launch_format<false>(a, s));
 }
 
