@@ -13,13 +13,21 @@
 // costs 4 packed FMAs of them, so the products are fp32 on the CUDA cores, exact
 // in every type, and h stays in fp32.
 //
+// The weights stream through a ring of 2 KB stages in shared memory that every warp
+// keeps for itself (four rows, 16 bytes a lane and row; a lane reads back only what
+// it copied, so nothing is waited for but the copies).  The ring runs from piece to
+// piece and on into the rows of down, which are on their way while the block waits
+// for the last of h.
+//
 // Every block chooses the experts itself (a microsecond, against a launch and its
-// gap).  Gate and up rows are handed out by a ticket counter in small pieces, so
-// the last piece is short and no block has to be resident for another's sake: a
+// gap).  Gate and up rows are handed out by a ticket counter, two features a piece,
+// so the last piece is short and no block has to be resident for another's sake: a
 // wait for the pieces is a wait for blocks that already run.  The rows of down are
-// split evenly beforehand; a block sums its rows over all experts, so nothing is
-// added through memory and equal inputs give equal bits.
+// split evenly beforehand; a block's warps share the experts and slices of their
+// widths and add over them in a fixed order, so nothing is added through memory and
+// equal inputs give equal bits.
 #include <algorithm>
+#include <type_traits>
 
 #include "rows.cuh"
 
@@ -31,7 +39,14 @@ constexpr int kSms = 152;
 constexpr int kMaxTokens = 16, kMaxPairs = kMaxTokens * kMaxTopK;
 constexpr int kMaxWidth = 16384;
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
-constexpr int kRows = 4;                   // weight rows a warp streams at once: two features' gate and up, or four rows of down
+constexpr int kRows = 4;                   // weight rows a stage: two features' gate and up, or four rows of down
+constexpr int kStage = kRows * 512;        // its bytes: 16 a lane and row
+constexpr int kMaxRing = 8;
+constexpr int kQueue = 16;                 // pieces between a warp's copies and its products, more than kMaxRing
+constexpr int kMostRows = 32;              // rows of down a block sums at once
+constexpr int kMostPairs = 4;              // tokens that share a pass over an expert's weights: what registers hold sums for
+constexpr size_t kSmem = kSmemSm - 2048;   // a block's
+constexpr size_t kMostX = 64 * 1024;       // tokens that are kept in shared memory
 
 struct LayerArgs {
     const void *x, *router;
@@ -45,11 +60,12 @@ struct LayerArgs {
     float *logits, *h;                     // [T][E]; [T * k][I], then [T][Is]
     int *count;                            // [0] pieces handed out, [1] pieces done
     int T, H, E, I, k, Is, kind, renorm;
+    int ring, pass_rows;                   // stages of a warp's ring; rows of down a block sums at once
 };
 
 // ------------------------------------------------------------ logits
 
-constexpr int kLogitThreads = 256;
+constexpr int kLogitThreads = 512;
 
 template <int RT> struct RouterWord { using T = float; };
 template <> struct RouterWord<MOE_ROUTER_BF16> { using T = __nv_bfloat16; };
@@ -95,10 +111,11 @@ __global__ void __launch_bounds__(kLogitThreads) k_layer_logits(LayerArgs a, int
 struct Routing {
     unsigned *mask;                        // [E] the tokens that chose an expert, a bit each
     int *first;                            // [E] its first pair
-    int *expert, *start;                   // the chosen experts in increasing order (E: the shared one) and their first pairs
+    int *expert, *start;                   // runs of up to kMostPairs pairs of one expert, experts increasing (E: the shared one):
+                                           // the expert and the first pair
     int *token;                            // [pairs] token of a pair
     float *weight;                         // [pairs]
-    int *n;                                // chosen experts, the shared one included
+    int *runs;                             // [0] of chosen experts, [1] with the shared one's
 };
 
 __host__ __device__ inline size_t routing_bytes(int E) { return sizeof(int) * (2 * (size_t)E + 4 * (kMaxPairs + kMaxTokens + 2) + 4); }
@@ -113,7 +130,7 @@ __device__ __forceinline__ Routing routing_at(uint8_t *smem, int E) {
     r.start = r.expert + P;
     r.token = r.start + P;
     r.weight = reinterpret_cast<float *>(r.token + P);
-    r.n = r.token + 2 * P;
+    r.runs = r.token + 2 * P;
     return r;
 }
 
@@ -189,36 +206,42 @@ __device__ void route(const LayerArgs &a, const Routing &r, uint8_t *scratch) {
         int n = 0, pairs = 0;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
             const int e = e0 + lane, c = e < a.E ? __popc(r.mask[e]) : 0;
-            const unsigned used = __ballot_sync(0xffffffffu, c > 0);
-            int sum = c;
+            const int own = (c + kMostPairs - 1) / kMostPairs << 16 | c;     // runs and pairs in one sum
+            int sum = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, sum, o);
                 if (lane >= o) sum += y;
             }
             if (c > 0) {
-                const int i = n + __popc(used & ((1u << lane) - 1u));
-                r.expert[i] = e;
-                r.start[i] = r.first[e] = pairs + sum - c;
+                const int before = sum - own, i = n + (before >> 16), p = pairs + (before & 0xFFFF);
+                r.first[e] = p;
+                for (int q = 0; q * kMostPairs < c; ++q) {
+                    r.expert[i + q] = e;
+                    r.start[i + q] = p + q * kMostPairs;
+                }
             }
-            n += __popc(used);
-            pairs += __shfl_sync(0xffffffffu, sum, 31);
+            sum = __shfl_sync(0xffffffffu, sum, 31);
+            n += sum >> 16;
+            pairs += sum & 0xFFFF;
         }
+        if (lane == 0) r.runs[0] = n;
         if (a.Is > 0) {
-            if (lane == 0) {
-                r.expert[n] = a.E;
-                r.start[n] = pairs;
+            const int more = (a.T + kMostPairs - 1) / kMostPairs;
+            if (lane < more) {
+                r.expert[n + lane] = a.E;
+                r.start[n + lane] = pairs + lane * kMostPairs;
             }
             if (lane < a.T) {
                 r.token[pairs + lane] = lane;
                 r.weight[pairs + lane] = 1.0f;
             }
-            ++n;
+            n += more;
             pairs += a.T;
         }
         if (lane == 0) {
             r.start[n] = pairs;
-            *r.n = n;
+            r.runs[1] = n;
         }
     }
     __syncthreads();
@@ -233,81 +256,24 @@ __device__ void route(const LayerArgs &a, const Routing &r, uint8_t *scratch) {
 
 // ------------------------------------------------------------ products
 
-// acc[i][j] = dot(row i, x_j) over the warp: every lane has every sum.  Eight values a lane and step, two steps' loads
-// ahead of their use.
-template <int DT, int XT, int M>
-__device__ __forceinline__ void dots(const typename RowType<DT>::T *const (&row)[kRows], const typename RowType<XT>::T *const (&x)[M], int K,
-                                     float (&sum)[kRows][M]) {
-    const int lane = threadIdx.x & 31;
-    float acc[kRows][M][2] = {};
-    for (int k = 8 * lane; k < K; k += 512) {
-        Raw8<DT> w[2][kRows];
-        const bool second = k + 256 < K;
+template <int N> constexpr int kLog = N <= 1 ? 0 : 1 + kLog<N / 2>;
+template <> constexpr int kLog<1> = 0;
+
+// Sums of v[0 .. N) over the warp: lane l returns that of v[l >> (5 - log2 N)].
+template <int N> __device__ __forceinline__ float spread_sum(float (&v)[N], int lane) {
+    int o = 16;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) w[0][i] = load8<DT>(row[i] + k);
+    for (int n = N / 2; n >= 1; n >>= 1, o >>= 1) {
+        const bool up = lane & o;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            w[1][i] = Raw8<DT>{};
-            if (second) w[1][i] = load8<DT>(row[i] + k + 256);
-        }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            if (s == 1 && !second) break;
-            float v[kRows][8];
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) widen8<DT>(w[s][i], v[i]);
-#pragma unroll
-            for (int j = 0; j < M; ++j) {
-                float y[8];
-                widen8<XT>(load8_shared<XT>(x[j] + k + 256 * s), y);
-#pragma unroll
-                for (int i = 0; i < kRows; ++i)
-#pragma unroll
-                    for (int q = 0; q < 8; q += 2) fma2(acc[i][j][0], acc[i][j][1], v[i][q], v[i][q + 1], y[q], y[q + 1]);
-            }
+        for (int i = 0; i < n; ++i) {
+            const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
         }
     }
 #pragma unroll
-    for (int i = 0; i < kRows; ++i)
-#pragma unroll
-        for (int j = 0; j < M; ++j) sum[i][j] = warp_sum(acc[i][j][0] + acc[i][j][1]);
-}
-
-// Gate, up and SwiGLU of features f and f + 1 of an expert for its pairs from p on, M at most, into their rows h.
-template <int DT, int M>
-__device__ void gate_up(const LayerArgs &a, const Routing &r, const typename RowType<DT>::T *const (&row)[kRows], int p, int end, int f, int I, float *h) {
-    using T = typename RowType<DT>::T;
-    const int lane = threadIdx.x & 31;
-    const T *x[M];
-#pragma unroll
-    for (int j = 0; j < M; ++j) x[j] = static_cast<const T *>(a.x) + r.token[min(p + j, end - 1)] * (int64_t)a.H;
-    float s[kRows][M];
-    dots<DT, DT, M>(row, x, a.H, s);
-#pragma unroll
-    for (int j = 0; j < M; ++j)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (lane == 2 * j + i && p + j < end) {
-                const float g = s[i][j];
-                h[(int64_t)j * I + f + i] = g / (1.0f + expf(-g)) * s[2 + i][j] * r.weight[p + j];
-            }
-}
-
-// Four rows of down of an expert for its pairs from p on, M at most, with rows h: added to the warp's sums [rows][kMaxTokens].
-template <int DT, int M>
-__device__ void down(const Routing &r, const typename RowType<DT>::T *const (&row)[kRows], const float *h, int p, int end, int I, float *sums) {
-    const int lane = threadIdx.x & 31;
-    const float *x[M];
-#pragma unroll
-    for (int j = 0; j < M; ++j) x[j] = h + (int64_t)min(j, end - 1 - p) * I;
-    float s[kRows][M];
-    dots<DT, MOE_DTYPE_F32, M>(row, x, I, s);
-#pragma unroll
-    for (int j = 0; j < M; ++j)
-#pragma unroll
-        for (int i = 0; i < kRows; ++i)
-            if (lane == j * kRows + i && p + j < end) sums[i * kMaxTokens + r.token[p + j]] += s[i][j];
-    __syncwarp();
+    for (int s = 16 >> kLog<N>; s >= 1; s >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], s);
+    return v[0];
 }
 
 template <int DT> __device__ __forceinline__ float load_f32(const void *p, int64_t i) { return as_f32(static_cast<const typename RowType<DT>::T *>(p)[i]); }
@@ -317,49 +283,220 @@ template <int DT> __device__ __forceinline__ void store_f32(void *p, int64_t i, 
     else static_cast<__half *>(p)[i] = __float2half_rn(v);
 }
 
-template <int DT>
+// The expert of a run.
+template <typename T> struct Expert {
+    const T *gate, *up, *down;
+    int I;
+};
+template <typename T> __device__ __forceinline__ Expert<T> expert_of(const LayerArgs &a, const Routing &r, int run) {
+    const int e = r.expert[run];
+    const bool shared = e == a.E;
+    const int64_t at = shared ? 0 : (int64_t)e * a.I * a.H;
+    return {static_cast<const T *>(shared ? a.sgate : a.gate) + at, static_cast<const T *>(shared ? a.sup : a.up) + at,
+            static_cast<const T *>(shared ? a.sdown : a.down) + at, shared ? a.Is : a.I};
+}
+
+// h's row of pair p.
+__device__ __forceinline__ float *h_row(const LayerArgs &a, int p) {
+    const int routed = a.T * a.k;
+    return p < routed ? a.h + (int64_t)p * a.I : a.h + (int64_t)routed * a.I + (int64_t)(p - routed) * a.Is;
+}
+
+// acc[i][j] += this lane's piece of the stage's row i times y_j, in fp32.
+template <int DT, int M>
+__device__ __forceinline__ void stage_dots(const uint8_t *stage, const float (&y)[M][kPieceValues<DT>], float (&acc)[kRows][M][2]) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        float w[kPieceValues<DT>];
+        widen_piece<DT>(*reinterpret_cast<const uint4 *>(stage + 512 * i), w);
+#pragma unroll
+        for (int j = 0; j < M; ++j)
+#pragma unroll
+            for (int q = 0; q < kPieceValues<DT>; q += 2) fma2(acc[i][j][0], acc[i][j][1], w[q], w[q + 1], y[j][q], y[j][q + 1]);
+    }
+}
+
+// Calls f with the least of 1, 2, 4 that is at least n, as a constant.
+template <typename F> __device__ __forceinline__ void by_pairs(int n, F f) {
+    if (n == 1) f(std::integral_constant<int, 1>{});
+    else if (n == 2) f(std::integral_constant<int, 2>{});
+    else f(std::integral_constant<int, 4>{});
+}
+
+template <int DT, bool kXShared>
 __global__ void __launch_bounds__(kThreads, 1) k_layer(LayerArgs a) {
     using T = typename RowType<DT>::T;
+    constexpr int V = kPieceValues<DT>, kStep = 32 * V;             // values of a stage's row: a lane's, all
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int ready;
+    __shared__ int queue[kWarps][kQueue];
     const Routing r = routing_at(smem, a.E);
-    uint8_t *rest = smem + (routing_bytes(a.E) + 15) / 16 * 16;
+    T *xs = reinterpret_cast<T *>(smem + (routing_bytes(a.E) + 15) / 16 * 16);
+    uint8_t *rest = reinterpret_cast<uint8_t *>(xs) + (kXShared ? sizeof(T) * a.T * a.H : 0);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float *sums = reinterpret_cast<float *>(rest) + warp * a.pass_rows * a.T;     // [rows of a pass][T], this warp's
+    uint8_t *ring = rest + sizeof(float) * kWarps * a.pass_rows * a.T + warp * a.ring * kStage;
     pdl_wait();
     pdl_trigger();
+    if constexpr (kXShared) {
+        for (int i = threadIdx.x; i < a.T * a.H / V; i += kThreads) copy16(xs + V * i, static_cast<const T *>(a.x) + V * i, true);
+        copy_commit();
+    }
     route(a, r, rest);
-    const int n = *r.n, routed = a.Is > 0 ? n - 1 : n;
-    const int each = a.I / 2, pieces = routed * each + a.Is / 2;
-    const int routed_pairs = a.T * a.k;
-    float *hs = a.h + (int64_t)routed_pairs * a.I;                  // the shared expert's rows
+    if constexpr (kXShared) {
+        copy_wait<0>();
+        __syncthreads();
+    }
+    const int routed = r.runs[0], runs = r.runs[1];
+    // pieces of two features, units of kStep values of an expert's width; the shared expert's lie behind the others
+    const int each = a.I / 2, shared_each = a.Is / 2, pieces = routed * each + (runs - routed) * shared_each;
+    const int slices = (a.I + kStep - 1) / kStep, shared_slices = (a.Is + kStep - 1) / kStep;
+    const int units = routed * slices + (runs - routed) * shared_slices;
+    auto split = [&](int i, int of, int of_shared, int &run, int &part) {
+        const bool shared = i >= routed * of;
+        const int k = shared ? i - routed * of : i, n = shared ? of_shared : of;
+        run = k / n;
+        part = k - run * n;
+        if (shared) run += routed;
+    };
+    const int row0 = (int)((int64_t)blockIdx.x * a.H / gridDim.x), row1 = (int)((int64_t)(blockIdx.x + 1) * a.H / gridDim.x);
 
-    // gate and up: two features a piece
-    for (;;) {
-        int piece = 0;
-        if (lane == 0) piece = atomicAdd(a.count, 1);
-        piece = __shfl_sync(0xffffffffu, piece, 0);
-        if (piece >= pieces) break;
-        const bool shared = piece >= routed * each;
-        const int c = shared ? routed : piece / each;
-        const int f = 2 * (shared ? piece - routed * each : piece - c * each);
-        const int I = shared ? a.Is : a.I;
-        const int64_t at = ((shared ? 0 : (int64_t)r.expert[c] * I) + f) * a.H;
-        const T *g = static_cast<const T *>(shared ? a.sgate : a.gate) + at, *u = static_cast<const T *>(shared ? a.sup : a.up) + at;
-        const T *const row[kRows] = {g, g + a.H, u, u + a.H};
-        const int end = r.start[c + 1];
-        for (int p = r.start[c]; p < end; p += 8) {
-            const int m = end - p;
-            float *h = shared ? hs + (int64_t)(p - routed_pairs) * I : a.h + (int64_t)p * I;
-            if (m == 1) gate_up<DT, 1>(a, r, row, p, end, f, I, h);
-            else if (m == 2) gate_up<DT, 2>(a, r, row, p, end, f, I, h);
-            else if (m <= 4) gate_up<DT, 4>(a, r, row, p, end, f, I, h);
-            else gate_up<DT, 8>(a, r, row, p, end, f, I, h);
+    // The warp's copies: pieces of gate and up as its tickets give them, kStep values a stage; then its units of down,
+    // pass after pass, kRows rows a stage.
+    int ticket = 0;                        // of lane 0: the next piece
+    if (lane == 0) ticket = atomicAdd(a.count, 1);
+    int head = 0, fill = 0, steps = 0;     // pieces queued; the next stage; stages left of the piece or unit
+    bool downs = false;
+    int unit = warp, base = row0, rows_left = 0, values = 0;        // values of a row from this lane's on
+    const T *p0 = nullptr, *p1 = nullptr;
+    int64_t row_step = a.H;
+    auto next_piece = [&]() {
+        const int piece = __shfl_sync(0xffffffffu, ticket, 0);
+        if (lane == 0) queue[warp][head % kQueue] = piece;
+        ++head;
+        if (piece >= pieces) {
+            downs = true;
+            return;
         }
+        if (lane == 0) ticket = atomicAdd(a.count, 1);
+        int run, part;
+        split(piece, each, shared_each, run, part);
+        const Expert<T> x = expert_of<T>(a, r, run);
+        p0 = x.gate + (int64_t)(2 * part) * a.H + V * lane;
+        p1 = x.up + (int64_t)(2 * part) * a.H + V * lane;
+        values = a.H - V * lane;
+        steps = (a.H + kStep - 1) / kStep;
+    };
+    auto next_unit = [&]() {
+        while (unit >= units && base < row1) {
+            unit = warp;
+            base += a.pass_rows;
+        }
+        if (base >= row1) return;
+        int run, part;
+        split(unit, slices, shared_slices, run, part);
+        const Expert<T> x = expert_of<T>(a, r, run);
+        p0 = x.down + (int64_t)base * x.I + part * kStep + V * lane;
+        values = x.I - part * kStep - V * lane;
+        row_step = x.I;
+        rows_left = min(a.pass_rows, row1 - base);
+        steps = (rows_left + kRows - 1) / kRows;
+        unit += kWarps;
+    };
+    auto copy_next = [&]() {
+        if (steps == 0 && !downs) next_piece();
+        if (steps == 0 && downs) next_unit();
+        if (steps > 0) {
+            uint8_t *to = ring + fill * kStage + 16 * lane;
+            if (!downs) {
+                if (values > 0) {
+                    copy16(to, p0, true);
+                    copy16(to + 512, p0 + a.H, true);
+                    copy16(to + 1024, p1, true);
+                    copy16(to + 1536, p1 + a.H, true);
+                }
+                p0 += kStep;
+                p1 += kStep;
+                values -= kStep;
+            } else {
+                if (values > 0) {
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i)
+                        if (i < rows_left) copy16(to + 512 * i, p0 + i * row_step, true);
+                }
+                p0 += kRows * row_step;
+                rows_left -= kRows;
+            }
+            --steps;
+        }
+        copy_commit();
+        if (++fill == a.ring) fill = 0;
+    };
+    int slot = 0;
+    auto next_stage = [&]() {              // the oldest stage: all but the ring - 1 latest copies are there
+        copy_next();
+        switch (a.ring) {
+            case 2: copy_wait<1>(); break;
+            case 3: copy_wait<2>(); break;
+            case 4: copy_wait<3>(); break;
+            case 5: copy_wait<4>(); break;
+            case 6: copy_wait<5>(); break;
+            case 7: copy_wait<6>(); break;
+            default: copy_wait<kMaxRing - 1>(); break;
+        }
+        const uint8_t *stage = ring + slot * kStage + 16 * lane;
+        if (++slot == a.ring) slot = 0;
+        return stage;
+    };
+    for (int i = 0; i < a.ring - 1; ++i) copy_next();
+
+    // gate and up: h of a piece's two features for the pairs of its run
+    int finished = 0;
+    for (int tail = 0;; ++tail) {
         __syncwarp();
-        if (lane == 0) {
-            __threadfence();
-            atomicAdd(a.count + 1, 1);
-        }
+        const int piece = queue[warp][tail % kQueue];               // queued: the copies are a stage ahead at least
+        if (piece >= pieces) break;
+        int run, part;
+        split(piece, each, shared_each, run, part);
+        const int p = r.start[run], end = r.start[run + 1];
+        by_pairs(end - p, [&](auto width) {
+            constexpr int M = decltype(width)::value;
+            const T *from[M];
+#pragma unroll
+            for (int j = 0; j < M; ++j)
+                from[j] = (kXShared ? xs : static_cast<const T *>(a.x)) + r.token[min(p + j, end - 1)] * (int64_t)a.H + V * lane;
+            float acc[kRows][M][2] = {};
+            for (int k = 0; k < a.H; k += kStep) {
+                const uint8_t *stage = next_stage();
+                if (k + V * lane >= a.H) continue;
+                float y[M][V];
+#pragma unroll
+                for (int j = 0; j < M; ++j) {
+                    uint4 q;
+                    if constexpr (kXShared) q = *reinterpret_cast<const uint4 *>(from[j] + k);
+                    else q = ld16_shared(from[j] + k);
+                    widen_piece<DT>(q, y[j]);
+                }
+                stage_dots<DT, M>(stage, y, acc);
+            }
+            float v[kRows * M];                                     // of a token: gate f, gate f + 1, up f, up f + 1
+#pragma unroll
+            for (int j = 0; j < M; ++j)
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) v[j * kRows + i] = acc[i][j][0] + acc[i][j][1];
+            constexpr int shift = 5 - kLog<kRows * M>;
+            const float own = spread_sum<kRows * M>(v, lane), up = __shfl_down_sync(0xffffffffu, own, 2 << shift);
+            const int j = lane >> shift >> 2, i = lane >> shift & 3;
+            if ((lane & ((1 << shift) - 1)) == 0 && i < 2 && p + j < end)
+                h_row(a, p + j)[2 * part + i] = own / (1.0f + expf(-own)) * up * r.weight[p + j];
+        });
+        ++finished;
+    }
+    // one release a warp: a fence behind every piece cost the stream a twentieth
+    __syncwarp();
+    if (lane == 0 && finished > 0) {
+        __threadfence();
+        atomicAdd(a.count + 1, finished);
     }
     if (threadIdx.x == 0) {
         const uint64_t t0 = now_ns();
@@ -369,45 +506,68 @@ __global__ void __launch_bounds__(kThreads, 1) k_layer(LayerArgs a) {
         } while (done < pieces && now_ns() - t0 < kWaitNs);
         ready = done >= pieces;
     }
-    // this block's rows of down
-    const int row0 = (int)((int64_t)blockIdx.x * a.H / gridDim.x), row1 = (int)((int64_t)(blockIdx.x + 1) * a.H / gridDim.x);
-    const int groups = (row1 - row0 + kRows - 1) / kRows;
-    float *sums = reinterpret_cast<float *>(rest) + warp * groups * kRows * kMaxTokens;
-    for (int i = lane; i < groups * kRows * kMaxTokens; i += 32) sums[i] = 0.0f;
     __syncthreads();
     const bool good = ready;
-    if (good) {
-        for (int u = warp; u < groups * n; u += kWarps) {
-            const int group = u / n, c = u - group * n;
-            const bool shared = c == routed;
-            const int I = shared ? a.Is : a.I;
-            const T *d = static_cast<const T *>(shared ? a.sdown : a.down) + (shared ? 0 : (int64_t)r.expert[c] * a.H * I);
-            const T *row[kRows];
+    if (!good) copy_wait<0>();
+
+    // this block's rows of down
+    for (int first = row0; first < row1; first += a.pass_rows) {
+        const int rows = min(a.pass_rows, row1 - first);
+        for (int i = lane; i < a.pass_rows * a.T; i += 32) sums[i] = 0.0f;
+        __syncwarp();
+        for (int u = warp; good && u < units; u += kWarps) {
+            int run, part;
+            split(u, slices, shared_slices, run, part);
+            const int I = r.expert[run] == a.E ? a.Is : a.I;
+            const int p = r.start[run], end = r.start[run + 1], k = part * kStep + V * lane;
+            by_pairs(end - p, [&](auto width) {
+                constexpr int M = decltype(width)::value;
+                float y[M][V] = {};
+                if (k < I) {
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) row[i] = d + (int64_t)min(row0 + group * kRows + i, row1 - 1) * I;
-            const int end = r.start[c + 1];
-            float *to = sums + group * kRows * kMaxTokens;
-            for (int p = r.start[c]; p < end; p += 8) {
-                const int m = end - p;
-                const float *h = shared ? hs + (int64_t)(p - routed_pairs) * I : a.h + (int64_t)p * I;
-                if (m == 1) down<DT, 1>(r, row, h, p, end, I, to);
-                else if (m == 2) down<DT, 2>(r, row, h, p, end, I, to);
-                else if (m <= 4) down<DT, 4>(r, row, h, p, end, I, to);
-                else down<DT, 8>(r, row, h, p, end, I, to);
-            }
+                    for (int j = 0; j < M; ++j) {
+                        const float *from = h_row(a, min(p + j, end - 1)) + k;
+#pragma unroll
+                        for (int q = 0; q < V; q += 4) {
+                            const uint4 v = ld16_shared(from + q);
+                            y[j][q] = __uint_as_float(v.x);
+                            y[j][q + 1] = __uint_as_float(v.y);
+                            y[j][q + 2] = __uint_as_float(v.z);
+                            y[j][q + 3] = __uint_as_float(v.w);
+                        }
+                    }
+                }
+                constexpr int shift = 5 - kLog<kRows * M>;
+                const int j = lane >> shift >> 2, i = lane >> shift & 3;
+                const bool writes = (lane & ((1 << shift) - 1)) == 0 && p + j < end;
+                float *to = sums + i * a.T + (writes ? r.token[p + j] : 0);
+                for (int row = 0; row < rows; row += kRows) {
+                    const uint8_t *stage = next_stage();
+                    float acc[kRows][M][2] = {};
+                    if (k < I) stage_dots<DT, M>(stage, y, acc);
+                    float v[kRows * M];
+#pragma unroll
+                    for (int b = 0; b < M; ++b)
+#pragma unroll
+                        for (int c = 0; c < kRows; ++c) v[b * kRows + c] = acc[c][b][0] + acc[c][b][1];
+                    const float own = spread_sum<kRows * M>(v, lane);
+                    if (writes) to[row * a.T] += own;
+                }
+            });
+            __syncwarp();
         }
-    }
-    __syncthreads();
-    const float *all = reinterpret_cast<const float *>(rest);
-    const int rows = row1 - row0;
-    for (int i = threadIdx.x; i < rows * a.T; i += kThreads) {
-        const int t = i / rows, row = i - t * rows;
-        float s = good ? 0.0f : __uint_as_float(0x7FC00000u);       // a wait that ran out
+        __syncthreads();
+        const float *all = reinterpret_cast<const float *>(rest);
+        for (int i = threadIdx.x; i < rows * a.T; i += kThreads) {
+            const int t = i / rows, row = i - t * rows;
+            float s = good ? 0.0f : __uint_as_float(0x7FC00000u);   // a wait that ran out
 #pragma unroll 4
-        for (int w = 0; w < kWarps; ++w) s += all[(w * groups * kRows + row) * kMaxTokens + t];
-        const int64_t at = (int64_t)t * a.H + row0 + row;
-        if (a.base) s += load_f32<DT>(a.base, at);
-        store_f32<DT>(a.out, at, s);
+            for (int w = 0; w < kWarps; ++w) s += all[(w * a.pass_rows + row) * a.T + t];
+            const int64_t at = (int64_t)t * a.H + first + row;
+            if (a.base) s += load_f32<DT>(a.base, at);
+            store_f32<DT>(a.out, at, s);
+        }
+        __syncthreads();
     }
 }
 
@@ -425,14 +585,20 @@ template <int DT, int RT> cudaError_t launch_logits(const LayerArgs &a, cudaStre
     return launch_pdl(k_layer_logits<DT, RT>, dim3(a.E), dim3(kLogitThreads), w + tokens * x, st, a, tokens);
 }
 
-template <int DT> cudaError_t launch_layer(const LayerArgs &a, int router_dtype, cudaStream_t st) {
-    cudaError_t e = router_dtype == MOE_ROUTER_F32 ? launch_logits<DT, MOE_ROUTER_F32>(a, st) : launch_logits<DT, MOE_ROUTER_BF16>(a, st);
-    if (e == cudaSuccess) e = allow_smem<k_layer<DT>>();
+template <int DT, bool kXShared> cudaError_t launch_weights(LayerArgs a, cudaStream_t st) {
+    const cudaError_t e = allow_smem<k_layer<DT, kXShared>>();
     if (e != cudaSuccess) return e;
-    const size_t choice = sizeof(float) * ((size_t)kWarps * a.E + 2 * kMaxPairs);
-    const int most = (a.H + kSms - 1) / kSms, groups = (most + kRows - 1) / kRows;
-    const size_t sums = sizeof(float) * (size_t)kWarps * groups * kRows * kMaxTokens;
-    return launch_pdl(k_layer<DT>, dim3(kSms), dim3(kThreads), (routing_bytes(a.E) + 15) / 16 * 16 + std::max(choice, sums), st, a);
+    a.pass_rows = std::min(kMostRows, (blocks_of(a.H, kSms) + kRows - 1) / kRows * kRows);
+    const size_t x = kXShared ? sizeof(typename RowType<DT>::T) * a.T * a.H : 0, front = (routing_bytes(a.E) + 15) / 16 * 16 + x;
+    const size_t sums = sizeof(float) * kWarps * a.pass_rows * a.T, choice = sizeof(float) * ((size_t)kWarps * a.E + 2 * kMaxPairs);
+    a.ring = (int)std::min<size_t>(kMaxRing, (kSmem - front - sums) / (kWarps * kStage));
+    return launch_pdl(k_layer<DT, kXShared>, dim3(kSms), dim3(kThreads), front + std::max(choice, sums + a.ring * kWarps * kStage), st, a);
+}
+
+template <int DT> cudaError_t launch_layer(const LayerArgs &a, int router_dtype, cudaStream_t st) {
+    const cudaError_t e = router_dtype == MOE_ROUTER_F32 ? launch_logits<DT, MOE_ROUTER_F32>(a, st) : launch_logits<DT, MOE_ROUTER_BF16>(a, st);
+    if (e != cudaSuccess) return e;
+    return (size_t)a.T * a.H * sizeof(typename RowType<DT>::T) <= kMostX ? launch_weights<DT, true>(a, st) : launch_weights<DT, false>(a, st);
 }
 
 bool good_width(int32_t v) { return v >= kChunk && v <= kMaxWidth && v % kChunk == 0; }
