@@ -15,9 +15,12 @@
 //
 // Layout: 2^lg lanes a row, 16 values a lane in two 8-value pieces of which the
 // second holds the partners of the first (half-split planes) or other whole
-// planes (interleaved ones), so a rotation needs no other lane's values.  A block
-// takes a tile of tokens of the queries or of the keys; the tile's sines and
-// cosines are computed once into shared memory and serve every head.
+// planes (interleaved ones), so a rotation needs no other lane's values: a lane has
+// eight planes (a, b) either way.  A block takes a tile of tokens of the queries or
+// of the keys; the tile's sines and cosines are computed once into shared memory.  A
+// group of lanes stays with one token and walks over its heads, so what a token and
+// a place in the row give (sines, cosines, weights, and in the forward pass their
+// products) is in registers and a row costs its own arithmetic only, in packed fp32.
 #include <algorithm>
 #include <cmath>
 
@@ -30,7 +33,7 @@ using namespace moe;
 constexpr int kThreads = 256;
 constexpr int kMaxHeads = 1024, kMaxDim = 512;
 constexpr int kSms = 152;
-constexpr int kAngleBytes = 32 * 1024;     // of a tile's sines and cosines
+constexpr int kEach = 8;                   // heads that share what a group of lanes has of a token
 
 // Queries or keys: rows [T][heads][D], `stride` values from token to token.
 struct HeadTensor {
@@ -38,8 +41,8 @@ struct HeadTensor {
     void *out;
     int64_t stride, out_stride, g_stride;
     float *sums;                           // backward: [blocks][D] partial sums of grad_w
-    int heads, inv;                        // inv = ceil(2^20 / heads): row / heads without a division
-    int tokens, tiles, blocks;             // tokens a tile, tiles, blocks that share them
+    int heads, split;                      // 2^split groups of lanes share a token's heads
+    int tokens, tiles, blocks;             // tokens a tile (2^-split of the groups), tiles, blocks that share them
 };
 
 struct HeadArgs {
@@ -48,19 +51,24 @@ struct HeadArgs {
     const uint64_t *turns;
     int T, D, R, lg;
     float eps, inv_d;
+    int ring_at;                           // backward: of the ring in shared memory, in floats
 };
 
 // What a thread is in its row.
 struct Lane {
-    int group, groups, c, p0, step;        // its row of a round, rows a round, its place, its pieces p0 and p0 + step
+    int groups, c, p0, step;               // rows of the block at once; its place in one, its pieces p0 and p0 + step
+    int token, head, heads;                // of the tile; its first head, and heads from one to the next
     bool on, turned;
 };
 
-__device__ __forceinline__ Lane lane_of(const HeadArgs &a) {
+__device__ __forceinline__ Lane lane_of(const HeadArgs &a, const HeadTensor &h) {
     Lane l;
+    const int group = threadIdx.x >> a.lg;
     l.c = threadIdx.x & ((1 << a.lg) - 1);
-    l.group = threadIdx.x >> a.lg;
     l.groups = blockDim.x >> a.lg;
+    l.heads = 1 << h.split;
+    l.head = group & (l.heads - 1);        // neighbouring groups have neighbouring heads
+    l.token = group >> h.split;
     const int planes = a.R >> 4;           // lanes whose two pieces turn
     l.on = l.c < (a.D >> 4);
     l.turned = l.c < planes;
@@ -75,24 +83,31 @@ template <bool kPairs>
 __device__ __forceinline__ void fill_angles(const HeadArgs &a, int t0, int n, float *cs) {
     const int half = a.R >> 1, planes = a.R >> 4;
     if (half == 0) return;
-    for (int j = threadIdx.x; j < n * half; j += blockDim.x) {
-        const int t = j / half, i = j - t * half;
+    int t = (int)threadIdx.x / half, i = (int)threadIdx.x - t * half;
+    const int more_t = (int)blockDim.x / half, more_i = (int)blockDim.x - more_t * half;
+    while (t < n) {
         const uint64_t turn = (uint64_t)(int64_t)a.pos[t0 + t] * a.turns[i];
         float s, c;
-        sincospif((float)(int64_t)turn * 0x1p-63f, &s, &c);      // 2^63 is half a turn
+        sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);              // 2^63 is half a turn
         const int at = kPairs ? i : (((i >> 2) & 1) * planes + (i >> 3)) * 4 + (i & 3);
         cs[t * half + at] = c;
         cs[(n + t) * half + at] = s;
+        t += more_t;
+        i += more_i;
+        if (i >= half) {
+            i -= half;
+            ++t;
+        }
     }
 }
 
 struct Angles { float c[8], s[8]; };
 
-__device__ __forceinline__ Angles angles_of(const HeadArgs &a, const Lane &l, const float *cs, int n, int t) {
+__device__ __forceinline__ Angles angles_of(const HeadArgs &a, const Lane &l, const float *cs, int n) {
     Angles r;
-    if (l.turned) {
+    if (l.turned && l.token < n) {
         const int half = a.R >> 1;
-        const float4 *c = reinterpret_cast<const float4 *>(cs + t * half), *s = reinterpret_cast<const float4 *>(cs + (n + t) * half);
+        const float4 *c = reinterpret_cast<const float4 *>(cs + l.token * half), *s = reinterpret_cast<const float4 *>(cs + (n + l.token) * half);
         *reinterpret_cast<float4 *>(r.c) = c[l.c];
         *reinterpret_cast<float4 *>(r.c + 4) = c[l.c + l.step];
         *reinterpret_cast<float4 *>(r.s) = s[l.c];
@@ -107,46 +122,80 @@ __device__ __forceinline__ Angles angles_of(const HeadArgs &a, const Lane &l, co
     return r;
 }
 
-// v[0..7] and v[8..15], the lane's pieces, turned by the angles (kBack: by their opposites).
-template <bool kPairs, bool kBack> __device__ __forceinline__ void turn16(float (&v)[16], const Angles &r) {
+// The lane's two pieces as eight planes (a, b), and back.
+template <int DT, bool kPairs> __device__ __forceinline__ void to_planes(const Raw8<DT> (&r)[2], float (&a)[8], float (&b)[8]) {
+    float v[2][8];
+    widen8<DT>(r[0], v[0]);
+    widen8<DT>(r[1], v[1]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        float &a = kPairs ? v[2 * i] : v[i], &b = kPairs ? v[2 * i + 1] : v[i + 8];
-        const float s = kBack ? -r.s[i] : r.s[i];
-        const float u = fmaf(a, r.c[i], -(b * s)), w = fmaf(b, r.c[i], a * s);
-        a = u;
-        b = w;
+        a[i] = kPairs ? v[i >> 2][2 * (i & 3)] : v[0][i];
+        b[i] = kPairs ? v[i >> 2][2 * (i & 3) + 1] : v[1][i];
     }
 }
-
-template <int DT> __device__ __forceinline__ void widen16(const Raw8<DT> (&r)[2], float (&v)[16]) {
-    float a[8];
+template <int DT, bool kPairs>
+__device__ __forceinline__ void store_planes(typename RowType<DT>::T *p, const Lane &l, const float (&a)[8], const float (&b)[8]) {
+    float v[2][8];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        widen8<DT>(r[h], a);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[8 * h + i] = a[i];
+    for (int i = 0; i < 8; ++i) {
+        (kPairs ? v[i >> 2][2 * (i & 3)] : v[0][i]) = a[i];
+        (kPairs ? v[i >> 2][2 * (i & 3) + 1] : v[1][i]) = b[i];
     }
+    store8<DT>(p + 8 * l.p0, narrow8<DT>(v[0]));
+    store8<DT>(p + 8 * (l.p0 + l.step), narrow8<DT>(v[1]));
 }
 
-template <int DT> __device__ __forceinline__ void store16(typename RowType<DT>::T *p, const Lane &l, const float (&v)[16]) {
+// r = x * y,  r += x * y  of eight values, two an instruction.
+__device__ __forceinline__ void mul8(float (&r)[8], const float (&x)[8], const float (&y)[8]) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float a[8];
+    for (int i = 0; i < 8; i += 2)
+        asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
+            "mov.b64 {%0, %1}, z;\n\t}"
+            : "=f"(r[i]), "=f"(r[i + 1]) : "f"(x[i]), "f"(x[i + 1]), "f"(y[i]), "f"(y[i + 1]));
+}
+__device__ __forceinline__ void mul8(float (&r)[8], const float (&x)[8], float y) {
+    const float all[8] = {y, y, y, y, y, y, y, y};
+    mul8(r, x, all);
+}
+__device__ __forceinline__ void fma8(float (&r)[8], const float (&x)[8], const float (&y)[8]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = v[8 * h + i];
-        store8<DT>(p + 8 * (l.p0 + h * l.step), narrow8<DT>(a));
-    }
+    for (int i = 0; i < 8; i += 2) fma2(r[i], r[i + 1], x[i], x[i + 1], y[i], y[i + 1]);
+}
+__device__ __forceinline__ void fma8(float (&r)[8], const float (&x)[8], float y) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) fma2(r[i], r[i + 1], x[i], x[i + 1], y, y);
+}
+// The sum of x * y added to two halves s.
+__device__ __forceinline__ void dot8(float (&s)[2], const float (&x)[8], const float (&y)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) fma2(s[0], s[1], x[i], x[i + 1], y[i], y[i + 1]);
+}
+__device__ __forceinline__ void scale8(float (&r)[8], float y) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) mul2(r, i, y, y);
 }
 
 template <int DT> __device__ __forceinline__ void fetch16(const typename RowType<DT>::T *p, const Lane &l, Raw8<DT> (&r)[2]) {
     r[0] = load8<DT>(p + 8 * l.p0);
     r[1] = load8<DT>(p + 8 * (l.p0 + l.step));
 }
+template <int DT> __device__ __forceinline__ void fetch_weight(const void *w, const Lane &l, Raw8<DT> (&r)[2]) {
+    using T = typename RowType<DT>::T;
+    r[0] = r[1] = Raw8<DT>{};
+    if (l.on) {
+        r[0] = load8_shared<DT>(static_cast<const T *>(w) + 8 * l.p0);
+        r[1] = load8_shared<DT>(static_cast<const T *>(w) + 8 * (l.p0 + l.step));
+    }
+}
 
-__device__ __forceinline__ float over_row(float v, int lg) {
+__device__ __forceinline__ void over_row(float &v, int lg) {
     for (int o = 1 << lg >> 1; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+}
+__device__ __forceinline__ void over_row(float &v, float &w, int lg) {
+    for (int o = 1 << lg >> 1; o >= 1; o >>= 1) {
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+        w += __shfl_xor_sync(0xffffffffu, w, o);
+    }
 }
 
 // U rows a thread at once, all loads ahead of their use.
@@ -156,135 +205,200 @@ __global__ void __launch_bounds__(kThreads) k_head_norm(HeadArgs a) {
     extern __shared__ __align__(16) float cs[];
     const bool key = (int)blockIdx.x >= a.q.blocks;
     const HeadTensor h = key ? a.k : a.q;
-    const int t0 = ((int)blockIdx.x - (key ? a.q.blocks : 0)) * h.tokens;
-    const int n = min(h.tokens, a.T - t0), rows = n * h.heads;
-    const Lane l = lane_of(a);
+    const int t0 = ((int)blockIdx.x - (key ? a.q.blocks : 0)) * h.tokens, n = min(h.tokens, a.T - t0);
+    const Lane l = lane_of(a, h);
+    const bool on = l.on && l.token < n;
     pdl_wait();
     pdl_trigger();
-    Raw8<DT> x[U][2], wr[2] = {};
-    auto at = [&](int r, int64_t stride, int &t) {
-        t = (int)((unsigned)(r * h.inv) >> 20);
-        return (int64_t)(t0 + t) * stride + (int64_t)(r - t * h.heads) * a.D;
-    };
-    auto fetch = [&](int base) {
+    Raw8<DT> x[U][2], wr[2];
+    const int64_t pitch = (int64_t)l.heads * a.D;                   // from a row to the thread's next one
+    const T *from = static_cast<const T *>(h.x) + (int64_t)(t0 + l.token) * h.stride + l.head * a.D;
+    T *to = static_cast<T *>(h.out) + (int64_t)(t0 + l.token) * h.out_stride + l.head * a.D;
+    int left = on ? (h.heads - l.head + l.heads - 1) >> h.split : 0;             // rows of this thread
+    auto fetch = [&]() {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = base + u * l.groups + l.group;
-            int t;
             x[u][0] = x[u][1] = Raw8<DT>{};
-            if (l.on && r < rows) fetch16<DT>(static_cast<const T *>(h.x) + at(r, h.stride, t), l, x[u]);
+            if (u < left) fetch16<DT>(from + u * pitch, l, x[u]);
         }
+        from += U * pitch;
     };
-    fetch(0);
-    if (l.on) {
-        wr[0] = load8_shared<DT>(static_cast<const T *>(h.w) + 8 * l.p0);
-        wr[1] = load8_shared<DT>(static_cast<const T *>(h.w) + 8 * (l.p0 + l.step));
-    }
+    fetch();
+    fetch_weight<DT>(h.w, l, wr);
     fill_angles<kPairs>(a, t0, n, cs);
     __syncthreads();
-    for (int base = 0; base < rows; base += U * l.groups) {
-        if (base > 0) fetch(base);
+    // a' = rstd (a (cos wa) - b (sin wb)),  b' = rstd (b (cos wb) + a (sin wa))
+    float wa[8], wb[8], ca[8], cb[8], sa[8], sb[8];
+    {
+        const Angles r = angles_of(a, l, cs, n);
+        to_planes<DT, kPairs>(wr, wa, wb);
+        mul8(ca, wa, r.c);
+        mul8(cb, wb, r.c);
+        mul8(sa, wa, r.s);
+        mul8(sb, wb, r.s);
+        scale8(sb, -1.0f);
+    }
+    for (int base = 0; base < h.heads; base += U * l.heads) {
+        if (base > 0) fetch();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = base + u * l.groups + l.group;
-            float v[16], w[16], sum = 0.0f;
-            widen16<DT>(x[u], v);
-            widen16<DT>(wr, w);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) sum = fmaf(v[i], v[i], sum);
-            sum = over_row(sum, a.lg);
-            if (l.on && r < rows) {
-                const float rstd = __frsqrt_rn(fmaf(sum, a.inv_d, a.eps));
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = v[i] * w[i] * rstd;
-                int t;
-                T *to = static_cast<T *>(h.out) + at(r, h.out_stride, t);
-                turn16<kPairs, false>(v, angles_of(a, l, cs, n, t));
-                store16<DT>(to, l, v);
+            float va[8], vb[8], ya[8], yb[8], sum[2] = {};
+            to_planes<DT, kPairs>(x[u], va, vb);
+            dot8(sum, va, va);
+            dot8(sum, vb, vb);
+            float mean = sum[0] + sum[1];
+            over_row(mean, a.lg);
+            if (u < left) {
+                const float rstd = rsqrtf(fmaf(mean, a.inv_d, a.eps));
+                mul8(ya, va, ca);
+                fma8(ya, vb, sb);
+                mul8(yb, vb, cb);
+                fma8(yb, va, sa);
+                scale8(ya, rstd);
+                scale8(yb, rstd);
+                store_planes<DT, kPairs>(to + u * pitch, l, ya, yb);
             }
         }
+        to += U * pitch;
+        left -= U;
     }
 }
 
 // Blocks walk over tiles; a thread holds its 16 values' part of grad_w in
-// registers until the end, so the order of the sums is fixed.
-template <int DT, bool kPairs, int U>
-__global__ void __launch_bounds__(kThreads) k_head_norm_backward(HeadArgs a) {
+// registers until the end, so the order of the sums is fixed.  Its rows come
+// through a ring in shared memory, kRing rows deep, that runs on into the next tile
+// (a thread reads what it copied itself: no barrier).  In registers, two rows at
+// once, 8192 x 36 heads of 128 took 57.6 us.
+template <int DT> constexpr int kRing = DT == MOE_DTYPE_F32 ? 3 : 4;
+template <int DT> constexpr int kRowWords = 2 * 2 * sizeof(Raw8<DT>) / 16;      // 16-byte words of x and grad a thread has of a row
+template <int DT> constexpr int kRingBytes = kRing<DT> * kRowWords<DT> * 16 * kThreads;
+
+template <int DT, bool kPairs>
+__global__ void __launch_bounds__(kThreads, 2) k_head_norm_backward(HeadArgs a) {
     using T = typename RowType<DT>::T;
-    extern __shared__ __align__(16) float cs[];
-    const bool key = (int)blockIdx.x >= a.q.blocks;
+    constexpr int W = kRowWords<DT> / 4;   // words a piece
+    extern __shared__ __align__(16) float cs[];                     // angles, in the end sums; then the ring
+    const bool key = (int)blockIdx.x < a.k.blocks;
     const HeadTensor h = key ? a.k : a.q;
-    const int block = (int)blockIdx.x - (key ? a.q.blocks : 0);
-    const Lane l = lane_of(a);
+    const int block = (int)blockIdx.x - (key ? 0 : a.k.blocks);
+    const Lane l = lane_of(a, h);
+    uint4 *ring = reinterpret_cast<uint4 *>(cs + a.ring_at) + threadIdx.x;
+    const int rounds = (h.heads + l.heads - 1) >> h.split;          // rows a thread and tile
+    const int64_t pitch = (int64_t)l.heads * a.D;                   // from a row to the thread's next one
     pdl_wait();
     pdl_trigger();
-    float w[16] = {}, gw[16] = {};
-    if (l.on) {
-        Raw8<DT> wr[2];
-        wr[0] = load8_shared<DT>(static_cast<const T *>(h.w) + 8 * l.p0);
-        wr[1] = load8_shared<DT>(static_cast<const T *>(h.w) + 8 * (l.p0 + l.step));
-        widen16<DT>(wr, w);
-    }
-    for (int tile = block; tile < h.tiles; tile += h.blocks) {
-        const int t0 = tile * h.tokens, n = min(h.tokens, a.T - t0), rows = n * h.heads;
-        Raw8<DT> x[U][2], g[U][2];
-        auto at = [&](int r, int64_t stride, int &t) {
-            t = (int)((unsigned)(r * h.inv) >> 20);
-            return (int64_t)(t0 + t) * stride + (int64_t)(r - t * h.heads) * a.D;
-        };
-        auto fetch = [&](int base) {
+    // the copies: row `cr` of tile `ct` next
+    int ct = block, cr = 0, fill = 0;
+    const T *cx = nullptr, *cg = nullptr;
+    auto tile_at = [&]() {
+        const int64_t t = (int64_t)ct * h.tokens + l.token;
+        cx = static_cast<const T *>(h.x) + t * h.stride + l.head * a.D + 8 * l.p0;
+        cg = static_cast<const T *>(h.g) + t * h.g_stride + l.head * a.D + 8 * l.p0;
+    };
+    auto copy_row = [&]() {
+        if (ct < h.tiles) {
+            if (l.on && l.token < min(h.tokens, a.T - ct * h.tokens) && l.head + cr * l.heads < h.heads) {
+                uint4 *to = ring + fill * (kRowWords<DT> * kThreads);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int r = base + u * l.groups + l.group;
-                int t;
-                x[u][0] = x[u][1] = g[u][0] = g[u][1] = Raw8<DT>{};
-                if (l.on && r < rows) {
-                    fetch16<DT>(static_cast<const T *>(h.x) + at(r, h.stride, t), l, x[u]);
-                    fetch16<DT>(static_cast<const T *>(h.g) + at(r, h.g_stride, t), l, g[u]);
+                for (int w = 0; w < W; ++w) {
+                    copy16(to + w * kThreads, cx + 4 * w, true);
+                    copy16(to + (W + w) * kThreads, cx + 8 * l.step + 4 * w, true);
+                    copy16(to + (2 * W + w) * kThreads, cg + 4 * w, true);
+                    copy16(to + (3 * W + w) * kThreads, cg + 8 * l.step + 4 * w, true);
                 }
             }
-        };
-        fetch(0);
+            cx += pitch;
+            cg += pitch;
+            if (++cr == rounds) {
+                cr = 0;
+                ct += h.blocks;
+                tile_at();
+            }
+        }
+        copy_commit();
+        if (++fill == kRing<DT>) fill = 0;
+    };
+    tile_at();
+#pragma unroll
+    for (int i = 0; i < kRing<DT> - 1; ++i) copy_row();
+    int slot = 0;
+    float wa[8], wb[8], gwa[8] = {}, gwb[8] = {};
+    {
+        Raw8<DT> wr[2];
+        fetch_weight<DT>(h.w, l, wr);
+        to_planes<DT, kPairs>(wr, wa, wb);
+    }
+    for (int tile = block; tile < h.tiles; tile += h.blocks) {
+        const int t0 = tile * h.tokens, n = min(h.tokens, a.T - t0);
+        const bool on = l.on && l.token < n;
+        T *to = static_cast<T *>(h.out) + (int64_t)(t0 + l.token) * h.out_stride + l.head * a.D;
         __syncthreads();                   // the tile before is done with the angles
         fill_angles<kPairs>(a, t0, n, cs);
         __syncthreads();
-        for (int base = 0; base < rows; base += U * l.groups) {
-            if (base > 0) fetch(base);
+        const Angles r = angles_of(a, l, cs, n);
+        float minus[8];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int r = base + u * l.groups + l.group;
-                const bool mine = l.on && r < rows;
-                int t = 0;
-                const int64_t to = mine ? at(r, h.out_stride, t) : 0;
-                float v[16], f[16], sum = 0.0f, dot = 0.0f;
-                widen16<DT>(x[u], v);
-                widen16<DT>(g[u], f);
-                turn16<kPairs, true>(f, angles_of(a, l, cs, n, t));
+        for (int i = 0; i < 8; ++i) minus[i] = -r.s[i];
+        for (int row = 0; row < rounds; ++row) {
+            copy_row();
+            copy_wait<kRing<DT> - 1>();
+            const uint4 *at = ring + slot * (kRowWords<DT> * kThreads);
+            if (++slot == kRing<DT>) slot = 0;
+            const bool mine = on && l.head + row * l.heads < h.heads;
+            Raw8<DT> x[2] = {}, g[2] = {};
+            if (mine) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    sum = fmaf(v[i], v[i], sum);
-                    dot = fmaf(f[i] * w[i], v[i], dot);
-                }
-                sum = over_row(sum, a.lg);
-                dot = over_row(dot, a.lg);
-                if (mine) {
-                    const float rstd = __frsqrt_rn(fmaf(sum, a.inv_d, a.eps));
-                    const float back = dot * rstd * a.inv_d * rstd;      // mean(g w n^) rstd
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        gw[i] = fmaf(f[i], v[i] * rstd, gw[i]);
-                        f[i] = rstd * fmaf(-v[i], back, f[i] * w[i]);
-                    }
-                    store16<DT>(static_cast<T *>(h.out) + to, l, f);
+                for (int i = 0; i < 2; ++i) {
+                    x[i] = take8<DT>(at + i * W * kThreads, kThreads);
+                    g[i] = take8<DT>(at + (2 + i) * W * kThreads, kThreads);
                 }
             }
+            float va[8], vb[8], fa[8], fb[8], sum[2] = {}, dot[2] = {};
+            {
+                float ga[8], gb[8];
+                to_planes<DT, kPairs>(g, ga, gb);
+                mul8(fa, ga, r.c);         // turned back
+                fma8(fa, gb, r.s);
+                mul8(fb, gb, r.c);
+                fma8(fb, ga, minus);
+            }
+            to_planes<DT, kPairs>(x, va, vb);
+            dot8(sum, va, va);
+            dot8(sum, vb, vb);
+            float pa[8], pb[8];            // g w
+            mul8(pa, fa, wa);
+            mul8(pb, fb, wb);
+            dot8(dot, pa, va);
+            dot8(dot, pb, vb);
+            float mean = sum[0] + sum[1], both = dot[0] + dot[1];
+            over_row(mean, both, a.lg);
+            if (mine) {
+                const float rstd = rsqrtf(fmaf(mean, a.inv_d, a.eps));
+                const float back = -(both * rstd * a.inv_d) * rstd;              // - rstd mean(g w n^)
+                float na[8], nb[8];
+                mul8(na, va, rstd);
+                mul8(nb, vb, rstd);
+                fma8(gwa, fa, na);
+                fma8(gwb, fb, nb);
+                scale8(pa, rstd);
+                scale8(pb, rstd);
+                fma8(pa, na, back);
+                fma8(pb, nb, back);
+                store_planes<DT, kPairs>(to, l, pa, pb);
+            }
+            to += pitch;
         }
     }
     // the groups' sums, [groups][D], added in order
     __syncthreads();
     if (l.on) {
+        float *mine = cs + (threadIdx.x >> a.lg) * a.D;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) cs[l.group * a.D + 8 * (l.p0 + (i >> 3) * l.step) + (i & 7)] = gw[i];
+        for (int i = 0; i < 8; ++i) {
+            const int pa = kPairs ? l.p0 + (i >> 2) * l.step : l.p0, pb = kPairs ? pa : l.p0 + l.step;
+            mine[8 * pa + (kPairs ? 2 * (i & 3) : i)] = gwa[i];
+            mine[8 * pb + (kPairs ? 2 * (i & 3) + 1 : i)] = gwb[i];
+        }
     }
     __syncthreads();
     for (int d = threadIdx.x; d < a.D; d += blockDim.x) {
@@ -311,46 +425,52 @@ int lanes_log(int D) {
     return lg;
 }
 
-// The tile of one tensor: about `rounds` rows a group of lanes, as many tokens
-// as their angles' shared memory allows, and no fewer tiles than fill the card
-// while there are tokens to share.
-void set_tiles(HeadTensor &t, int T, int heads, int R, int lg, int rounds) {
-    const int groups = kThreads >> lg;
+// The tile of one tensor: about `each` heads a group of lanes, fewer where tokens
+// are so few that their tiles would not fill the card.
+void set_tiles(HeadTensor &t, int T, int heads, int lg, int each) {
+    int groups_log = 0;
+    while ((kThreads >> lg) >> (groups_log + 1)) ++groups_log;
     t.heads = heads;
-    t.inv = (1 << 20) / heads + ((1 << 20) % heads != 0);
-    int n = std::max(1, groups * rounds / heads);
-    n = std::min(n, std::max(1, T / (2 * kSms)));
-    if (R > 0) n = std::min(n, std::max(1, kAngleBytes / (4 * R)));
-    t.tokens = n;
-    t.tiles = blocks_of(T, n);
+    t.split = 0;
+    while (t.split < groups_log && (heads > each << t.split || T >> (groups_log - t.split) < 2 * kSms) && 1 << t.split < heads) ++t.split;
+    t.tokens = 1 << (groups_log - t.split);
+    while (t.tokens > 1 && t.tokens > T) t.tokens /= 2;
+    t.tiles = blocks_of(T, t.tokens);
     t.blocks = t.tiles;
 }
 
 size_t angle_bytes(const HeadArgs &a) { return sizeof(float) * (size_t)a.R * std::max(a.q.tokens, a.k.tokens); }
 
-// Blocks of the backward pass: `most` in all, shared by rows.
-constexpr int kBackBlocks = 3 * kSms;
+// Blocks of the backward pass, shared by work: a row of a thread costs about three
+// times a sine and cosine (a tile of few heads has many tokens: shared by rows, 8192
+// tokens of 32 and 4 heads took 57 us, the keys' blocks half as long again).
+constexpr int kBackBlocks = 2 * kSms;
+int64_t work(const HeadTensor &t, int R) {
+    return (int64_t)t.tiles * (3 * blocks_of(t.heads, 1 << t.split) + (t.tokens * (R / 2) + kThreads - 1) / kThreads);
+}
 void set_backward(HeadArgs &a, int T, int q_heads, int k_heads) {
-    const int rounds = 4;
-    set_tiles(a.q, T, q_heads, a.R, a.lg, rounds);
-    set_tiles(a.k, T, k_heads, a.R, a.lg, rounds);
-    const int for_q = std::max(1, std::min(kBackBlocks - 1, (int)((int64_t)kBackBlocks * q_heads / (q_heads + k_heads))));
-    a.q.blocks = std::min(a.q.tiles, for_q);
-    a.k.blocks = std::min(a.k.tiles, kBackBlocks - for_q);
+    set_tiles(a.q, T, q_heads, a.lg, kEach);
+    set_tiles(a.k, T, k_heads, a.lg, kEach);
+    const int64_t for_q = kBackBlocks * work(a.q, a.R) / (work(a.q, a.R) + work(a.k, a.R));
+    const int q = (int)std::max<int64_t>(1, std::min<int64_t>(kBackBlocks - 1, for_q));
+    a.q.blocks = std::min(a.q.tiles, q);
+    a.k.blocks = std::min(a.k.tiles, kBackBlocks - q);
 }
 
 bool one_each(const HeadArgs &a) { return a.q.blocks == 1 && a.k.blocks == 1; }   // whose sums are the result
 
 template <int DT, bool kPairs> cudaError_t launch_forward(const HeadArgs &a, cudaStream_t st) {
-    constexpr int U = DT == MOE_DTYPE_F32 ? 2 : 4;
+    constexpr int U = DT == MOE_DTYPE_F32 ? 1 : 2;
     return launch_pdl(k_head_norm<DT, kPairs, U>, dim3(a.q.blocks + a.k.blocks), dim3(kThreads), angle_bytes(a), st, a);
 }
 
 template <int DT, bool kPairs> cudaError_t launch_backward(const HeadArgs &a, cudaStream_t st) {
-    constexpr int U = DT == MOE_DTYPE_F32 ? 1 : 2;
-    const size_t sums = sizeof(float) * (size_t)(kThreads >> a.lg) * a.D;
-    return launch_pdl(k_head_norm_backward<DT, kPairs, U>, dim3(a.q.blocks + a.k.blocks), dim3(kThreads),
-                      std::max(angle_bytes(a), sums), st, a);
+    const cudaError_t e = allow_smem<k_head_norm_backward<DT, kPairs>>();
+    if (e != cudaSuccess) return e;
+    const size_t sums = sizeof(float) * (size_t)(kThreads >> a.lg) * a.D, front = std::max(angle_bytes(a), sums);
+    HeadArgs b = a;
+    b.ring_at = (int)(front / sizeof(float));
+    return launch_pdl(k_head_norm_backward<DT, kPairs>, dim3(a.q.blocks + a.k.blocks), dim3(kThreads), front + kRingBytes<DT>, st, b);
 }
 
 moe_status check_heads(int32_t T, int32_t q_heads, int32_t k_heads, int32_t D, int32_t R, int32_t interleaved, int32_t dtype, float eps) {
@@ -394,9 +514,8 @@ moe_status moe_head_norm(const void *q, int64_t q_stride, const void *k, int64_t
     a.lg = lanes_log(D);
     a.eps = eps;
     a.inv_d = 1.0f / (float)D;
-    const int rounds = dtype == MOE_DTYPE_F32 ? 2 : 4;
-    set_tiles(a.q, T, q_heads, R, a.lg, rounds);
-    set_tiles(a.k, T, k_heads, R, a.lg, rounds);
+    set_tiles(a.q, T, q_heads, a.lg, kEach);
+    set_tiles(a.k, T, k_heads, a.lg, kEach);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (dtype) {
         case MOE_DTYPE_F32:
