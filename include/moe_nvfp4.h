@@ -499,7 +499,7 @@ moe_status moe_head_norm_backward(const void *grad_q, int64_t grad_q_stride, con
  *   x      [T] rows of K, x_stride values apart, of `dtype` (bf16 or f16)
  *   weight host struct: codes [N][K/2], scales [N][K/16] or [N][K/32],
  *          tensor_scale one fp32 (NVFP4; ignored for MXFP4)
- *   out    [T][N] of out_dtype: `dtype` or MOE_DTYPE_F32
+ *   out    [T][N] of out_dtype: `dtype` or MOE_DTYPE_F32; overlaps nothing else
  * W is not rounded (a value has at most six significant bits and the tensor
  * scale is applied to the sum); f16 rows are taken as they are, bf16 ones to
  * within 2^-32 of the largest finite magnitude of each of their blocks of 256 (128

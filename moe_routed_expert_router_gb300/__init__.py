@@ -570,6 +570,8 @@ def rotary_turns(dim, base=10000.0, frequencies=None, device="cuda"):
     where = "rotary_turns"
     if dim < 0 or dim % 16:
         _refuse(where, f"dim {dim}; a multiple of 16 expected", ERR_UNSUPPORTED_SHAPE)
+    if frequencies is None and not 0 < base < math.inf:
+        _refuse(where, f"base {base}")
     freqs = [base ** (-2.0 * i / dim) for i in range(dim // 2)] if frequencies is None else [float(f) for f in frequencies]
     if len(freqs) != dim // 2 or not all(math.isfinite(f) for f in freqs):
         _refuse(where, f"{len(freqs)} frequencies for dim {dim}; dim / 2 finite numbers expected")
@@ -624,7 +626,7 @@ def head_norm(q, k, q_weight, k_weight, positions, turns, interleaved=False, eps
     call = lib().moe_head_norm
     if _devices != 1 and _elsewhere(index):
         call = _there(index, call)
-    st = call(*given, *small, *sizes, int(interleaved), code, eps, op, os_, pp, ps, handle)
+    st = call(*given, *small, *sizes, int(bool(interleaved)), code, eps, op, os_, pp, ps, handle)
     if st:
         raise MoeError(st, where)
     return out
@@ -649,13 +651,14 @@ def head_norm_backward(grad_q, grad_k, q, k, q_weight, k_weight, positions, turn
     L = lib()
     n = L.moe_head_norm_backward_workspace(*sizes)
     handle = _raw_stream(index) if stream is None else _given(
-        where, index, stream, grad_q, grad_k, q, k, q_weight, k_weight, positions, turns, *out.values())
+        where, index, stream, grad_q, grad_k, q, k, q_weight, k_weight, positions, turns, out["grad_q"], out["grad_k"], out["grad_qw"],
+        out["grad_kw"])
     call = L.moe_head_norm_backward
     if _devices != 1 and _elsewhere(index):
         call = _there(index, call)
     ws = torch.cuda.caching_allocator_alloc(n, index, handle) if n else None
     try:
-        st = call(gp, gs, hp, hs, *given, *small, *sizes, int(interleaved), code, eps, *outs, ws, n, handle)
+        st = call(gp, gs, hp, hs, *given, *small, *sizes, int(bool(interleaved)), code, eps, *outs, ws, n, handle)
     finally:
         if ws is not None:
             torch.cuda.caching_allocator_delete(ws)
@@ -669,7 +672,8 @@ _U8 = torch.uint8
 
 def linear_fp4(x, weight: NvfpTensor, out=None, out_dtype=None, stream=None):
     """x [T][K] (bfloat16 or float16; rows may be strided) times the transpose of one 4-bit weight [N][K], as
-    quantize_nvfp4 and quantize_mxfp4 give it: [T][N] in x's type, or in float32 with out_dtype=torch.float32.
+    quantize_nvfp4 and quantize_mxfp4 give it: [T][N] in x's type, or in float32 with out_dtype=torch.float32.  out
+    overlaps nothing else.
 
     Made for the few tokens of a decode step: every 32 of them read the weight."""
     where = "moe_linear_fp4"
@@ -747,6 +751,8 @@ def decode_layer(x, router_w, gate, up, down, top_k, router_bias=None, router=RO
     if rt is not _F32 and rt is not torch.bfloat16:
         _refuse(where, f"router_w {rt}; float32 or bfloat16 expected")
     rp = _want(router_w, where, "router_w", (E, H), rt, index)
+    if router != ROUTER_SOFTMAX and router != ROUTER_SIGMOID:
+        _refuse(where, f"router {router}")
     ep, I = _ffn(where, "", (gate, up, down), (E,), H, dt, index)
     if (T | H | E | I | top_k) >> 31:
         _too_large(where, T, H, E, I, top_k)
