@@ -21,6 +21,8 @@
 // a time, with a cp.async ring of its own, so that neither tokens nor weights pass
 // between warps and no barrier stops the stream.  The warps' sums of a pass over
 // the rows are joined in shared memory in a fixed order.
+#include <limits.h>
+
 #include <algorithm>
 
 #include "rows.cuh"
@@ -140,6 +142,7 @@ template <bool MX, int NT>
 __global__ void __launch_bounds__(32 * kWarps<NT>, 1) k_linear(LinearArgs a) {
     constexpr int SK = kStageK<NT>;
     constexpr int kUnits = SK / 32, kCodePitch = SK / 2 + kCodePad, kStage = kStageBytes<NT>;   // a unit: 32 values of K
+    constexpr int kChains = MX || NT == 4 ? 1 : 2;                  // of dependent MMAs a token group (MXFP4's are two long)
     extern __shared__ __align__(16) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -274,7 +277,7 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) k_linear(LinearArgs a) {
                 wait_oldest();
                 const uint8_t *from = ring + slot * kStage;
                 if (++slot == a.ring) slot = 0;
-                float acc[NT][4] = {};
+                float acc[NT][kChains][4] = {};
                 // the stage's scales of rows g and g + 8: per two units a word of E4M3 bytes, or a pair of bf16 values
                 uint32_t sc[2][kUnits / 2];
 #pragma unroll
@@ -322,12 +325,12 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) k_linear(LinearArgs a) {
 #pragma unroll
                                 for (int h = 0; h < 2; ++h) {
                                     const float s = __uint_as_float(v ? sc[h][p] & 0xFFFF0000u : sc[h][p] << 16);
-                                    acc[n][2 * h] = fmaf(d[2 * h], s, acc[n][2 * h]);
-                                    acc[n][2 * h + 1] = fmaf(d[2 * h + 1], s, acc[n][2 * h + 1]);
+                                    acc[n][0][2 * h] = fmaf(d[2 * h], s, acc[n][0][2 * h]);
+                                    acc[n][0][2 * h + 1] = fmaf(d[2 * h + 1], s, acc[n][0][2 * h + 1]);
                                 }
                             } else {
-                                mma16816(acc[n], w[v][0][0], w[v][1][0], w[v][0][1], w[v][1][1], b.x, b.y);
-                                mma16816(acc[n], w[v][0][2], w[v][1][2], w[v][0][3], w[v][1][3], b.z, b.w);
+                                mma16816(acc[n][v % kChains], w[v][0][0], w[v][1][0], w[v][0][1], w[v][1][1], b.x, b.y);
+                                mma16816(acc[n][v % kChains], w[v][0][2], w[v][1][2], w[v][0][3], w[v][1][3], b.z, b.w);
                             }
                         }
                 }
@@ -335,10 +338,14 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) k_linear(LinearArgs a) {
                 for (int n = 0; n < NT; ++n) {
                     float4 *at = mine + (j * NT + n) * 32;
                     float4 s = stage > wk ? *at : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    s.x = fmaf(acc[n][0], undo[n][0], s.x);
-                    s.y = fmaf(acc[n][1], undo[n][1], s.y);
-                    s.z = fmaf(acc[n][2], undo[n][0], s.z);
-                    s.w = fmaf(acc[n][3], undo[n][1], s.w);
+#pragma unroll
+                    for (int c = 1; c < kChains; ++c)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[n][0][i] += acc[n][c][i];
+                    s.x = fmaf(acc[n][0][0], undo[n][0], s.x);
+                    s.y = fmaf(acc[n][0][1], undo[n][1], s.y);
+                    s.z = fmaf(acc[n][0][2], undo[n][0], s.z);
+                    s.w = fmaf(acc[n][0][3], undo[n][1], s.w);
                     *at = s;
                 }
                 __syncwarp();
@@ -378,8 +385,17 @@ template <bool MX, int NT> cudaError_t launch(LinearArgs a, cudaStream_t st) {
     const int rows = blocks_of(a.N, blocks);
     a.base = a.N / blocks;
     a.extra = a.N % blocks;
-    a.wk = blocks_of(stages, blocks_of(stages, kWarps<NT>));           // no more warps than the longest share of K needs
-    a.wm = std::min(kWarps<NT> / a.wk, blocks_of(rows, kRows));
+    // the split with the shortest longest share: stages, each taking its tokens (about three tiles of work) and its tiles
+    const int all = blocks_of(rows, kRows);
+    int best = INT_MAX;
+    for (int wk = std::min(stages, kWarps<NT>); wk >= 1; --wk) {
+        const int wm = std::min(kWarps<NT> / wk, all), cost = blocks_of(stages, wk) * (3 + blocks_of(all, wm));
+        if (cost < best) {
+            best = cost;
+            a.wk = wk;
+            a.wm = wm;
+        }
+    }
     const int warps = a.wk * a.wm;
     const int most = (int)((kSmem / warps - ring * stage) / join); // tiles of a warp in a pass
     a.passes = blocks_of(rows, a.wm * most * kRows);
