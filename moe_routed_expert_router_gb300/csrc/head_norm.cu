@@ -13,16 +13,18 @@
 // exactly and what is left rounds to fp32 once (an error of 1e-7 radians at any
 // position; an fp32 product would be off by 0.06 at position 10^6).
 //
-// Layout: 2^lg lanes a row, 16 values a lane in two 8-value pieces of which the
-// second holds the partners of the first (half-split planes) or other whole
-// planes (interleaved ones), so a rotation needs no other lane's values: a lane has
-// eight planes (a, b) either way.  A block takes a tile of tokens of the queries or
+// Layout: 2^lg lanes a row, 16 values a lane in 16-byte words (two of 16-bit values,
+// four of fp32 ones) a step apart, so that neighbouring lanes touch neighbouring
+// words and the second half of a lane's words holds the partners of the first
+// (half-split planes) or every word whole planes (interleaved ones): a rotation needs
+// no other lane's values, and a lane has eight planes (a, b) either way.  A block takes a tile of tokens of the queries or
 // of the keys; the tile's sines and cosines are computed once into shared memory.  A
 // group of lanes stays with one token and walks over its heads, so what a token and
 // a place in the row give (sines, cosines, weights, and in the forward pass their
 // products) is in registers and a row costs its own arithmetic only, in packed fp32.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "rows.cuh"
 
@@ -56,12 +58,17 @@ struct HeadArgs {
 
 // What a thread is in its row.
 struct Lane {
-    int groups, c, p0, step;               // rows of the block at once; its place in one, its pieces p0 and p0 + step
+    int groups, c, p0, step;               // rows of the block at once; its place in one, its words p0, p0 + step, ..
     int token, head, heads;                // of the tile; its first head, and heads from one to the next
     bool on, turned;
 };
 
-__device__ __forceinline__ Lane lane_of(const HeadArgs &a, const HeadTensor &h) {
+// A lane's words of a row, and values a word.
+template <int DT> constexpr int kWords = DT == MOE_DTYPE_F32 ? 4 : 2;
+template <int DT> struct Words { uint4 w[kWords<DT>]; };
+
+
+template <int DT> __device__ __forceinline__ Lane lane_of(const HeadArgs &a, const HeadTensor &h) {
     Lane l;
     const int group = threadIdx.x >> a.lg;
     l.c = threadIdx.x & ((1 << a.lg) - 1);
@@ -69,17 +76,18 @@ __device__ __forceinline__ Lane lane_of(const HeadArgs &a, const HeadTensor &h) 
     l.heads = 1 << h.split;
     l.head = group & (l.heads - 1);        // neighbouring groups have neighbouring heads
     l.token = group >> h.split;
-    const int planes = a.R >> 4;           // lanes whose two pieces turn
+    const int planes = a.R >> 4;           // lanes whose words turn
     l.on = l.c < (a.D >> 4);
     l.turned = l.c < planes;
-    l.p0 = l.turned ? l.c : l.c + planes;
+    l.p0 = l.turned ? l.c : l.c - planes + a.R / kPieceValues<DT>;
     l.step = l.turned ? planes : (a.D - a.R) >> 4;
     return l;
 }
 
-// Sines and cosines of `n` tokens from t0 on: cos [n][R / 2], then sin.  The
-// angles of a lane's pieces lie at 16-byte places c and c + R / 16 of a token.
-template <bool kPairs>
+// Sines and cosines of `n` tokens from t0 on: cos [n][R / 2], then sin, in the
+// planes' order but for half-split planes of 16-bit values, whose lane c has planes
+// 8 c .. 8 c + 7: these lie at 16-byte places c and c + R / 16 as well.
+template <int DT, bool kPairs>
 __device__ __forceinline__ void fill_angles(const HeadArgs &a, int t0, int n, float *cs) {
     const int half = a.R >> 1, planes = a.R >> 4;
     if (half == 0) return;
@@ -89,7 +97,7 @@ __device__ __forceinline__ void fill_angles(const HeadArgs &a, int t0, int n, fl
         const uint64_t turn = (uint64_t)(int64_t)a.pos[t0 + t] * a.turns[i];
         float s, c;
         sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);              // 2^63 is half a turn
-        const int at = kPairs ? i : (((i >> 2) & 1) * planes + (i >> 3)) * 4 + (i & 3);
+        const int at = kPairs || DT == MOE_DTYPE_F32 ? i : (((i >> 2) & 1) * planes + (i >> 3)) * 4 + (i & 3);
         cs[t * half + at] = c;
         cs[(n + t) * half + at] = s;
         t += more_t;
@@ -103,15 +111,18 @@ __device__ __forceinline__ void fill_angles(const HeadArgs &a, int t0, int n, fl
 
 struct Angles { float c[8], s[8]; };
 
-__device__ __forceinline__ Angles angles_of(const HeadArgs &a, const Lane &l, const float *cs, int n) {
+template <int DT, bool kPairs> __device__ __forceinline__ Angles angles_of(const HeadArgs &a, const Lane &l, const float *cs, int n) {
     Angles r;
     if (l.turned && l.token < n) {
         const int half = a.R >> 1;
-        const float4 *c = reinterpret_cast<const float4 *>(cs + l.token * half), *s = reinterpret_cast<const float4 *>(cs + (n + l.token) * half);
-        *reinterpret_cast<float4 *>(r.c) = c[l.c];
-        *reinterpret_cast<float4 *>(r.c + 4) = c[l.c + l.step];
-        *reinterpret_cast<float4 *>(r.s) = s[l.c];
-        *reinterpret_cast<float4 *>(r.s + 4) = s[l.c + l.step];
+        using F = std::conditional_t<kPairs && DT == MOE_DTYPE_F32, float2, float4>;      // the planes of a word, or of two
+        constexpr int N = sizeof(F) / sizeof(float);
+        const F *c = reinterpret_cast<const F *>(cs + l.token * half), *s = reinterpret_cast<const F *>(cs + (n + l.token) * half);
+#pragma unroll
+        for (int w = 0; w < 8 / N; ++w) {
+            *reinterpret_cast<F *>(r.c + N * w) = c[l.c + w * l.step];
+            *reinterpret_cast<F *>(r.s + N * w) = s[l.c + w * l.step];
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -122,27 +133,35 @@ __device__ __forceinline__ Angles angles_of(const HeadArgs &a, const Lane &l, co
     return r;
 }
 
-// The lane's two pieces as eight planes (a, b), and back.
-template <int DT, bool kPairs> __device__ __forceinline__ void to_planes(const Raw8<DT> (&r)[2], float (&a)[8], float (&b)[8]) {
-    float v[2][8];
-    widen8<DT>(r[0], v[0]);
-    widen8<DT>(r[1], v[1]);
+// Where value a (b) of the lane's plane i is: its word, and its place in it.
+template <int DT, bool kPairs> __device__ __forceinline__ constexpr int word_of(int i, int b) {
+    return DT == MOE_DTYPE_F32 ? (kPairs ? i >> 1 : (i >> 2) + 2 * b) : (kPairs ? i >> 2 : b);
+}
+template <int DT, bool kPairs> __device__ __forceinline__ constexpr int place_of(int i, int b) {
+    return DT == MOE_DTYPE_F32 ? (kPairs ? 2 * (i & 1) + b : i & 3) : (kPairs ? 2 * (i & 3) + b : i);
+}
+
+// The lane's words as eight planes (a, b), and back.
+template <int DT, bool kPairs> __device__ __forceinline__ void to_planes(const Words<DT> &r, float (&a)[8], float (&b)[8]) {
+    float v[kWords<DT>][kPieceValues<DT>];
+#pragma unroll
+    for (int w = 0; w < kWords<DT>; ++w) widen_piece<DT>(r.w[w], v[w]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        a[i] = kPairs ? v[i >> 2][2 * (i & 3)] : v[0][i];
-        b[i] = kPairs ? v[i >> 2][2 * (i & 3) + 1] : v[1][i];
+        a[i] = v[word_of<DT, kPairs>(i, 0)][place_of<DT, kPairs>(i, 0)];
+        b[i] = v[word_of<DT, kPairs>(i, 1)][place_of<DT, kPairs>(i, 1)];
     }
 }
 template <int DT, bool kPairs>
 __device__ __forceinline__ void store_planes(typename RowType<DT>::T *p, const Lane &l, const float (&a)[8], const float (&b)[8]) {
-    float v[2][8];
+    float v[kWords<DT>][kPieceValues<DT>];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        (kPairs ? v[i >> 2][2 * (i & 3)] : v[0][i]) = a[i];
-        (kPairs ? v[i >> 2][2 * (i & 3) + 1] : v[1][i]) = b[i];
+        v[word_of<DT, kPairs>(i, 0)][place_of<DT, kPairs>(i, 0)] = a[i];
+        v[word_of<DT, kPairs>(i, 1)][place_of<DT, kPairs>(i, 1)] = b[i];
     }
-    store8<DT>(p + 8 * l.p0, narrow8<DT>(v[0]));
-    store8<DT>(p + 8 * (l.p0 + l.step), narrow8<DT>(v[1]));
+#pragma unroll
+    for (int w = 0; w < kWords<DT>; ++w) st16(p + kPieceValues<DT> * (l.p0 + w * l.step), narrow_piece<DT>(v[w]));
 }
 
 // r = x * y,  r += x * y  of eight values, two an instruction.
@@ -175,16 +194,16 @@ __device__ __forceinline__ void scale8(float (&r)[8], float y) {
     for (int i = 0; i < 8; i += 2) mul2(r, i, y, y);
 }
 
-template <int DT> __device__ __forceinline__ void fetch16(const typename RowType<DT>::T *p, const Lane &l, Raw8<DT> (&r)[2]) {
-    r[0] = load8<DT>(p + 8 * l.p0);
-    r[1] = load8<DT>(p + 8 * (l.p0 + l.step));
+template <int DT> __device__ __forceinline__ void fetch_row(const typename RowType<DT>::T *p, const Lane &l, Words<DT> &r) {
+#pragma unroll
+    for (int w = 0; w < kWords<DT>; ++w) r.w[w] = ld16(p + kPieceValues<DT> * (l.p0 + w * l.step));
 }
-template <int DT> __device__ __forceinline__ void fetch_weight(const void *w, const Lane &l, Raw8<DT> (&r)[2]) {
-    using T = typename RowType<DT>::T;
-    r[0] = r[1] = Raw8<DT>{};
+template <int DT> __device__ __forceinline__ void fetch_weight(const void *from, const Lane &l, Words<DT> &r) {
+    r = Words<DT>{};
     if (l.on) {
-        r[0] = load8_shared<DT>(static_cast<const T *>(w) + 8 * l.p0);
-        r[1] = load8_shared<DT>(static_cast<const T *>(w) + 8 * (l.p0 + l.step));
+#pragma unroll
+        for (int w = 0; w < kWords<DT>; ++w)
+            r.w[w] = ld16_shared(static_cast<const typename RowType<DT>::T *>(from) + kPieceValues<DT> * (l.p0 + w * l.step));
     }
 }
 
@@ -206,11 +225,11 @@ __global__ void __launch_bounds__(kThreads) k_head_norm(HeadArgs a) {
     const bool key = (int)blockIdx.x >= a.q.blocks;
     const HeadTensor h = key ? a.k : a.q;
     const int t0 = ((int)blockIdx.x - (key ? a.q.blocks : 0)) * h.tokens, n = min(h.tokens, a.T - t0);
-    const Lane l = lane_of(a, h);
+    const Lane l = lane_of<DT>(a, h);
     const bool on = l.on && l.token < n;
     pdl_wait();
     pdl_trigger();
-    Raw8<DT> x[U][2], wr[2];
+    Words<DT> x[U], wr;
     const int64_t pitch = (int64_t)l.heads * a.D;                   // from a row to the thread's next one
     const T *from = static_cast<const T *>(h.x) + (int64_t)(t0 + l.token) * h.stride + l.head * a.D;
     T *to = static_cast<T *>(h.out) + (int64_t)(t0 + l.token) * h.out_stride + l.head * a.D;
@@ -218,19 +237,19 @@ __global__ void __launch_bounds__(kThreads) k_head_norm(HeadArgs a) {
     auto fetch = [&]() {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            x[u][0] = x[u][1] = Raw8<DT>{};
-            if (u < left) fetch16<DT>(from + u * pitch, l, x[u]);
+            x[u] = Words<DT>{};
+            if (u < left) fetch_row<DT>(from + u * pitch, l, x[u]);
         }
         from += U * pitch;
     };
     fetch();
     fetch_weight<DT>(h.w, l, wr);
-    fill_angles<kPairs>(a, t0, n, cs);
+    fill_angles<DT, kPairs>(a, t0, n, cs);
     __syncthreads();
     // a' = rstd (a (cos wa) - b (sin wb)),  b' = rstd (b (cos wb) + a (sin wa))
     float wa[8], wb[8], ca[8], cb[8], sa[8], sb[8];
     {
-        const Angles r = angles_of(a, l, cs, n);
+        const Angles r = angles_of<DT, kPairs>(a, l, cs, n);
         to_planes<DT, kPairs>(wr, wa, wb);
         mul8(ca, wa, r.c);
         mul8(cb, wb, r.c);
@@ -270,18 +289,18 @@ __global__ void __launch_bounds__(kThreads) k_head_norm(HeadArgs a) {
 // (a thread reads what it copied itself: no barrier).  In registers, two rows at
 // once, 8192 x 36 heads of 128 took 57.6 us.
 template <int DT> constexpr int kRing = DT == MOE_DTYPE_F32 ? 3 : 4;
-template <int DT> constexpr int kRowWords = 2 * 2 * sizeof(Raw8<DT>) / 16;      // 16-byte words of x and grad a thread has of a row
+template <int DT> constexpr int kRowWords = 2 * kWords<DT>;                     // of x and of grad
 template <int DT> constexpr int kRingBytes = kRing<DT> * kRowWords<DT> * 16 * kThreads;
 
 template <int DT, bool kPairs>
 __global__ void __launch_bounds__(kThreads, 2) k_head_norm_backward(HeadArgs a) {
     using T = typename RowType<DT>::T;
-    constexpr int W = kRowWords<DT> / 4;   // words a piece
+    constexpr int W = kWords<DT>, VW = kPieceValues<DT>;
     extern __shared__ __align__(16) float cs[];                     // angles, in the end sums; then the ring
     const bool key = (int)blockIdx.x < a.k.blocks;
     const HeadTensor h = key ? a.k : a.q;
     const int block = (int)blockIdx.x - (key ? 0 : a.k.blocks);
-    const Lane l = lane_of(a, h);
+    const Lane l = lane_of<DT>(a, h);
     uint4 *ring = reinterpret_cast<uint4 *>(cs + a.ring_at) + threadIdx.x;
     const int rounds = (h.heads + l.heads - 1) >> h.split;          // rows a thread and tile
     const int64_t pitch = (int64_t)l.heads * a.D;                   // from a row to the thread's next one
@@ -292,8 +311,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_head_norm_backward(HeadArgs a) 
     const T *cx = nullptr, *cg = nullptr;
     auto tile_at = [&]() {
         const int64_t t = (int64_t)ct * h.tokens + l.token;
-        cx = static_cast<const T *>(h.x) + t * h.stride + l.head * a.D + 8 * l.p0;
-        cg = static_cast<const T *>(h.g) + t * h.g_stride + l.head * a.D + 8 * l.p0;
+        cx = static_cast<const T *>(h.x) + t * h.stride + l.head * a.D + VW * l.p0;
+        cg = static_cast<const T *>(h.g) + t * h.g_stride + l.head * a.D + VW * l.p0;
     };
     auto copy_row = [&]() {
         if (ct < h.tiles) {
@@ -301,10 +320,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_head_norm_backward(HeadArgs a) 
                 uint4 *to = ring + fill * (kRowWords<DT> * kThreads);
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
-                    copy16(to + w * kThreads, cx + 4 * w, true);
-                    copy16(to + (W + w) * kThreads, cx + 8 * l.step + 4 * w, true);
-                    copy16(to + (2 * W + w) * kThreads, cg + 4 * w, true);
-                    copy16(to + (3 * W + w) * kThreads, cg + 8 * l.step + 4 * w, true);
+                    copy16(to + w * kThreads, cx + VW * w * l.step, true);
+                    copy16(to + (W + w) * kThreads, cg + VW * w * l.step, true);
                 }
             }
             cx += pitch;
@@ -324,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_head_norm_backward(HeadArgs a) 
     int slot = 0;
     float wa[8], wb[8], gwa[8] = {}, gwb[8] = {};
     {
-        Raw8<DT> wr[2];
+        Words<DT> wr;
         fetch_weight<DT>(h.w, l, wr);
         to_planes<DT, kPairs>(wr, wa, wb);
     }
@@ -333,9 +350,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_head_norm_backward(HeadArgs a) 
         const bool on = l.on && l.token < n;
         T *to = static_cast<T *>(h.out) + (int64_t)(t0 + l.token) * h.out_stride + l.head * a.D;
         __syncthreads();                   // the tile before is done with the angles
-        fill_angles<kPairs>(a, t0, n, cs);
+        fill_angles<DT, kPairs>(a, t0, n, cs);
         __syncthreads();
-        const Angles r = angles_of(a, l, cs, n);
+        const Angles r = angles_of<DT, kPairs>(a, l, cs, n);
         float minus[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) minus[i] = -r.s[i];
@@ -345,12 +362,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_head_norm_backward(HeadArgs a) 
             const uint4 *at = ring + slot * (kRowWords<DT> * kThreads);
             if (++slot == kRing<DT>) slot = 0;
             const bool mine = on && l.head + row * l.heads < h.heads;
-            Raw8<DT> x[2] = {}, g[2] = {};
+            Words<DT> x{}, g{};
             if (mine) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    x[i] = take8<DT>(at + i * W * kThreads, kThreads);
-                    g[i] = take8<DT>(at + (2 + i) * W * kThreads, kThreads);
+                for (int w = 0; w < W; ++w) {
+                    x.w[w] = at[w * kThreads];
+                    g.w[w] = at[(W + w) * kThreads];
                 }
             }
             float va[8], vb[8], fa[8], fb[8], sum[2] = {}, dot[2] = {};
@@ -395,9 +412,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_head_norm_backward(HeadArgs a) 
         float *mine = cs + (threadIdx.x >> a.lg) * a.D;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int pa = kPairs ? l.p0 + (i >> 2) * l.step : l.p0, pb = kPairs ? pa : l.p0 + l.step;
-            mine[8 * pa + (kPairs ? 2 * (i & 3) : i)] = gwa[i];
-            mine[8 * pb + (kPairs ? 2 * (i & 3) + 1 : i)] = gwb[i];
+            mine[VW * (l.p0 + word_of<DT, kPairs>(i, 0) * l.step) + place_of<DT, kPairs>(i, 0)] = gwa[i];
+            mine[VW * (l.p0 + word_of<DT, kPairs>(i, 1) * l.step) + place_of<DT, kPairs>(i, 1)] = gwb[i];
         }
     }
     __syncthreads();
