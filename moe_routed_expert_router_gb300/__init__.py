@@ -299,6 +299,20 @@ def _there(index, function):
     return call
 
 
+# Memory of the caching allocator for a stream of the current device; torch's own function makes the device current first,
+# 2 us a call where it is that already.
+_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+
+
+def _workspace(n, index, handle):
+    """n bytes that belong to the call's stream (None for 0); caching_allocator_delete gives them back behind the launches."""
+    if not n:
+        return None
+    if _raw_alloc is None or _elsewhere(index):
+        return torch.cuda.caching_allocator_alloc(n, index, handle)
+    return _raw_alloc(n, handle)
+
+
 def rms_norm(x, weight, residual=None, eps=1e-6, quant=QUANT_NONE, out=None, stream=None):
     """Residual addition and root-mean-square norm of x [T][H] (rows may be strided).
 
@@ -656,7 +670,7 @@ def head_norm_backward(grad_q, grad_k, q, k, q_weight, k_weight, positions, turn
     call = L.moe_head_norm_backward
     if _devices != 1 and _elsewhere(index):
         call = _there(index, call)
-    ws = torch.cuda.caching_allocator_alloc(n, index, handle) if n else None
+    ws = _workspace(n, index, handle)
     try:
         st = call(gp, gs, hp, hs, *given, *small, *sizes, int(bool(interleaved)), code, eps, *outs, ws, n, handle)
     finally:
@@ -763,22 +777,22 @@ def decode_layer(x, router_w, gate, up, down, top_k, router_bias=None, router=RO
         if Is == 0 or Is >> 31:
             _refuse(where, f"a shared expert of {Is} features", ERR_UNSUPPORTED_SHAPE)
     ap = None if base is None else _want(base, where, "base", shape, dt, index)
-    given = (x, router_w, gate, up, down, router_bias, base, *(shared or ()))
-    if torch.is_grad_enabled():
-        for t in given:
-            if t is not None and t.requires_grad:
-                _followed(where)
+    if (x.requires_grad or router_w.requires_grad or gate.requires_grad or up.requires_grad or down.requires_grad
+            or (router_bias is not None and router_bias.requires_grad) or (base is not None and base.requires_grad)
+            or (shared is not None and any(t.requires_grad for t in shared))):
+        _followed(where)
     if out is None:
         out = {"out": _new(shape, dt, dev, stream), "topk_ids": _new((T, top_k), _I32, dev, stream), "topk_w": _new((T, top_k), _F32, dev, stream)}
     op = _want(out["out"], where, "out", shape, dt, index)
     ip, wp = _want(out["topk_ids"], where, "topk_ids", (T, top_k), _I32, index), _want(out["topk_w"], where, "topk_w", (T, top_k), _F32, index)
     L = lib()
     n = L.moe_decode_layer_workspace(T, E, I, top_k, Is)
-    handle = _raw_stream(index) if stream is None else _given(where, index, stream, *given, out["out"], out["topk_ids"], out["topk_w"])
+    handle = _raw_stream(index) if stream is None else _given(
+        where, index, stream, x, router_w, gate, up, down, router_bias, base, *(shared or ()), out["out"], out["topk_ids"], out["topk_w"])
     call = L.moe_decode_layer
     if _devices != 1 and _elsewhere(index):
         call = _there(index, call)
-    ws = torch.cuda.caching_allocator_alloc(n, index, handle) if n else None
+    ws = _workspace(n, index, handle)
     try:
         st = call(xp, code, T, H, rp, ROUTER_F32 if rt is _F32 else ROUTER_BF16, bp, E, top_k, router, int(bool(renormalize)), *ep, I, *sp, Is, ap,
                   op, ip, wp, ws, n, handle)

@@ -211,3 +211,31 @@ def test_captured_replayed_and_beside_another_stream():
                 assert torch.equal(got[name], want[name])
         check(L, a)
         assert torch.equal(c["out"], moe.decode_layer(a["out"], L.rw, L.gate, L.up, L.down, 4)["out"])
+
+
+def test_many_calls_at_once():
+    """Layers on three streams beside products that hold the card: each call's blocks wait inside for others of its own,
+    and have to finish whatever else keeps them from running together."""
+    layers = [Layer(4, 2048, 16, 256, 4, "bf16", shared=128, seed=9), Layer(16, 1024, 32, 128, 6, "f16", seed=10), Layer(1, 4096, 8, 512, 2, "f32", seed=11)]
+    want = [L.run() for L in layers]
+    a = torch.randn(4096, 4096, device="cuda", dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    streams, big, got = [torch.cuda.Stream() for _ in layers], torch.cuda.Stream(), []
+    for _ in range(12):
+        with torch.cuda.stream(big):
+            for _ in range(4):
+                torch.mm(a, a)
+        got += [L.run(stream=s) for L, s in zip(layers, streams)]
+    torch.cuda.synchronize()
+    for i, out in enumerate(got):
+        for name in out:
+            assert torch.equal(out[name], want[i % 3][name])
+
+
+def test_workspaces_of_calls_behind_one_another():
+    """Calls of different sizes, nothing waiting between them: each has the memory of the one before."""
+    layers = [Layer(T, 512, 24, 64 * (1 + T % 3), 4, "bf16", base=True, seed=20 + T) for T in (16, 1, 7, 2, 12)]
+    want = [L.run()["out"].clone() for L in layers]
+    got = [L.run()["out"] for _ in range(6) for L in layers]
+    for i, out in enumerate(got):
+        assert torch.equal(out, want[i % 5])

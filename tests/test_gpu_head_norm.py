@@ -282,3 +282,17 @@ def test_captured_and_replayed_on_another_stream():
         for a, b in ((out, want), (back, wback)):
             for name in a:
                 assert torch.equal(a[name], b[name])
+
+
+def test_workspaces_of_calls_behind_one_another():
+    """Gradients of different sizes, nothing waiting between them: each has the memory of the one before."""
+    cases = []
+    for T, Hq, Hk, D in ((900, 8, 2, 64), (37, 3, 1, 128), (2500, 4, 4, 32), (300, 16, 2, 256)):
+        q, k, qw, kw, pos = inputs(T, Hq, Hk, D, torch.bfloat16, T)
+        gq, gk, *_ = inputs(T, Hq, Hk, D, torch.bfloat16, T + 1)
+        cases.append((gq, gk, q, k, qw, kw, pos, moe.rotary_turns(D)))
+    want = [{n: t.clone() for n, t in moe.head_norm_backward(*c).items()} for c in cases]
+    got = [moe.head_norm_backward(*c) for _ in range(5) for c in cases]
+    for i, out in enumerate(got):
+        for name in out:
+            assert torch.equal(out[name], want[i % 4][name])
