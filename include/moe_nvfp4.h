@@ -500,16 +500,25 @@ moe_status moe_head_norm_backward(const void *grad_q, int64_t grad_q_stride, con
  *   weight host struct: codes [N][K/2], scales [N][K/16] or [N][K/32],
  *          tensor_scale one fp32 (NVFP4; ignored for MXFP4)
  *   out    [T][N] of out_dtype: `dtype` or MOE_DTYPE_F32; overlaps nothing else
+ *   workspace: moe_linear_fp4_workspace bytes (0 for most products), 256-byte
+ *          aligned, used during the call only
  * W is not rounded (a value has at most six significant bits and the tensor
- * scale is applied to the sum); f16 rows are taken as they are, bf16 ones to
- * within 2^-32 of the largest finite magnitude of each of their blocks of 256 (128
- * for more than 16 tokens) values.  A row that holds an infinity or a NaN gives
- * what fp32 arithmetic gives and leaves the other rows alone.
+ * scale is applied to the sum).  Small products take f16 rows as they are and bf16
+ * ones to within 2^-32 of the largest finite magnitude of each of their blocks of
+ * 256 (128 for more than 16 tokens) values.  Large ones, those that want a workspace,
+ * take rows as integers of 23 bits: to within 2^-22 of the largest finite magnitude
+ * of the 16 (MXFP4: 32) values that share a weight's scale or, for NVFP4 where that is
+ * more, 2^-30 of the row's.  A row that holds an infinity or a NaN gives what fp32
+ * arithmetic gives and leaves the other rows alone.  Sums are taken in a fixed order:
+ * equal inputs give equal bits.  Waits inside a launch end after a second; if one ever
+ * runs out, out is NaN.
  * K: a multiple of 128 up to 65536; x_stride: a multiple of 8, at least K; T: up
- * to 2^20, made for up to 64 (every 32 tokens read the weight once, the later ones from cache).  T = 0 is a
- * no-op. */
+ * to 2^20, made for up to 64 (every 32 tokens, of large products every 16, read the
+ * weight once, the later ones from cache).  T = 0 is a no-op. */
+size_t moe_linear_fp4_workspace(int32_t weight_format, int32_t T, int32_t N, int32_t K);
 moe_status moe_linear_fp4(const void *x, int64_t x_stride, const moe_nvfp4 *weight, int32_t weight_format, int32_t T,
-                          int32_t N, int32_t K, int32_t dtype, int32_t out_dtype, void *out, void *stream);
+                          int32_t N, int32_t K, int32_t dtype, int32_t out_dtype, void *out, void *workspace,
+                          size_t workspace_bytes, void *stream);
 
 /* The whole mixture-of-experts layer of up to 16 tokens with experts that are not
  * quantised, in two launches:

@@ -36,7 +36,7 @@ EXPORTS = ["moe_plan_create", "moe_plan_destroy", "moe_route", "moe_forward", "m
            "moe_rms_norm_backward_workspace_for",
            "moe_sorted_rows", "moe_sort_pairs", "moe_dispatch", "moe_combine", "moe_combine_backward",
            "moe_head_norm", "moe_head_norm_backward", "moe_head_norm_backward_workspace",
-           "moe_linear_fp4", "moe_decode_layer", "moe_decode_layer_workspace"]
+           "moe_linear_fp4", "moe_linear_fp4_workspace", "moe_decode_layer", "moe_decode_layer_workspace"]
 FMT_E4M3, FMT_E2M1 = 0, 1
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 QUANT_NONE, QUANT_E4M3_128, QUANT_E4M3_ROW, QUANT_MXFP8 = 0, 1, 2, 3
@@ -105,7 +105,8 @@ def lib():
         L.moe_head_norm.argtypes = [P, I64, P, I64, *head, P, I64, P, I64, P]
         L.moe_head_norm_backward.argtypes = [P, I64, P, I64, P, I64, P, I64, *head, P, P, P, P, P, SZ, P]
         L.moe_head_norm_backward_workspace.argtypes = [I32, I32, I32, I32, I32]
-        L.moe_linear_fp4.argtypes = [P, I64, ctypes.POINTER(Nvfp4), I32, I32, I32, I32, I32, I32, P, P]
+        L.moe_linear_fp4.argtypes = [P, I64, ctypes.POINTER(Nvfp4), I32, I32, I32, I32, I32, I32, P, P, SZ, P]
+        L.moe_linear_fp4_workspace.argtypes = [I32, I32, I32, I32]
         L.moe_decode_layer.argtypes = [P, I32, I32, I32, P, I32, P, I32, I32, I32, I32, P, P, P, I32, P, P, P, I32, P, P, P, P, P, SZ, P]
         L.moe_decode_layer_workspace.argtypes = [I32, I32, I32, I32, I32]
         L.moe_status_string.argtypes = [I32]
@@ -115,7 +116,7 @@ def lib():
             if n not in ("moe_status_string", "moe_version"):
                 getattr(L, n).restype = I32
         L.moe_rms_norm_backward_workspace.restype = L.moe_rms_norm_backward_workspace_for.restype = SZ
-        L.moe_head_norm_backward_workspace.restype = L.moe_decode_layer_workspace.restype = SZ
+        L.moe_head_norm_backward_workspace.restype = L.moe_linear_fp4_workspace.restype = L.moe_decode_layer_workspace.restype = SZ
         L.moe_sorted_rows.restype = I64
         _lib = L
     return _lib
@@ -596,10 +597,11 @@ def rotary_turns(dim, base=10000.0, frequencies=None, device="cuda"):
 def _want_heads(t, where, name, shape, dtype, index):
     """Heads of contiguous values behind one another, tokens a stride apart; returns their address and stride in values."""
     T, n, D = shape
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not (
-            t.is_contiguous() or (t.stride(2) == 1 and (n == 1 or t.stride(1) == D))):
+    steps = t.stride()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or (
+            (steps[2] != 1 or (steps[1] != D and n != 1)) and not t.is_contiguous()):
         _refuse(where, f"{name} {t.dtype}{list(t.shape)} on {t.device}; heads of contiguous {dtype}{list(shape)} on cuda:{index} expected")
-    return t.data_ptr(), t.stride(0) if T > 1 else n * D
+    return t.data_ptr(), steps[0] if T > 1 else n * D
 
 
 def _heads(q, k, q_weight, k_weight, positions, turns, where):
@@ -689,7 +691,8 @@ def linear_fp4(x, weight: NvfpTensor, out=None, out_dtype=None, stream=None):
     quantize_nvfp4 and quantize_mxfp4 give it: [T][N] in x's type, or in float32 with out_dtype=torch.float32.  out
     overlaps nothing else.
 
-    Made for the few tokens of a decode step: every 32 of them read the weight."""
+    Made for the few tokens of a decode step: every 32 of them read the weight, or every 16 where the product is large
+    enough for the tensor cores that take 4-bit operands."""
     where = "moe_linear_fp4"
     codes, scales, ts = weight.codes, weight.scales, weight.ts
     shape, rows = x.shape, codes.shape[-2:]
@@ -725,10 +728,17 @@ def linear_fp4(x, weight: NvfpTensor, out=None, out_dtype=None, stream=None):
         _refuse(where, f"out {to}; {dt} or float32 expected")
     op = _want(out, where, "out", (T, N), to, index)
     handle = _raw_stream(index) if stream is None else _given(where, index, stream, x, codes, scales, ts, out)
-    call = lib().moe_linear_fp4
+    L = lib()
+    n = L.moe_linear_fp4_workspace(fmt, T, N, K) if T * N * K >> 28 else 0       # a smaller product never wants one
+    call = L.moe_linear_fp4
     if _devices != 1 and _elsewhere(index):
         call = _there(index, call)
-    st = call(xp, xs, ctypes.byref(Nvfp4(wp, sp, tp)), fmt, T, N, K, code, DTYPE_F32 if to is _F32 else code, op, handle)
+    ws = _workspace(n, index, handle) if n else None
+    try:
+        st = call(xp, xs, ctypes.byref(Nvfp4(wp, sp, tp)), fmt, T, N, K, code, DTYPE_F32 if to is _F32 else code, op, ws, n, handle)
+    finally:
+        if ws is not None:
+            torch.cuda.caching_allocator_delete(ws)
     if st:
         raise MoeError(st, where)
     return out

@@ -40,11 +40,9 @@
 //              accumulators)
 // Every mbarrier wait is bounded (about one second); on expiry the kernel sets
 // the plan's timeout bit and every role leaves its loop.
-#include <cuda.h>
-
 #include <algorithm>
 
-#include "moe_internal.cuh"
+#include "tc.cuh"
 
 namespace moe {
 namespace {
@@ -105,105 +103,8 @@ struct TcArgs {
     int keep_h;             // also store the fp32 h (stage-by-stage checks)
 };
 
-__device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
-        ::"r"(smem_u32(dst)), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y)
-        : "memory");
-}
-
-// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
-// 1024 bytes apart (the layout TMA writes with CU_TENSOR_MAP_SWIZZLE_128B).
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
-// Descriptor of one 512-byte scale-factor atom (32 rows x 16 bytes, no swizzle)
-// for tcgen05.cp .32x128b.
-__device__ __forceinline__ uint64_t desc_sf(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
-}
-
-// Instruction descriptor, kind::mxf4nvf4: A and B E2M1, UE4M3 scales, K-major,
-// M = 128, N = n (a multiple of 16).
-__device__ __forceinline__ uint32_t idesc_fp4(uint32_t n) {
-    return (1u << 7) | (1u << 10) | ((n >> 3) << 17) | (0u << 23) | ((128u >> 4) << 24);
-}
-
-__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                        uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb)
-        : "memory");
-}
-
-// MXFP4 (kind::mxf4, UE8M0 scales, one a 32-value block): a K = 64 MMA takes
-// two scale bytes a row.  A 32-bit scale cell of tensor memory holds four
-// (K = 128, two MMAs); the descriptor's scale-factor ids (A: bits 29-30, B:
-// bits 4-5) pick bytes 0-1 (id 0) or 2-3 (id 2) of the cell.
-__device__ __forceinline__ uint32_t idesc_mx4(uint32_t n, int kk) {
-    const uint32_t id = 2u * (uint32_t)(kk & 1);
-    return idesc_fp4(n) | (1u << 23) | (id << 29) | (id << 4);
-}
-
-__device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                        uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb)
-        : "memory");
-}
-
-// One block-scaled FP4 MMA of K chunk kk: NVFP4 (cell = four 16-value blocks =
-// one K chunk) or MXFP4 (cell = four 32-value blocks = two K chunks).
-// sfa0 / sfb0: the stage's first scale column of the A / B operand.
-template <int MX>
-__device__ __forceinline__ void mma_blk(uint32_t d, uint64_t a, uint64_t b, uint32_t n, int kk, uint32_t sfa0,
-                                        uint32_t sfb0, uint32_t acc) {
-    if (MX)
-        mma_mx4(d, a, b, idesc_mx4(n, kk), sfa0 + 4 * (kk >> 1), sfb0 + 4 * (kk >> 1), acc);
-    else
-        mma_fp4(d, a, b, idesc_fp4(n), sfa0 + 4 * kk, sfb0 + 4 * kk, acc);
-}
-
 // Token rows a tile loads and multiplies: 32, 64 or 128 (index into TcArgs::b).
 __device__ __forceinline__ int rows_class(int valid) { return valid <= 32 ? 0 : (valid <= 64 ? 1 : 2); }
-
-__device__ __forceinline__ void sf_copy(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-}
-
-__device__ __forceinline__ void mma_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// 32 lanes x 16 columns from v[0..15] (each thread: its lane).
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
-}
-
-// 32 lanes x 16 columns of fp32 into v[0..15] (each thread: its lane); the
-// caller waits with tcgen05.wait::ld before reading v.
-__device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, float *v) {
-    uint32_t *r = reinterpret_cast<uint32_t *>(v);
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
 
 struct Item {
     int e, row0, valid, f, sh, K;
@@ -1849,40 +1750,6 @@ __global__ void __launch_bounds__(256) k_permute_fp4(const uint8_t *__restrict__
 }
 
 // ------------------------------------------------------------------ host side
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    if (!fn) {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    }
-    return fn;
-}
-
-// 2-D tensor map of 1-byte (or, with u16, 2-byte) elements: `rows` rows of
-// `row_elems` elements (row stride `stride` bytes), box = box_elems x box_rows.
-bool make_map(CUtensorMap *m, const void *base, uint64_t row_elems, uint64_t rows, uint64_t stride,
-              uint32_t box_elems, uint32_t box_rows, bool swizzle, bool u16 = false) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {row_elems, rows};
-    cuuint64_t strides[1] = {stride};
-    cuuint32_t box[2] = {box_elems, box_rows};
-    cuuint32_t es[2] = {1, 1};
-    CUresult r = fn(m, u16 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
-                    const_cast<void *>(base), dims, strides, box, es,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
 
 constexpr size_t kSmemBytes = kStages * kStageBytes + 512 + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "FP4 pipeline exceeds shared memory");

@@ -21,21 +21,19 @@
 // a time, with a cp.async ring of its own, so that neither tokens nor weights pass
 // between warps and no barrier stops the stream.  The warps' sums of a pass over
 // the rows are joined in shared memory in a fixed order.  (Tokens in shared memory,
-// whole or in chunks with a barrier each: 16 x 16384 x 7168 31 to 41 us.)
+// whole or in chunks with a barrier each: 16 x 16384 x 7168 31 to 41 us against 27.)
 //
-// Measured: 1 x 100003 x 4096 NVFP4 47.7 us (4.8 TB/s, 72 % of the copy bandwidth),
-// 16 x 16384 x 7168 MXFP4 27.5 us (34 %), 4 x 4096 x 4096 5.5 us.  With all data in
-// shared memory a sub-partition needs 39 cycles for 16 rows x 32 values and eight
-// tokens (the eight code conversions 23 of them, the two MMAs 21 beside them; codes
-// widened by shifts and masks instead 44), 27 us of those 47.7; 65 are spent: four
-// warps do not hide each other's chains of load, conversion, product and MMA.  Each
-// eight tokens more add two MMAs, so from 16 tokens on the warp MMAs are the limit,
-// not the bytes.
+// Measured: 1 x 38912 x 7168 NVFP4 33.9 us (0.69 of the copy bandwidth), 1 x 16384 x 7168 18.8, 4 x 4096 x 4096 5.5.  With
+// all data in shared memory a sub-partition needs 39 cycles for 16 rows x 32 values and eight tokens (the eight code
+// conversions 23 of them, the two MMAs 21 beside them; codes widened by shifts and masks instead 44), 27 us of the 48 that
+// 1 x 100000 x 4096 takes; 65 are spent: four warps do not hide each other's chains of load, conversion, product and MMA.
+// Each eight tokens more add two MMAs, so from 16 tokens on the warp MMAs are the limit, not the bytes: large products go
+// to linear_tc.cu.
 #include <limits.h>
 
 #include <algorithm>
 
-#include "rows.cuh"
+#include "linear.cuh"
 
 namespace {
 
@@ -104,14 +102,6 @@ template <int B> __device__ __forceinline__ void copy_small(void *dst, const voi
 }
 
 __device__ __forceinline__ uint32_t lds32(const uint8_t *p) { return *reinterpret_cast<const uint32_t *>(p); }
-
-// The power of two that brings values whose largest finite magnitude has exponent e to [2^7, 2^8), in two factors, and
-// what undoes it; e is -127 where all are subnormals or zeros.
-__device__ __forceinline__ int exponent_of(float amax) { return (int)(__float_as_uint(amax) >> 23) - 127; }
-__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }    // -126 to 127
-__device__ __forceinline__ float scale_up(int e) { return power_of_two(min(7 - e, 127)); }
-__device__ __forceinline__ float scale_more(int e) { return power_of_two(max(0, 7 - e - 127)); }
-__device__ __forceinline__ float scale_down(int e) { return power_of_two(max(e - 7, -126)) * power_of_two(min(0, e - 7 + 126)); }
 
 // Largest magnitude of bf16 values, NaNs aside: pairs, then the larger of the two.
 __device__ __forceinline__ uint32_t amax_pair(uint32_t m, uint32_t pair) {
@@ -428,8 +418,14 @@ moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_E
 
 extern "C" {
 
+size_t moe_linear_fp4_workspace(int32_t weight_format, int32_t T, int32_t N, int32_t K) {
+    if (T < 1 || T > kMaxTokens || N < 1 || N > INT32_MAX - 1024 || K < 128 || K > kMaxK || K % 128) return 0;
+    return linear_tc_workspace(weight_format == MOE_WEIGHTS_MXFP4, T, N, K);
+}
+
 moe_status moe_linear_fp4(const void *x, int64_t x_stride, const moe_nvfp4 *weight, int32_t weight_format, int32_t T,
-                          int32_t N, int32_t K, int32_t dtype, int32_t out_dtype, void *out, void *stream) {
+                          int32_t N, int32_t K, int32_t dtype, int32_t out_dtype, void *out, void *workspace,
+                          size_t workspace_bytes, void *stream) {
     if (T < 0 || (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F16) || (out_dtype != dtype && out_dtype != MOE_DTYPE_F32) ||
         (weight_format != MOE_WEIGHTS_NVFP4 && weight_format != MOE_WEIGHTS_MXFP4) || !weight)
         return MOE_ERR_INVALID_ARG;
@@ -437,10 +433,18 @@ moe_status moe_linear_fp4(const void *x, int64_t x_stride, const moe_nvfp4 *weig
         return MOE_ERR_UNSUPPORTED_SHAPE;
     if (T == 0) return MOE_OK;
     const bool mx = weight_format == MOE_WEIGHTS_MXFP4;
-    if (!x || !out || !weight->codes || !weight->scales || (!mx && !weight->tensor_scale)) return MOE_ERR_INVALID_ARG;
+    const size_t ws = linear_tc_workspace(mx, T, N, K);
+    if (!x || !out || !weight->codes || !weight->scales || (!mx && !weight->tensor_scale) || (ws && !workspace) || workspace_bytes < ws)
+        return MOE_ERR_INVALID_ARG;
     if (!aligned_to(x, 16) || !aligned_to(weight->codes, 16) || !aligned_to(weight->scales, 16) ||
-        !aligned_to(mx ? nullptr : weight->tensor_scale, 4) || !aligned_to(out, out_dtype == MOE_DTYPE_F32 ? 4 : 2))
+        !aligned_to(mx ? nullptr : weight->tensor_scale, 4) || !aligned_to(out, out_dtype == MOE_DTYPE_F32 ? 4 : 2) ||
+        (ws && !aligned_to(workspace, 256)))
         return MOE_ERR_MISALIGNED;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (ws) {
+        const LinearCall c{x, x_stride, weight->codes, weight->scales, mx ? nullptr : weight->tensor_scale, T, N, K, dtype, out_dtype, out, workspace};
+        return cuda_status(launch_linear_tc(c, s));
+    }
     LinearArgs a{};
     a.codes = weight->codes;
     a.scales = weight->scales;
@@ -453,7 +457,6 @@ moe_status moe_linear_fp4(const void *x, int64_t x_stride, const moe_nvfp4 *weig
     a.K = K;
     a.dtype = out_dtype;
     a.bf16 = dtype == MOE_DTYPE_BF16;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     return cuda_status(mx ? launch_format<true>(a, s) : launch_format<false>(a, s));
 }
 

@@ -58,8 +58,9 @@ def weight(codes=A, scales=A, ts=A):
     return moe.Nvfp4(codes, scales, ts)
 
 
-def linear(x=A, xs=256, w=weight(), fmt=moe.WEIGHTS_NVFP4, T=4, N=64, K=256, dt=moe.DTYPE_BF16, to=moe.DTYPE_BF16, out=A):
-    return moe.lib().moe_linear_fp4(x, xs, None if w is None else ctypes.byref(w), fmt, T, N, K, dt, to, out, None)
+def linear(x=A, xs=256, w=weight(), fmt=moe.WEIGHTS_NVFP4, T=4, N=64, K=256, dt=moe.DTYPE_BF16, to=moe.DTYPE_BF16, out=A, ws=NULL,
+           n=0):
+    return moe.lib().moe_linear_fp4(x, xs, None if w is None else ctypes.byref(w), fmt, T, N, K, dt, to, out, ws, n, None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -71,6 +72,22 @@ def linear(x=A, xs=256, w=weight(), fmt=moe.WEIGHTS_NVFP4, T=4, N=64, K=256, dt=
     (dict(w=weight(ts=A + 2)), ALIGN), (dict(out=A + 1), ALIGN), (dict(to=moe.DTYPE_F32, out=A + 2), ALIGN), (dict(T=0), moe.OK)])
 def test_linear(kw, want):
     assert linear(**kw) == want
+
+
+def test_linear_workspace():
+    """Large products want one and refuse to run without it."""
+    n = moe.lib().moe_linear_fp4_workspace
+    nv, mx = moe.WEIGHTS_NVFP4, moe.WEIGHTS_MXFP4
+    assert n(nv, 0, 1 << 17, 256) == 0 and n(nv, 16, 0, 256) == 0 and n(nv, (1 << 20) + 1, 1 << 17, 256) == 0
+    assert n(nv, 16, 1 << 17, 384) == 0 and n(mx, 16, 1 << 17, 256) == 0      # rows of scales of whole 16 bytes
+    assert n(nv, 16, (1 << 17) - 1, 256) == 0 and n(nv, 8, 1 << 17, 256) == 0
+    big = dict(T=16, N=1 << 17, K=256)
+    want = n(nv, 16, 1 << 17, 256)
+    assert want >= 16 * 8 * 256 // 2
+    assert linear(**big) == INV and linear(**big, ws=A, n=want - 1) == INV and linear(**big, n=want) == INV
+    assert linear(**big, ws=A + 128, n=want) == ALIGN
+    for T in (17, 255, 256, 257, 300, 1 << 20):                   # more tokens go in pieces of 256
+        assert n(nv, T, 1 << 16, 1024) <= n(nv, 256, 1 << 16, 1024) + n(nv, T % 256 or 256, 1 << 16, 1024)
 
 
 def layer(x=A, dt=moe.DTYPE_BF16, T=4, H=256, rw=A, rdt=0, bias=NULL, E=16, k=4, router=0, renorm=1, gate=A, up=A, down=A, I=64, sg=NULL,
