@@ -17,12 +17,14 @@
 // weights while the digits are still being written.  An item is 256 weight rows (the M side, two accumulators of 128) x 16
 // tokens x a part of K; the parts of an item are a cluster's blocks, each of which adds a share of the rows, in order.
 //
-// Bound by the weight's bytes where there are enough of them: 16 x 100000 x 4096 NVFP4 45 us (0.77 of the copy bandwidth),
-// 16 x 38912 x 7168 38 (0.62), 16 x 16384 x 7168 MXFP4 21.1 (0.45; the warp MMAs of linear.cu 27.4).  About 8 us are outside
-// the stream: digits, the first token tile, joining and storing.  Every 16 tokens more read weights and digits from L2, 54 KB
-// a stage in 0.53 us: 64 x 38912 x 7168 67 us (197).
-// (Digits made in the multiplying blocks, by the warps of the epilogue: 16 x 16384 x 7168 30 us; each block makes all of
-// them again and eight warps take 1.5 us a stage.)
+// Bound by the weight's bytes where there are enough of them: 1 x 100003 x 4096 NVFP4 42.8 us (0.80 of the copy bandwidth),
+// 16 x 100000 x 4096 45.5 (0.77), 16 x 38912 x 7168 38 (0.62), 16 x 16384 x 7168 MXFP4 21.6 (0.44; the warp MMAs of linear.cu
+// 27.4).  The stream itself runs at 5 to 6 TB/s; about 8 us are outside it: digits, the first token tile, joining and
+// storing.  Every 16 tokens more read weights and digits from L2, 54 KB a stage in 0.53 us, near what an SM takes from it:
+// 64 x 38912 x 7168 67 us (197).
+// Tried, 16 x 16384 x 7168: digits made in the multiplying blocks by the warps of the epilogue 30 us (each block makes all of
+// them again, 1.5 us a stage); rings of their own for weights, five stages, and digits, two, 22.2; groups of 216 rows that
+// fill all SMs instead of 128 of them 25.0 (the next launch's blocks find no room beside the last ones).
 #include <algorithm>
 
 #include "linear.cuh"
@@ -609,7 +611,9 @@ template <bool MX> cudaError_t launch_chunk(const LinearCall &c, cudaStream_t st
     a.stages = l.stages;
     a.atoms = l.atoms;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(l.parts * (unsigned)std::min<int64_t>((int64_t)l.tiles * l.groups, clusters_of(l.parts)));
+    // as few clusters as take the items in that many rounds: an SM that is free early takes the next launch's blocks
+    const int64_t items = (int64_t)l.tiles * l.groups, at_once = clusters_of(l.parts), rounds = (items + at_once - 1) / at_once;
+    cfg.gridDim = dim3(l.parts * (unsigned)((items + rounds - 1) / rounds));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;
