@@ -497,8 +497,8 @@ moe_status moe_head_norm_backward(const void *grad_q, int64_t grad_q_stride, con
  * and moe_quantize_mxfp4 write it (moe_weight_format):
  *   out[t][n] = round(sum over k of x[t][k] * W[n][k]),  summed in fp32
  *   x      [T] rows of K, x_stride values apart, of `dtype` (bf16 or f16)
- *   weight host struct: codes [N][K/2], scales [N][K/16] or [N][K/32],
- *          tensor_scale one fp32 (NVFP4; ignored for MXFP4)
+ *   weight host struct: codes [N][K/2], scales [N][K/16] (E4M3, none negative) or
+ *          [N][K/32], tensor_scale one fp32 (NVFP4; ignored for MXFP4)
  *   out    [T][N] of out_dtype: `dtype` or MOE_DTYPE_F32; overlaps nothing else
  *   workspace: moe_linear_fp4_workspace bytes (0 for most products), 256-byte
  *          aligned, used during the call only

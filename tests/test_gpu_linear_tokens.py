@@ -117,6 +117,19 @@ def test_infinities_and_nans_stay_in_their_rows(K, fmt):
         assert torch.equal(bad[row][there], want[there].float())
 
 
+def test_scales_that_are_nan_or_zero_stay_in_their_rows():
+    T, K = 20, 1024
+    N = enough(T, K, 5)
+    w, x = a_weight(N, K, "nvfp4"), rows(T, K, BF, 6)
+    fine = moe.linear_fp4(x, w, out_dtype=F32)
+    w.scales[130, 3], w.scales[N - 1, 0] = 0x7F, 0x7F             # E4M3's NaN
+    w.scales[7] = 0
+    out = moe.linear_fp4(x, w, out_dtype=F32)
+    assert out[:, 130].isnan().all() and out[:, N - 1].isnan().all() and (out[:, 7] == 0).all()
+    keep = [i for i in range(N) if i not in (7, 130, N - 1)]
+    assert torch.equal(out[:, keep], fine[:, keep])
+
+
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 def test_a_token_does_not_depend_on_the_others(fmt):
     w, x = a_weight(enough(9, 1024, 200, fmt), 1024, fmt), rows(32, 1024, BF)
