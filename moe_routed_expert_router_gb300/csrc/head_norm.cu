@@ -40,7 +40,6 @@ using namespace moe;
 
 constexpr int kThreads = 256;
 constexpr int kMaxHeads = 1024, kMaxDim = 512;
-constexpr int kSms = 152;
 constexpr int kEach = 8;                   // heads that share what a group of lanes has of a token
 
 // Queries or keys: rows [T][heads][D], `stride` values from token to token.

@@ -43,7 +43,6 @@ namespace {
 
 using namespace moe;
 
-constexpr int kSms = 152;
 constexpr int kMaxTokens = 16, kMaxPairs = kMaxTokens * kMaxTopK;
 constexpr int kMaxWidth = 16384;
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
@@ -53,7 +52,6 @@ constexpr int kMaxRing = 8;
 constexpr int kQueue = 16;                 // pieces between a warp's copies and its products, more than kMaxRing
 constexpr int kMostRows = 32;              // rows of down a block sums at once
 constexpr int kMostPairs = 4;              // tokens that share a pass over an expert's weights: what registers hold sums for
-constexpr size_t kSmem = kSmemSm - 2048;   // a block's
 constexpr int kLeastRing = 2, kLeastRows = 8;                     // what the tokens in shared memory have to leave room for
 
 struct LayerArgs {
@@ -603,7 +601,7 @@ LayerShape layer_shape(const LayerArgs &a, size_t x) {
     s.front = (routing_bytes(a.E) + 15) / 16 * 16 + x;
     s.choice = sizeof(float) * ((size_t)kWarps * a.E + 2 * kMaxPairs);
     s.pass_rows = std::min(kMostRows, (blocks_of(a.H, kSms) + kRows - 1) / kRows * kRows);
-    auto rings = [&]() { return ((int64_t)kSmem - (int64_t)(s.front + sums_bytes(a.T, s.pass_rows))) / (kWarps * kStage); };
+    auto rings = [&]() { return ((int64_t)kSmemBlock - (int64_t)(s.front + sums_bytes(a.T, s.pass_rows))) / (kWarps * kStage); };
     while (rings() < kLeastRing && s.pass_rows > kLeastRows) s.pass_rows -= kRows;
     s.ring = (int)std::min<int64_t>(kMaxRing, rings());
     return s;
@@ -624,7 +622,7 @@ template <int DT> cudaError_t launch_layer(const LayerArgs &a, int router_dtype,
     const cudaError_t e = router_dtype == MOE_ROUTER_F32 ? launch_logits<DT, MOE_ROUTER_F32>(a, st) : launch_logits<DT, MOE_ROUTER_BF16>(a, st);
     if (e != cudaSuccess) return e;
     const LayerShape s = layer_shape(a, sizeof(typename RowType<DT>::T) * a.T * a.H);
-    if (s.ring >= kLeastRing && s.front + s.choice <= kSmem) return launch_weights<DT, true>(a, s, st);
+    if (s.ring >= kLeastRing && s.front + s.choice <= kSmemBlock) return launch_weights<DT, true>(a, s, st);
     return launch_weights<DT, false>(a, layer_shape(a, 0), st);
 }
 

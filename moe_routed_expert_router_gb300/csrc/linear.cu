@@ -29,32 +29,20 @@
 // 1 x 100000 x 4096 takes; 65 are spent: four warps do not hide each other's chains of load, conversion, product and MMA.
 // Each eight tokens more add two MMAs, so from 16 tokens on the warp MMAs are the limit, not the bytes: large products go
 // to linear_tc.cu.
-#include <limits.h>
-
-#include <algorithm>
-
 #include "linear.cuh"
+#include "linear_split.cuh"
 
 namespace {
 
 using namespace moe;
 
-// Values of K a stage: 256, and half of it where 32 tokens have to share the registers.
-template <int NT> constexpr int kStageK = NT >= 4 ? 128 : 256;
-constexpr int kScaleBytes = 16;            // a row's place for a stage's scales (MXFP4 uses half)
-constexpr int kCodePad = 16;               // behind a row's codes: eight rows' equal words lie in different banks
-constexpr int kRows = 16;                  // rows a tile (32: 53.1 us for 1 x 100003 x 4096 against 47.1, the sums' place taken from the ring)
-// Warps of a block: what the tokens' registers leave room for.
-template <int NT> constexpr int kWarps = NT == 1 ? 16 : 12;
-constexpr int kSms = 152;
+template <int NT> constexpr int kStageK = linear_stage_k(NT);
+template <int NT> constexpr int kWarps = linear_warps(NT);
+template <int NT> constexpr int kStageBytes = linear_stage_bytes(NT);
+constexpr int kRows = kLinearRows;
 constexpr int kMaxK = 1 << 16, kMaxTokens = 1 << 20;
-constexpr int kMaxRing = 6;
-constexpr size_t kSmem = kSmemSm - 1024;   // a block's
 
-// Bytes of a warp's stage of a tile.
-template <int NT> constexpr int kStageBytes = kRows * (kStageK<NT> / 2 + kCodePad + kScaleBytes);
-
-struct LinearArgs {
+struct LinearArgs : LinearSplit {
     const uint8_t *codes, *scales;
     const float *ts;                       // tensor scale or null
     const void *x;                         // [T] rows, x_stride values apart
@@ -62,10 +50,6 @@ struct LinearArgs {
     void *out;
     int T, N, K, dtype;                    // out's type
     int bf16;                              // x's type
-    int base, extra;                       // rows of a block: base, and one more in the first `extra` blocks
-    int passes, pass_rows, tile_rows;      // over a block's rows; rows a pass and a tile
-    int wk, wm, tiles;                     // warps that share K; groups of them, which share a pass's tiles; tiles a group
-    int ring;                              // stages of a warp's ring
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -217,7 +201,7 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) k_linear(LinearArgs a) {
             case 3: copy_wait<2>(); break;
             case 4: copy_wait<3>(); break;
             case 5: copy_wait<4>(); break;
-            default: copy_wait<kMaxRing - 1>(); break;
+            default: copy_wait<kMostLinearRing - 1>(); break;
         }
         __syncwarp();
     };
@@ -378,38 +362,16 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) k_linear(LinearArgs a) {
 template <bool MX, int NT> cudaError_t launch(LinearArgs a, cudaStream_t st) {
     const cudaError_t e = allow_smem<k_linear<MX, NT>>();
     if (e != cudaSuccess) return e;
-    constexpr size_t stage = kStageBytes<NT>, join = NT * 512;     // a tile's sums of a warp
-    constexpr int ring = 2;                                        // stages at least
-    const int stages = blocks_of(a.K, kStageK<NT>), groups = blocks_of(a.T, 8 * NT);
-    const int blocks = std::min(std::max(1, kSms / groups), a.N);
-    const int rows = blocks_of(a.N, blocks);
-    a.base = a.N / blocks;
-    a.extra = a.N % blocks;
-    // the split with the shortest longest share: stages, each taking its tokens (about three tiles of work) and its tiles
-    const int all = blocks_of(rows, kRows);
-    int best = INT_MAX;
-    for (int wk = std::min(stages, kWarps<NT>); wk >= 1; --wk) {
-        const int wm = std::min(kWarps<NT> / wk, all), cost = blocks_of(stages, wk) * (3 + blocks_of(all, wm));
-        if (cost < best) {
-            best = cost;
-            a.wk = wk;
-            a.wm = wm;
-        }
-    }
-    const int warps = a.wk * a.wm;
-    const int most = (int)((kSmem / warps - ring * stage) / join); // tiles of a warp in a pass
-    a.passes = blocks_of(rows, a.wm * most * kRows);
-    a.pass_rows = blocks_of(rows, a.passes);
-    a.tiles = blocks_of(a.pass_rows, a.wm * kRows);
-    a.tile_rows = blocks_of(a.pass_rows, a.wm * a.tiles);
-    a.ring = (int)std::min<size_t>(kMaxRing, (kSmem / warps - a.tiles * join) / stage);
-    return launch_pdl(k_linear<MX, NT>, dim3(blocks, groups), dim3(32 * warps), warps * (a.ring * stage + a.tiles * join), st, a);
+    static_cast<LinearSplit &>(a) = linear_split(NT, a.T, a.N, a.K);
+    return launch_pdl(k_linear<MX, NT>, dim3(a.blocks, a.groups), dim3(32 * a.wk * a.wm), a.smem, st, a);
 }
 
 template <bool MX> cudaError_t launch_format(const LinearArgs &a, cudaStream_t st) {
-    if (a.T <= 8) return launch<MX, 1>(a, st);
-    if (a.T <= 16) return launch<MX, 2>(a, st);
-    return launch<MX, 4>(a, st);
+    switch (linear_tokens(a.T)) {
+        case 1: return launch<MX, 1>(a, st);
+        case 2: return launch<MX, 2>(a, st);
+        default: return launch<MX, 4>(a, st);
+    }
 }
 
 moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }

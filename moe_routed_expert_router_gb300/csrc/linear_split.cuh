@@ -1,0 +1,67 @@
+// How a product of linear.cu is shared by blocks, warps and passes over a block's rows.  Plain C++: tests compile it
+// without CUDA and run it over the sizes.
+#pragma once
+
+#include <limits.h>
+
+#include <algorithm>
+
+#include "card.cuh"
+
+namespace moe {
+
+// Of a product whose blocks take 8 * nt tokens (nt 1, 2 or 4).
+constexpr int linear_tokens(int T) { return T <= 8 ? 1 : T <= 16 ? 2 : 4; }
+// Values of K a stage: 256, and half of it where 32 tokens have to share the registers.
+constexpr int linear_stage_k(int nt) { return nt >= 4 ? 128 : 256; }
+// Warps of a block: what the tokens' registers leave room for.
+constexpr int linear_warps(int nt) { return nt == 1 ? 16 : 12; }
+constexpr int kLinearRows = 16;            // rows a tile (32: 53.1 us for 1 x 100003 x 4096 against 47.1, the sums' place taken from the ring)
+constexpr int kScaleBytes = 16;            // a row's place for a stage's scales (MXFP4 uses half)
+constexpr int kCodePad = 16;               // behind a row's codes: eight rows' equal words lie in different banks
+constexpr int kLeastLinearRing = 2, kMostLinearRing = 6;
+// Bytes of a warp's stage of a tile, and of its sums of one.
+constexpr int linear_stage_bytes(int nt) { return kLinearRows * (linear_stage_k(nt) / 2 + kCodePad + kScaleBytes); }
+constexpr int linear_sum_bytes(int nt) { return nt * 512; }
+
+struct LinearSplit {
+    int blocks, groups;                    // blocks that share the rows, and groups of tokens: the grid
+    int base, extra;                       // rows of a block: base, and one more in the first `extra` blocks
+    int passes, pass_rows, tile_rows;      // over a block's rows; rows a pass and a tile
+    int wk, wm, tiles;                     // warps that share K; groups of them, which share a pass's tiles; tiles a group
+    int ring;                              // stages of a warp's ring
+    int smem;                              // bytes a block
+};
+
+inline LinearSplit linear_split(int nt, int T, int N, int K) {
+    const size_t stage = linear_stage_bytes(nt), join = linear_sum_bytes(nt);
+    const int most_warps = linear_warps(nt), stages = blocks_of(K, linear_stage_k(nt));
+    LinearSplit s{};
+    s.groups = blocks_of(T, 8 * nt);
+    s.blocks = std::min(std::max(1, kSms / s.groups), N);
+    const int rows = blocks_of(N, s.blocks);
+    s.base = N / s.blocks;
+    s.extra = N % s.blocks;
+    // the split with the shortest longest share: stages, each taking its tokens (about three tiles of work) and its tiles
+    const int all = blocks_of(rows, kLinearRows);
+    int best = INT_MAX;
+    for (int wk = std::min(stages, most_warps); wk >= 1; --wk) {
+        const int wm = std::min(most_warps / wk, all), cost = blocks_of(stages, wk) * (3 + blocks_of(all, wm));
+        if (cost < best) {
+            best = cost;
+            s.wk = wk;
+            s.wm = wm;
+        }
+    }
+    const int warps = s.wk * s.wm;
+    const int most = (int)((kSmemBlock / warps - kLeastLinearRing * stage) / join);    // tiles of a warp in a pass
+    s.passes = blocks_of(rows, s.wm * most * kLinearRows);
+    s.pass_rows = blocks_of(rows, s.passes);
+    s.tiles = blocks_of(s.pass_rows, s.wm * kLinearRows);
+    s.tile_rows = blocks_of(s.pass_rows, s.wm * s.tiles);
+    s.ring = (int)std::min<size_t>(kMostLinearRing, (kSmemBlock / warps - s.tiles * join) / stage);
+    s.smem = (int)(warps * (s.ring * stage + s.tiles * join));
+    return s;
+}
+
+}  // namespace moe

@@ -46,11 +46,10 @@ constexpr uint32_t kSfCol0 = 256;              // scales in tensor memory, behin
 constexpr int kSfStride = 48;                  // columns of a stage's: A0, A1, B
 constexpr int kThreads = 32 * 14;              // TMA, MMA, four scale warps, eight epilogue warps
 constexpr int kEpiWarp0 = 6;
-constexpr int kSms = 152;
 constexpr int kChunkTokens = 256;              // tokens a pair of launches
 constexpr int kMaxParts = 8;
 
-static_assert(kSmem <= kSmemSm - 2048, "the stages exceed a block's shared memory");
+static_assert(kSmem <= kSmemBlock, "the stages exceed a block's shared memory");
 
 // Where a call's workspace holds what; tiles of 16 tokens, groups of 256 rows.
 struct Layout {

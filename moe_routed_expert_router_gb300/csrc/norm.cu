@@ -450,7 +450,6 @@ RowShape row_shape(int n8, bool few, int two) {
 // Pieces a lane where a row takes a warp.
 int warp_pieces(int n8) { return n8 <= 32 ? 1 : n8 <= 64 ? 2 : 4; }
 
-constexpr int kSms = 152;
 template <int DT, int Q, bool kWarp>
 cudaError_t launch_norm_v(const NormArgs &a, int T, int threads, int v, cudaStream_t st) {
     const dim3 grid(kWarp ? blocks_of(T, kWarpRows) : T), block(kWarp ? 32 * kWarpRows : threads);
@@ -534,7 +533,7 @@ template <int DT> cudaError_t launch_norm_grad(const NormGradArgs &a, const Grad
     }
     if constexpr (f32) {
         if (v == 1) return launch_norm_grad_v<DT, 1, 2, false>(a, blocks, threads, stage, st);
-        if (2 * stage > kSmemSm - 2048) return launch_norm_grad_v<DT, 4, 1, false>(a, blocks, threads, stage, st);
+        if (2 * stage > kSmemBlock) return launch_norm_grad_v<DT, 4, 1, false>(a, blocks, threads, stage, st);
     }
     if (v == 2) return launch_norm_grad_v<DT, 2, 2, false>(a, blocks, threads, stage, st);
     return launch_norm_grad_v<DT, 4, 2, false>(a, blocks, threads, stage, st);

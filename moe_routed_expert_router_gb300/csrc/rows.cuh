@@ -4,6 +4,7 @@
 
 #include <mutex>
 
+#include "card.cuh"
 #include "moe_internal.cuh"
 
 namespace moe {
@@ -204,9 +205,7 @@ __device__ __forceinline__ void column_sums(const float *part, int blocks, int H
     }
 }
 
-constexpr size_t kSmemSm = 227 * 1024;   // shared memory of an SM that its blocks share
-
-// The kernel's dynamic shared-memory limit, set once a device.
+// The kernel's dynamic shared-memory limit, kSmemBlock, set once a device.
 template <auto Kernel> cudaError_t allow_smem() {
     static std::mutex mu;
     static bool done[kMaxDevices] = {};
@@ -216,13 +215,10 @@ template <auto Kernel> cudaError_t allow_smem() {
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
     if (done[dev]) return cudaSuccess;
-    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemSm - 2048);
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBlock);
     if (e == cudaSuccess) done[dev] = true;
     return e;
 }
-
-// Blocks for n rows, `each` of them a block; n may be the largest int.
-inline int blocks_of(int n, int each) { return n > 0 ? (n - 1) / each + 1 : 0; }
 
 inline bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline bool known_dtype(int32_t d) { return d == MOE_DTYPE_F32 || d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F16; }
