@@ -512,9 +512,9 @@ moe_status moe_head_norm_backward(const void *grad_q, int64_t grad_q_stride, con
  * arithmetic gives and leaves the other rows alone.  Sums are taken in a fixed order:
  * equal inputs give equal bits.  Waits inside a launch end after a second; if one ever
  * runs out, out is NaN.
- * K: a multiple of 128 up to 65536; x_stride: a multiple of 8, at least K; T: up
- * to 2^20, made for up to 64 (every 32 tokens, of large products every 16, read the
- * weight once, the later ones from cache).  T = 0 is a no-op. */
+ * N: up to 2^31 - 1025; K: a multiple of 128 up to 65536; x_stride: a multiple of
+ * 8, at least K; T: up to 2^20, made for up to 64 (every 32 tokens, of large products
+ * every 16, read the weight once, the later ones from cache).  T = 0 is a no-op. */
 size_t moe_linear_fp4_workspace(int32_t weight_format, int32_t T, int32_t N, int32_t K);
 moe_status moe_linear_fp4(const void *x, int64_t x_stride, const moe_nvfp4 *weight, int32_t weight_format, int32_t T,
                           int32_t N, int32_t K, int32_t dtype, int32_t out_dtype, void *out, void *workspace,

@@ -132,18 +132,12 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) k_linear(LinearArgs a) {
     const int g = lane >> 2, t = lane & 3;
     const int wm = warp / a.wk, wk = warp - wm * a.wk;
     const int token0 = blockIdx.y * (8 * NT), tokens = min(8 * NT, a.T - token0);
-    const int row0 = (int)blockIdx.x * a.base + min((int)blockIdx.x, a.extra), row1 = row0 + a.base + ((int)blockIdx.x < a.extra);
+    const RowRange rows_here = linear_block_rows(a, blockIdx.x);
     uint8_t *ring = smem + warp * a.ring * kStage;
     float4 *red = reinterpret_cast<float4 *>(smem + a.wk * a.wm * a.ring * kStage);   // [warp][tile][NT][lane]
     const int stages = (a.K + SK - 1) / SK;
     const int64_t code_row = a.K / 2, scale_row = a.K / (MX ? 32 : 16);
 
-    // rows of this warp's j-th tile in a pass: first and end
-    auto tile_rows = [&](int pass, int j, int &n0, int &n1) {
-        const int end = min(row0 + (pass + 1) * a.pass_rows, row1);
-        n0 = min(row0 + pass * a.pass_rows + (wm * a.tiles + j) * a.tile_rows, end);
-        n1 = min(n0 + a.tile_rows, end);
-    };
     // The stream of this warp: pass, stage, tile.  A lane copies one 16-byte unit of every kLoadRows-th row and a piece of
     // a row's scales; rows that are not there are left out, for no result that is stored uses them.
     constexpr int kLoadRows = 32 / kUnits, kScalePiece = MX ? 4 : 8, kPieces = kUnits / 4;
@@ -153,9 +147,10 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) k_linear(LinearArgs a) {
     int lp = 0, ls = wk, lj = 0, fill = 0, left = 0;                         // rows left in the warp's share of the pass
     const uint8_t *code_at = nullptr, *scale_at = nullptr;
     auto stream_at = [&]() {               // the first tile of pass lp and stage ls
-        int n0, n1;
-        tile_rows(lp, 0, n0, n1);
-        left = min(row0 + (lp + 1) * a.pass_rows, row1) - n0;
+        if (lp == a.passes) return;
+        const RowRange pass = linear_pass_rows(a, rows_here, lp);
+        const int n0 = linear_tile_rows(a, pass, wm * a.tiles).first;
+        left = pass.end - n0;
         code_at = a.codes + (n0 + load_row) * code_row + ls * (SK / 2) + 16 * load_unit;
         scale_at = a.scales + (n0 + scale_lane_row) * scale_row + ls * (kPieces * kScalePiece) + scale_piece * kScalePiece;
     };
@@ -337,18 +332,18 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) k_linear(LinearArgs a) {
         }
         // join the sums of the group's warps in order
         group_sync(wm, a.wk);
+        const RowRange there = linear_pass_rows(a, rows_here, pass);
         const float *all = reinterpret_cast<const float *>(red + wm * a.wk * a.tiles * (NT * 32));
         for (int i = wk * 32 + lane; i < a.tiles * kRows * tokens; i += 32 * a.wk) {
             const int row = i % kRows, tok = i / kRows % tokens, j = i / kRows / tokens;
-            int n0, n1;
-            tile_rows(pass, j, n0, n1);
-            if (n0 + row >= n1) continue;
+            const RowRange tile = linear_tile_rows(a, there, wm * a.tiles + j);
+            if (tile.first + row >= tile.end) continue;
             const float *p = all + ((j * NT + (tok >> 3)) * 32 + (row & 7) * 4 + ((tok & 7) >> 1)) * 4 + (row >> 3) * 2 + (tok & 1);
             float s = 0.0f;
 #pragma unroll 4
             for (int w = 0; w < a.wk; ++w) s += p[w * a.tiles * (NT * 128)];
             s *= ts;
-            const int64_t at = (int64_t)(token0 + tok) * a.N + n0 + row;
+            const int64_t at = (int64_t)(token0 + tok) * a.N + tile.first + row;
             if (a.dtype == MOE_DTYPE_F32) static_cast<float *>(a.out)[at] = s;
             else if (a.dtype == MOE_DTYPE_BF16) static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(s);
             else static_cast<__half *>(a.out)[at] = __float2half_rn(s);

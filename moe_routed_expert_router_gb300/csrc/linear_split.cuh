@@ -8,6 +8,12 @@
 
 #include "card.cuh"
 
+#ifdef __CUDACC__
+#define MOE_BOTH __host__ __device__
+#else
+#define MOE_BOTH
+#endif
+
 namespace moe {
 
 // Of a product whose blocks take 8 * nt tokens (nt 1, 2 or 4).
@@ -57,11 +63,34 @@ inline LinearSplit linear_split(int nt, int T, int N, int K) {
     const int most = (int)((kSmemBlock / warps - kLeastLinearRing * stage) / join);    // tiles of a warp in a pass
     s.passes = blocks_of(rows, s.wm * most * kLinearRows);
     s.pass_rows = blocks_of(rows, s.passes);
+    s.passes = blocks_of(rows, s.pass_rows);       // rounding up may have emptied the last ones
     s.tiles = blocks_of(s.pass_rows, s.wm * kLinearRows);
     s.tile_rows = blocks_of(s.pass_rows, s.wm * s.tiles);
     s.ring = (int)std::min<size_t>(kMostLinearRing, (kSmemBlock / warps - s.tiles * join) / stage);
     s.smem = (int)(warps * (s.ring * stage + s.tiles * join));
     return s;
+}
+
+// Rows `first` up to `end`.
+struct RowRange {
+    int first, end;
+};
+
+// Rows of a block.
+MOE_BOTH inline RowRange linear_block_rows(const LinearSplit &s, int block) {
+    const int first = block * s.base + std::min(block, s.extra);
+    return {first, first + s.base + (block < s.extra)};
+}
+
+// Rows of a block's pass, and of tile `tile` (of wm * tiles) of those.  Only lengths are compared and added up to where
+// rows are: a pass that there is starts at most at the block's end, so nothing passes 32 bits for the largest N.
+MOE_BOTH inline RowRange linear_pass_rows(const LinearSplit &s, RowRange block, int pass) {
+    const int first = block.first + std::min(pass * s.pass_rows, block.end - block.first);
+    return {first, first + std::min(s.pass_rows, block.end - first)};
+}
+MOE_BOTH inline RowRange linear_tile_rows(const LinearSplit &s, RowRange pass, int tile) {
+    const int first = pass.first + std::min(tile * s.tile_rows, pass.end - pass.first);
+    return {first, first + std::min(s.tile_rows, pass.end - first)};
 }
 
 }  // namespace moe
