@@ -8,7 +8,9 @@
 // each of which E2M1 holds: what is dropped is at most 2^(e - 22).  Sixteen tokens are 128 columns of the MMA, a column a
 // digit, and a digit's power of eight is its column's block scale.  Adding octal 44444444 to the integer makes its digits
 // d + 4, all from 0 to 7, so no digit waits for another's carry.
-//   E8M0 holds every such power.  E4M3 holds 2^-9 to 2^8, so for NVFP4 a token's largest value is brought to [2^7, 2^8),
+//   E8M0 holds every such power, so MXFP4 takes a token's values as they are; only a token below 2^-20 is brought there, so
+// that its smallest digits have a power too (a block below 2^-106 is written as if it were that).  A column's sum then passes
+// fp32 only where the result does: 65536 values of 2^-20 times 6 * 2^127 stay below 2^127.  E4M3 holds 2^-9 to 2^8, so for NVFP4 a token's largest value is brought to [2^7, 2^8),
 // columns 0-3 have scales of 2^8 down, columns 4-7 of 2^12 times their own, and the epilogue adds those sums times 2^-12;
 // a block whose largest value is below 2^-9 of the token's is written as if it were that, to 2^-30 of it.
 //   Infinities and NaNs count as zeros in the digits; the epilogue of a token that holds some adds their products.
@@ -48,6 +50,7 @@ constexpr int kThreads = 32 * 14;              // TMA, MMA, four scale warps, ei
 constexpr int kEpiWarp0 = 6;
 constexpr int kChunkTokens = 256;              // tokens a pair of launches
 constexpr int kMaxParts = 8;
+constexpr int kLeastMx = -20;                  // the least exponent of a token's largest value, MXFP4
 
 static_assert(kSmem <= kSmemBlock, "the stages exceed a block's shared memory");
 
@@ -122,9 +125,10 @@ template <bool MX> __global__ void __launch_bounds__(128) k_linear_digits(DigitA
     if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
     bad = __syncthreads_or(bad);
     const int E = exponent_of(fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])));
-    const float up = scale_up(E), more = scale_more(E);
-    // sums are of values below 2^8; NVFP4's scales are twice a digit's weight
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.info[t] = make_float2(scale_down(E) * (MX ? 1.0f : 0.5f), bad ? 1.0f : 0.0f);
+    const int lift = MX ? max(0, kLeastMx - E) : 0;
+    const float up = MX ? power_of_two(lift) : scale_up(E), more = MX ? 1.0f : scale_more(E);
+    // what undoes it; NVFP4's scales are twice a digit's weight
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.info[t] = make_float2(MX ? power_of_two(-lift) : scale_down(E) * 0.5f, bad ? 1.0f : 0.0f);
 
     m = 0.0f;
 #pragma unroll
@@ -136,7 +140,7 @@ template <bool MX> __global__ void __launch_bounds__(128) k_linear_digits(DigitA
     for (int o = 1; o < kLanes; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (at >= a.K) return;                     // K is a multiple of a warp's 256 values
     const int lane = threadIdx.x & 31;
-    const int e = max(exponent_of(m), MX ? -93 : -1);      // at most 7
+    const int e = max(exponent_of(m), MX ? -106 : -1);     // at most 127, NVFP4 7
     const float fixed = power_of_two(21 - e);
     // digits of a value in the nibbles of a word: 24 bits spread to 32 in three steps (what strays into a nibble's fourth
     // bit is cleared at the end)

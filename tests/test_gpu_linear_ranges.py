@@ -10,7 +10,7 @@ from test_gpu_linear import BF, F16, F32, a_weight, rows
 
 pytestmark = pytest.mark.gpu
 
-KERNELS = [(5, "small"), (12, "small"), (20, "small")]
+KERNELS = [(5, "small"), (12, "small"), (20, "small"), (20, "large"), (6, "large")]
 
 
 def shape(T, kernel, fmt):
