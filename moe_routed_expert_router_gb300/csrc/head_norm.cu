@@ -222,8 +222,8 @@ __device__ __forceinline__ void over_row(float &v, float &w, int lg) {
     }
 }
 
-// U rows a thread at once, all loads ahead of their use.
-template <int DT, bool kPairs, int U>
+// U rows a thread at once, all loads ahead of their use.  kRest: R < D, some values are not rotated.
+template <int DT, bool kPairs, int U, bool kRest>
 __global__ void __launch_bounds__(kThreads) k_head_norm(HeadArgs a) {
     using T = typename RowType<DT>::T;
     extern __shared__ __align__(16) float cs[];
@@ -254,16 +254,21 @@ __global__ void __launch_bounds__(kThreads) k_head_norm(HeadArgs a) {
     // a' = rstd (a (cos wa) - b (sin wb)),  b' = rstd (b (cos wb) + a (sin wa))
     float wa[8], wb[8], ca[8], cb[8], sa[8], sb[8];
     {
-        const Angles r = angles_of<DT, kPairs>(a, l, cs, n);
         to_planes<DT, kPairs>(wr, wa, wb);
+        const Angles r = angles_of<DT, kPairs>(a, l, cs, n);
         mul8(ca, wa, r.c);
         mul8(cb, wb, r.c);
         mul8(sa, wa, r.s);
         mul8(sb, wb, r.s);
         scale8(sb, -1.0f);
+        if (kRest && !l.turned) {          // whatever the weight is
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sa[i] = sb[i] = 0.0f;
+        }
     }
     for (int base = 0; base < h.heads; base += U * l.heads) {
         if (base > 0) fetch();
+        float least = 1.0f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float va[8], vb[8], ya[8], yb[8], sum[2] = {};
@@ -274,6 +279,7 @@ __global__ void __launch_bounds__(kThreads) k_head_norm(HeadArgs a) {
             over_row(mean, a.lg);
             if (u < left) {
                 const float rstd = rsqrtf(fmaf(mean, a.inv_d, a.eps));
+                if constexpr (kRest) least = fminf(least, rstd);
                 mul8(ya, va, ca);
                 fma8(ya, vb, sb);
                 mul8(yb, vb, cb);
@@ -281,6 +287,27 @@ __global__ void __launch_bounds__(kThreads) k_head_norm(HeadArgs a) {
                 scale8(ya, rstd);
                 scale8(yb, rstd);
                 store_planes<DT, kPairs>(to + u * pitch, l, ya, yb);
+            }
+        }
+        // A row with an infinity has an rstd of 0.  Where values are not rotated, 0 (a sine) times the infinity has reached
+        // its place's other value above; they are written again, each by itself: 0, the infinity's own NaN.  (4096 x 40 heads
+        // of 128, 64 turned: 16.9 us, without this 16.5; with a branch around the sines' products instead 18.8.  Rows that are
+        // rotated whole have no such values.)
+        if (kRest && least == 0.0f && !l.turned) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float va[8], vb[8];
+#pragma unroll
+                for (int w = 0; w < kWords<DT>; ++w)                // widened anew: kept from above they took 114 registers
+                    asm volatile("" : "+r"(x[u].w[w].x), "+r"(x[u].w[w].y), "+r"(x[u].w[w].z), "+r"(x[u].w[w].w));
+                to_planes<DT, kPairs>(x[u], va, vb);
+                bool infinite = false;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) infinite |= isinf(va[i]) || isinf(vb[i]);
+                if (!infinite || u >= left) continue;
+                scale8(va, 0.0f);
+                scale8(vb, 0.0f);
+                store_planes<DT, kPairs>(to + u * pitch, l, va, vb);
             }
         }
         to += U * pitch;
@@ -380,9 +407,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_head_norm_backward(HeadArgs a) 
                 float ga[8], gb[8];
                 to_planes<DT, kPairs>(g, ga, gb);
                 mul8(fa, ga, r.c);         // turned back
-                fma8(fa, gb, r.s);
                 mul8(fb, gb, r.c);
-                fma8(fb, ga, minus);
+                if (l.turned) {            // else a and b are no pair: 0 times an infinity would reach the other
+                    fma8(fa, gb, r.s);
+                    fma8(fb, ga, minus);
+                }
             }
             to_planes<DT, kPairs>(x, va, vb);
             dot8(sum, va, va);
@@ -482,7 +511,7 @@ bool one_each(const HeadArgs &a) { return a.q.blocks == 1 && a.k.blocks == 1; } 
 
 template <int DT, bool kPairs> cudaError_t launch_forward(const HeadArgs &a, cudaStream_t st) {
     constexpr int U = DT == MOE_DTYPE_F32 ? 1 : 2;
-    return launch_pdl(k_head_norm<DT, kPairs, U>, dim3(a.q.blocks + a.k.blocks), dim3(kThreads), angle_bytes(a), st, a);
+    return launch_pdl(a.R < a.D ? k_head_norm<DT, kPairs, U, true> : k_head_norm<DT, kPairs, U, false>, dim3(a.q.blocks + a.k.blocks), dim3(kThreads), angle_bytes(a), st, a);
 }
 
 template <int DT, bool kPairs> cudaError_t launch_backward(const HeadArgs &a, cudaStream_t st) {
