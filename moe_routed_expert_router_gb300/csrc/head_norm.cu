@@ -307,6 +307,8 @@ __global__ void __launch_bounds__(kThreads) k_head_norm(HeadArgs a) {
                 if (!infinite || u >= left) continue;
                 scale8(va, 0.0f);
                 scale8(vb, 0.0f);
+                mul8(va, va, ca);
+                mul8(vb, vb, cb);
                 store_planes<DT, kPairs>(to + u * pitch, l, va, vb);
             }
         }
@@ -511,7 +513,8 @@ bool one_each(const HeadArgs &a) { return a.q.blocks == 1 && a.k.blocks == 1; } 
 
 template <int DT, bool kPairs> cudaError_t launch_forward(const HeadArgs &a, cudaStream_t st) {
     constexpr int U = DT == MOE_DTYPE_F32 ? 1 : 2;
-    return launch_pdl(a.R < a.D ? k_head_norm<DT, kPairs, U, true> : k_head_norm<DT, kPairs, U, false>, dim3(a.q.blocks + a.k.blocks), dim3(kThreads), angle_bytes(a), st, a);
+    return launch_pdl(a.R < a.D ? k_head_norm<DT, kPairs, U, true> : k_head_norm<DT, kPairs, U, false>, dim3(a.q.blocks + a.k.blocks),
+                      dim3(kThreads), angle_bytes(a), st, a);
 }
 
 template <int DT, bool kPairs> cudaError_t launch_backward(const HeadArgs &a, cudaStream_t st) {

@@ -68,3 +68,16 @@ def test_an_infinite_weight(D, R, pairs):
     out = moe.head_norm(q, k, qw, kw, pos, moe.rotary_turns(R), interleaved=pairs, eps=EPS)["q"]
     want = rotate(normed(q)[0] * qw.double(), pos, R, pairs)[0]
     assert torch.equal(out.isfinite(), want.isfinite())
+
+
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("D,R", SHAPES)
+def test_an_infinite_weight_in_a_row_with_an_infinity(D, R, pairs):
+    """0 times the infinite weight is a NaN there as well."""
+    q, k, qw, kw, pos = inputs(D, 2, 1, D, torch.float32, D + R)
+    t = torch.arange(D, device="cuda")
+    q[t, 1, t] = INF
+    qw[D - 1], qw[D // 2] = INF, float("nan")
+    out = moe.head_norm(q, k, qw, kw, pos, moe.rotary_turns(R), interleaved=pairs, eps=EPS)["q"]
+    want = rotate(normed(q)[0] * qw.double(), pos, R, pairs)[0]
+    assert torch.equal(out[:, 1].isnan(), want[:, 1].isnan())
