@@ -508,7 +508,7 @@ moe_status moe_head_norm_backward(const void *grad_q, int64_t grad_q_stride, con
  * 256 (128 for more than 16 tokens) values.  Large ones, those that want a workspace,
  * take rows as integers of 23 bits: to within 2^-22 of the largest finite magnitude
  * of the 16 (MXFP4: 32) values that share a weight's scale or, where that is more, for
- * NVFP4 2^-30 of the row's, for MXFP4 2^-108 of the row's and at most 2^-128.  A row that holds an infinity or a NaN gives what fp32
+ * NVFP4 2^-39 of the row's, for MXFP4 2^-108 of the row's and at most 2^-128.  A row that holds an infinity or a NaN gives what fp32
  * arithmetic gives and leaves the other rows alone.  Sums are taken in a fixed order:
  * equal inputs give equal bits.  Waits inside a launch end after a second; if one ever
  * runs out, out is NaN.

@@ -6,13 +6,14 @@
 // integers of 23 bits in eight balanced octal digits,
 //   x = 2^(e - 21) * (d0 * 8^7 + d1 * 8^6 + ... + d7),      -4 <= d <= 3,      largest |x| < 2^(e + 1),
 // each of which E2M1 holds: what is dropped is at most 2^(e - 22).  Sixteen tokens are 128 columns of the MMA, a column a
-// digit, and a digit's power of eight is its column's block scale.  Adding octal 44444444 to the integer makes its digits
-// d + 4, all from 0 to 7, so no digit waits for another's carry.
-//   E8M0 holds every such power, so MXFP4 takes a token's values as they are; only a token below 2^-20 is brought there, so
-// that its smallest digits have a power too (a block below 2^-106 is written as if it were that).  A column's sum then passes
-// fp32 only where the result does: 65536 values of 2^-20 times 6 * 2^127 stay below 2^127.  E4M3 holds 2^-9 to 2^8, so for NVFP4 a token's largest value is brought to [2^7, 2^8),
-// columns 0-3 have scales of 2^8 down, columns 4-7 of 2^12 times their own, and the epilogue adds those sums times 2^-12;
-// a block whose largest value is below 2^-9 of the token's is written as if it were that, to 2^-30 of it.
+// digit.  Adding octal 44444444 to the integer makes its digits d + 4, all from 0 to 7, so no digit waits for another's carry.
+//   The columns' block scales give a block its power.  E4M3 holds 2^-9 to 2^8, so NVFP4 brings a token's largest value to
+// [2^7, 2^8), gives a block's eight columns the one scale of 2^(e + 1), and the epilogue adds their sums with factors of 8^-i:
+// a block whose largest value is below 2^-17 of the token's is written as if it were that, to 2^-39 of it.  (With the powers
+// of eight in the scales as well that was 2^-30.)
+//   E8M0 holds the powers of eight too, so MXFP4 has them in the scales and takes a token's values as they are; only a token
+// below 2^-20 is brought there, so that its smallest digits have a power (a block below 2^-106 is written as if it were
+// that).  A column's sum then passes fp32 only where the result does: 65536 values of 2^-20 times 6 * 2^127 stay below 2^127.
 //   Infinities and NaNs count as zeros in the digits; the epilogue of a token that holds some adds their products.
 //
 // Two launches: k_linear_digits writes the digits and scales (8 x 4.5 bits a value), k_linear_tc multiplies; its blocks load
@@ -140,7 +141,7 @@ template <bool MX> __global__ void __launch_bounds__(128) k_linear_digits(DigitA
     for (int o = 1; o < kLanes; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (at >= a.K) return;                     // K is a multiple of a warp's 256 values
     const int lane = threadIdx.x & 31;
-    const int e = max(exponent_of(m), MX ? -106 : -1);     // at most 127, NVFP4 7
+    const int e = max(exponent_of(m), MX ? -106 : -10);    // at most 127, NVFP4 7
     const float fixed = power_of_two(21 - e);
     // digits of a value in the nibbles of a word: 24 bits spread to 32 in three steps (what strays into a nibble's fourth
     // bit is cleared at the end)
@@ -184,7 +185,7 @@ template <bool MX> __global__ void __launch_bounds__(128) k_linear_digits(DigitA
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
         const int eb = __shfl_sync(0xffffffffu, e, from + kLanes * b);
-        word |= (MX ? (uint32_t)(127 + eb - 3 * d) : e4m3_power(eb + 1 - 3 * d + (d >= 4 ? 12 : 0))) << (8 * b);
+        word |= (MX ? (uint32_t)(127 + eb - 3 * d) : e4m3_power(eb + 1)) << (8 * b);
     }
     uint8_t *scales = a.scales + ((int64_t)tile * a.atoms + at / (32 * kLanes)) * 512 + (r0 & 31) * 16 + (r0 >> 5) * 4;
     if (!MX || (lane & 8) == 0) *reinterpret_cast<uint32_t *>(scales + d * 16) = word;
@@ -460,9 +461,10 @@ template <bool MX> __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(co
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
                             const float *u = v + 8 * q;
-                            const float low = ((u[7] + u[6]) + u[5]) + u[4];
-                            sum[h][2 * c + q] = MX ? (((low + u[3]) + u[2]) + u[1]) + u[0]
-                                                   : fmaf(low, 0x1p-12f, ((u[3] + u[2]) + u[1]) + u[0]);
+                            float all = u[7];
+#pragma unroll
+                            for (int d = 6; d >= 0; --d) all = MX ? all + u[d] : fmaf(all, 0.125f, u[d]);
+                            sum[h][2 * c + q] = all;
                         }
                     }
             }
