@@ -264,7 +264,11 @@ template <bool MX> __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(co
     uint64_t *drain = acc_empty + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     int *err = reinterpret_cast<int *>(tmem_slot + 1);   // this block's
-    uint64_t *joined = drain + 2;              // every part's sums are there
+    // Every part's sums of an item are there: two barriers in turn.  A part that is ahead may arrive for its next item before
+    // another's arrival for this one has come to this block (it came to that part first), and would complete the phase in
+    // its place.  An arrival for the item after next is behind the other's for the next one, which that issued behind all of
+    // its arrivals for this.
+    uint64_t *joined = drain + 2;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int items = a.tiles * a.groups, first = blockIdx.x / a.parts, step = gridDim.x / a.parts;
@@ -280,6 +284,7 @@ template <bool MX> __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(co
         mbar_init(acc_empty, 8);
         mbar_init(drain, 1);
         mbar_init(joined, a.parts);
+        mbar_init(joined + 1, a.parts);
         *err = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -435,7 +440,7 @@ template <bool MX> __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(co
         const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2;
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + 64 * half;
         const bool busy = 64 * half < a.rows;
-        uint32_t aph = 0, jph = 0;
+        uint32_t aph = 0, turn = 0;
         bool ok = true;
         float ts = 1.0f;
         pdl_wait();
@@ -500,10 +505,10 @@ template <bool MX> __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(co
                 const int tid = threadIdx.x - 32 * kEpiWarp0;
                 if (tid < a.parts) {
                     __threadfence();
-                    arrive_at(joined, tid);
+                    arrive_at(joined + (turn & 1), tid);
                 }
-                if (!mbar_wait_cluster(joined, jph, err)) ok = false;
-                jph ^= 1;
+                if (!mbar_wait_cluster(joined + (turn & 1), turn >> 1 & 1, err)) ok = false;
+                ++turn;
                 // this block's rows of the 256 (parts is a power of two): element e is row e % rows of token e / rows, sixteen loads a thread
                 const int lp = 31 - __clz(a.parts), rows = 256 >> lp, all = min(kTileTokens, a.T - it.tile * kTileTokens);
                 const float *from = a.partial + (int64_t)it.tile * kTileTokens * a.N;
