@@ -208,8 +208,11 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) k_linear(LinearArgs a) {
     // A stage's tokens: unit u's values 8 t .. 8 t + 7 of token 8 n + g (a column without one takes the last: its sums are
     // not stored), and the scales of the sums' columns 2 t and 2 t + 1.
     uint4 x[NT][kUnits];
-    float undo[NT][2];
-    uint32_t rest[NT];                     // MXFP4: `undo` goes with the scales, and what is left of it, a pair of bf16 powers, with the sum
+    // Of the power that gives a sum its size back, two factors: `undo`, which MXFP4 has with the scales, and what is left of it,
+    // a pair of bf16 powers, with the sum.  NVFP4's bf16 tokens have the tensor scale's power in it too.
+    float undo[NT][2], ts = 1.0f;
+    uint32_t rest[NT];
+    int more_power = 0;
     auto take_tokens = [&](int stage) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -237,14 +240,12 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) k_linear(LinearArgs a) {
                 const float up = scale_up(e), more = scale_more(e);
 #pragma unroll
                 for (int u = 0; u < kUnits; ++u) x[n][u] = scaled8(x[n][u], up, more);
-                const int with_scale = max(-kScaleShift, min(0, e - 7));
-                const float down = MX ? power_of_two(with_scale) : scale_down(e);
-                undo[n][0] = __shfl_sync(0xffffffffu, down, 8 * t);
-                undo[n][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
-                if constexpr (MX) {
-                    const uint32_t left_over = __float_as_uint(power_of_two(e - 7 - with_scale));
-                    rest[n] = __shfl_sync(0xffffffffu, left_over, 8 * t) >> 16 | __shfl_sync(0xffffffffu, left_over, 8 * t + 4);
-                }
+                const int power = e - 7 + more_power, with_scale = max(-kScaleShift, min(0, power));
+                const float first = MX ? power_of_two(with_scale) : first_factor(power);
+                undo[n][0] = __shfl_sync(0xffffffffu, first, 8 * t);
+                undo[n][1] = __shfl_sync(0xffffffffu, first, 8 * t + 4);
+                const uint32_t second = __float_as_uint(MX ? power_of_two(power - with_scale) : second_factor(power));
+                rest[n] = __shfl_sync(0xffffffffu, second, 8 * t) >> 16 | __shfl_sync(0xffffffffu, second, 8 * t + 4);
             }
         }
     };
@@ -253,9 +254,13 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) k_linear(LinearArgs a) {
     pdl_wait();
     for (int i = 0; i < a.ring - 1; ++i) load_next();
     pdl_trigger();
-    take_tokens(wk);
-    float ts = 1.0f;
     if (a.ts) ts = *a.ts;
+    if (!MX && a.bf16) {
+        const TensorScale split = split_scale(ts);
+        more_power = split.power;
+        ts = split.rest;
+    }
+    take_tokens(wk);
     const uint32_t scale_bytes = t >> 1 ? 0x3311 : 0x2200;
     float4 *mine = red + warp * a.tiles * (NT * 32) + lane;
     const bool one_stage = wk + a.wk >= stages;
@@ -335,7 +340,11 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) k_linear(LinearArgs a) {
                     for (int c = 1; c < kChains; ++c)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) acc[n][0][i] += acc[n][c][i];
-                    const float u0 = MX ? __uint_as_float(rest[n] << 16) : undo[n][0], u1 = MX ? __uint_as_float(rest[n] & 0xFFFF0000u) : undo[n][1];
+                    const float u0 = __uint_as_float(rest[n] << 16), u1 = __uint_as_float(rest[n] & 0xFFFF0000u);
+                    if constexpr (!MX) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[n][0][i] *= undo[n][i & 1];
+                    }
                     s.x = fmaf(acc[n][0][0], u0, s.x);
                     s.y = fmaf(acc[n][0][1], u1, s.y);
                     s.z = fmaf(acc[n][0][2], u0, s.z);

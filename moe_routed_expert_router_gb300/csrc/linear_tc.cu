@@ -70,7 +70,7 @@ struct TcArgs {
     int64_t x_stride;
     void *out;
     float *partial;                            // [part][T][N]
-    const float2 *info;                        // a token's factor, and 1 where it holds infinities or NaNs
+    const int2 *info;                          // a token's power of two, and 1 where it holds infinities or NaNs
     int T, N, K, bf16, dtype;
     int tiles, groups, parts, stages, atoms, rows;
 };
@@ -79,7 +79,7 @@ struct DigitArgs {
     const void *x;
     int64_t x_stride;
     uint8_t *codes, *scales;
-    float2 *info;
+    int2 *info;
     int T, K, bf16, atoms;
 };
 
@@ -129,7 +129,7 @@ template <bool MX> __global__ void __launch_bounds__(128) k_linear_digits(DigitA
     const int lift = MX ? max(0, kLeastMx - E) : 0;
     const float up = MX ? power_of_two(lift) : scale_up(E), more = MX ? 1.0f : scale_more(E);
     // what undoes it; NVFP4's scales are twice a digit's weight
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.info[t] = make_float2(MX ? power_of_two(-lift) : scale_down(E) * 0.5f, bad ? 1.0f : 0.0f);
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.info[t] = make_int2(MX ? -lift : E - 8, bad);
 
     m = 0.0f;
 #pragma unroll
@@ -444,13 +444,19 @@ template <bool MX> __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(co
         bool ok = true;
         float ts = 1.0f;
         pdl_wait();
-        if (a.ts) ts = *a.ts;
+        int power = 0;                     // the tensor scale's
+        if (a.ts) {
+            const TensorScale split = split_scale(*a.ts);
+            power = split.power;
+            ts = split.rest;
+        }
         for (int i = first; i < items; i += step) {
             const Item it = item_at(a, i);
             const int t0 = it.tile * kTileTokens + 8 * half, tokens = busy ? min(8, a.T - t0) : 0;
             const int n0 = it.group * 256 + quad * 32 + lane;
-            float2 info = make_float2(0.0f, 0.0f);                 // lane j: token j's
+            int2 info = make_int2(0, 0);                           // lane j: token j's
             if (lane < tokens) info = a.info[t0 + lane];
+            const float own_first = first_factor(info.x + power), own_second = second_factor(info.x + power);
             if (ok) ok = mbar_wait(acc_full, aph, err);
             aph ^= 1;
             tc_fence_after();
@@ -478,11 +484,11 @@ template <bool MX> __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(co
             if (lane == 0) mbar_arrive(acc_empty);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float factor = __shfl_sync(0xffffffffu, info.x, j);
-                const bool bad = __shfl_sync(0xffffffffu, info.y, j) != 0.0f;
+                const float first = __shfl_sync(0xffffffffu, own_first, j), second = __shfl_sync(0xffffffffu, own_second, j);
+                const bool bad = __shfl_sync(0xffffffffu, info.y, j) != 0;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    sum[h][j] = ok ? sum[h][j] * factor : NAN;
+                    sum[h][j] = ok ? sum[h][j] * first * second : NAN;
                     if (bad && j < tokens && n0 + 128 * h < a.N)
                         sum[h][j] += beyond<MX>(a, t0 + j, n0 + 128 * h, k0 * kBK, k1 * kBK);
                 }
@@ -571,7 +577,7 @@ Layout layout_of(bool mx, int T, int N, int K) {
     };
     l.codes = take((size_t)l.tiles * 128 * (K / 2));
     l.scales = take((size_t)l.tiles * l.atoms * 512);
-    l.info = take((size_t)T * sizeof(float2));
+    l.info = take((size_t)T * sizeof(int2));
     l.partial = take(l.parts > 1 ? (size_t)l.parts * T * N * sizeof(float) : 0);
     l.bytes = at;
     return l;
@@ -585,7 +591,7 @@ template <bool MX> cudaError_t launch_chunk(const LinearCall &c, cudaStream_t st
     t.x_stride = c.x_stride;
     t.codes = ws + l.codes;
     t.scales = ws + l.scales;
-    t.info = reinterpret_cast<float2 *>(ws + l.info);
+    t.info = reinterpret_cast<int2 *>(ws + l.info);
     t.T = c.T;
     t.K = c.K;
     t.bf16 = c.dtype == MOE_DTYPE_BF16;

@@ -64,3 +64,48 @@ def test_mxfp4_largest_scales_over_codes_of_zero(T, kernel):
     assert out.isfinite().all()
     w.codes.view(N, K // 32, 16)[:, 3::4] = 0x88                  # negative ones
     assert torch.equal(moe.linear_fp4(x, w, out_dtype=F32), out)
+
+
+# rows, tensor scale: a sum without the tensor scale passes fp32's largest number, or falls below its smallest normal one
+@pytest.mark.parametrize("exponent,ts", [(117, 1.3e-7), (117, 2.0 ** -126), (112, -3e-9), (-116, 1.7e9), (-126, 2.0 ** 100), (0, 1e-45), (0, 0.0)])
+@pytest.mark.parametrize("T,kernel", KERNELS)
+def test_nvfp4_tensor_scales_of_any_size(T, kernel, exponent, ts):
+    N, K = shape(T, kernel, "nvfp4")
+    w = a_weight(N, K, "nvfp4", 3)
+    w.ts.fill_(ts)
+    if exponent < 0:
+        w.scales.fill_(0x08)                                      # 2^-6
+    x = (rows(T, K, F32, 10).double() * 2.0 ** exponent).to(BF)
+    check(kernel, moe.linear_fp4(x, w, out_dtype=F32), x, w)
+
+
+@pytest.mark.parametrize("exponent,ts", [(-126, 2.0 ** 110), (-130, 1.1 * 2.0 ** 127), (-60, 2.0 ** 60), (118, -2.0 ** -149), (119, 2.0 ** -140), (-100, 2.0 ** -40)])
+@pytest.mark.parametrize("T,kernel", KERNELS)
+def test_nvfp4_tensor_scales_over_the_least_and_largest_blocks(T, kernel, exponent, ts):
+    """Scales of 2^-9 below rows that are small, of 448 above large ones, codes of every size."""
+    N, K = shape(T, kernel, "nvfp4")
+    w = a_weight(N, K, "nvfp4", 4)
+    w.ts.fill_(ts)
+    w.scales.fill_(0x01 if exponent < 0 else 0x7E)
+    x = (torch.randn(T, K, generator=torch.Generator(device="cuda").manual_seed(T), device="cuda").double() * 2.0 ** exponent).to(BF)
+    check(kernel, moe.linear_fp4(x, w, out_dtype=F32), x, w)
+
+
+@pytest.mark.parametrize("exponent,ts", [(-109, 2.0 ** -20), (-118, 1.0), (-100, 1.7 * 2.0 ** -28)])
+@pytest.mark.parametrize("T,kernel", KERNELS)
+def test_nvfp4_results_below_the_smallest_normal_number(T, kernel, exponent, ts):
+    """There every operation on a sum rounds to half of 2^-149: two of a warp's stage, up to 4 stages a warp and 16 warps or 8
+    parts joined, two of the tensor scale."""
+    N, K = shape(T, kernel, "nvfp4")
+    w = a_weight(N, K, "nvfp4", 4)
+    w.ts.fill_(ts)
+    w.scales.fill_(0x01)
+    x = (torch.randn(T, K, generator=torch.Generator(device="cuda").manual_seed(T), device="cuda").double() * 2.0 ** exponent).to(BF)
+    out = moe.linear_fp4(x, w, out_dtype=F32)
+    for i in range(0, N, 1 << 13):
+        m = small.weight64(moe.NvfpTensor(w.codes[i:i + (1 << 13)], w.scales[i:i + (1 << 13)], w.ts))
+        y = x.double() @ m.T * w.ts.double().item()
+        size = x.double().abs() @ m.abs().T * abs(ts)
+        off = 2.0 ** -22 * x.double().abs().amax(1, keepdim=True) * m.abs().sum(1) * abs(ts)
+        assert ((out[:, i:i + (1 << 13)].double() - y).abs() <= 26 * 2.0 ** -150 + (K / 4 + 20) * small.U * size + off).all()
+    assert (out != 0).any()
