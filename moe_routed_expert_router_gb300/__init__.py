@@ -587,10 +587,13 @@ def rotary_turns(dim, base=10000.0, frequencies=None, device="cuda"):
         _refuse(where, f"dim {dim}; a multiple of 16 expected", ERR_UNSUPPORTED_SHAPE)
     if frequencies is None and not 0 < base < math.inf:
         _refuse(where, f"base {base}")
-    freqs = [base ** (-2.0 * i / dim) for i in range(dim // 2)] if frequencies is None else [float(f) for f in frequencies]
+    try:
+        freqs = [base ** (-2.0 * i / dim) for i in range(dim // 2)] if frequencies is None else [float(f) for f in frequencies]
+    except OverflowError:
+        _refuse(where, f"base {base}, whose frequencies pass the largest number")
     if len(freqs) != dim // 2 or not all(math.isfinite(f) for f in freqs):
         _refuse(where, f"{len(freqs)} frequencies for dim {dim}; dim / 2 finite numbers expected")
-    turns = [math.floor(f / (2 * math.pi) * 2.0 ** 64) % 2 ** 64 for f in freqs]
+    turns = [math.floor(math.fmod(f / (2 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64 for f in freqs]      # whole turns drop out exactly
     return torch.tensor([t - 2 ** 64 if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
 
 
