@@ -18,3 +18,19 @@ def test_splits_that_fill_the_shared_memory(T, N, K, dt, fmt):
     out = moe.linear_fp4(x, w, out_dtype=F32)
     check(out, x, w)
     assert torch.equal(moe.linear_fp4(x, w), out.to(dt))
+
+
+def test_weights_past_four_gigabytes():
+    """Code offsets beyond 32 bits: the last rows of a weight of 4.5 GB whose K keeps it on the warp kernel."""
+    K = 65536 - 128
+    N = (1 << 32) // (K // 2) + 5000
+    assert moe.lib().moe_linear_fp4_workspace(moe.WEIGHTS_NVFP4, 3, N, K) == 0
+    codes = torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.full((N, K // 16), 0x38, dtype=torch.uint8, device="cuda")          # 1
+    tail = a_weight(300, K, "nvfp4")
+    codes[-300:], scales[-300:] = tail.codes, tail.scales
+    ts = torch.tensor([0.0173], device="cuda")
+    x = rows(3, K, F16, 5)
+    out = moe.linear_fp4(x, moe.NvfpTensor(codes, scales, ts), out_dtype=F32)
+    assert (out[:, :-300] == 0).all()
+    check(out[:, -300:], x, moe.NvfpTensor(tail.codes, tail.scales, ts))
