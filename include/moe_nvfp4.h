@@ -500,22 +500,25 @@ moe_status moe_head_norm_backward(const void *grad_q, int64_t grad_q_stride, con
  *   weight host struct: codes [N][K/2], scales [N][K/16] (E4M3, none negative) or
  *          [N][K/32], tensor_scale one fp32 (NVFP4; ignored for MXFP4)
  *   out    [T][N] of out_dtype: `dtype` or MOE_DTYPE_F32; overlaps nothing else
- *   workspace: moe_linear_fp4_workspace bytes (0 for most products), 256-byte
- *          aligned, used during the call only
+ *   workspace: moe_linear_fp4_workspace_for(weight_format, dtype, T, N, K) bytes (0
+ *          for most products: NULL then), 256-byte aligned, used during the call only;
+ *          moe_linear_fp4_workspace(weight_format, T, N, K) is enough for either dtype
  * W is not rounded (a value has at most six significant bits and the tensor
  * scale is applied to the sum).  Small products take f16 rows as they are and bf16
  * ones to within 2^-32 of the largest finite magnitude of each of their blocks of
  * 256 (128 for more than 16 tokens) values.  Large ones, those that want a workspace,
  * take rows as integers of 23 bits: to within 2^-22 of the largest finite magnitude
  * of the 16 (MXFP4: 32) values that share a weight's scale or, where that is more, for
- * NVFP4 2^-39 of the row's, for MXFP4 2^-108 of the row's and at most 2^-128.  A row that holds an infinity or a NaN gives what fp32
- * arithmetic gives and leaves the other rows alone.  Sums are taken in a fixed order:
- * equal inputs give equal bits.  Waits inside a launch end after a second; if one ever
- * runs out, out is NaN.
+ * NVFP4 2^-39 of the row's, for MXFP4 2^-108 of the row's and at most 2^-128.  A sum is
+ * finite where it is in fp32 arithmetic, whatever the sizes of rows, scales and tensor
+ * scale.  A row that holds an infinity or a NaN gives what fp32 arithmetic gives and
+ * leaves the other rows alone.  Sums are taken in a fixed order: equal inputs give equal
+ * bits.  Waits inside a launch end after a second; if one ever runs out, out is NaN.
  * N: up to 2^31 - 1025; K: a multiple of 128 up to 65536; x_stride: a multiple of
  * 8, at least K; T: up to 2^20, made for up to 64 (every 32 tokens, of large products
  * every 16, read the weight once, the later ones from cache).  T = 0 is a no-op. */
 size_t moe_linear_fp4_workspace(int32_t weight_format, int32_t T, int32_t N, int32_t K);
+size_t moe_linear_fp4_workspace_for(int32_t weight_format, int32_t dtype, int32_t T, int32_t N, int32_t K);
 moe_status moe_linear_fp4(const void *x, int64_t x_stride, const moe_nvfp4 *weight, int32_t weight_format, int32_t T,
                           int32_t N, int32_t K, int32_t dtype, int32_t out_dtype, void *out, void *workspace,
                           size_t workspace_bytes, void *stream);

@@ -36,7 +36,7 @@ EXPORTS = ["moe_plan_create", "moe_plan_destroy", "moe_route", "moe_forward", "m
            "moe_rms_norm_backward_workspace_for",
            "moe_sorted_rows", "moe_sort_pairs", "moe_dispatch", "moe_combine", "moe_combine_backward",
            "moe_head_norm", "moe_head_norm_backward", "moe_head_norm_backward_workspace",
-           "moe_linear_fp4", "moe_linear_fp4_workspace", "moe_decode_layer", "moe_decode_layer_workspace"]
+           "moe_linear_fp4", "moe_linear_fp4_workspace", "moe_linear_fp4_workspace_for", "moe_decode_layer", "moe_decode_layer_workspace"]
 FMT_E4M3, FMT_E2M1 = 0, 1
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 QUANT_NONE, QUANT_E4M3_128, QUANT_E4M3_ROW, QUANT_MXFP8 = 0, 1, 2, 3
@@ -107,6 +107,7 @@ def lib():
         L.moe_head_norm_backward_workspace.argtypes = [I32, I32, I32, I32, I32]
         L.moe_linear_fp4.argtypes = [P, I64, ctypes.POINTER(Nvfp4), I32, I32, I32, I32, I32, I32, P, P, SZ, P]
         L.moe_linear_fp4_workspace.argtypes = [I32, I32, I32, I32]
+        L.moe_linear_fp4_workspace_for.argtypes = [I32, I32, I32, I32, I32]
         L.moe_decode_layer.argtypes = [P, I32, I32, I32, P, I32, P, I32, I32, I32, I32, P, P, P, I32, P, P, P, I32, P, P, P, P, P, SZ, P]
         L.moe_decode_layer_workspace.argtypes = [I32, I32, I32, I32, I32]
         L.moe_status_string.argtypes = [I32]
@@ -116,7 +117,7 @@ def lib():
             if n not in ("moe_status_string", "moe_version"):
                 getattr(L, n).restype = I32
         L.moe_rms_norm_backward_workspace.restype = L.moe_rms_norm_backward_workspace_for.restype = SZ
-        L.moe_head_norm_backward_workspace.restype = L.moe_linear_fp4_workspace.restype = L.moe_decode_layer_workspace.restype = SZ
+        L.moe_head_norm_backward_workspace.restype = L.moe_linear_fp4_workspace.restype = L.moe_linear_fp4_workspace_for.restype = L.moe_decode_layer_workspace.restype = SZ
         L.moe_sorted_rows.restype = I64
         _lib = L
     return _lib
@@ -732,7 +733,7 @@ def linear_fp4(x, weight: NvfpTensor, out=None, out_dtype=None, stream=None):
     op = _want(out, where, "out", (T, N), to, index)
     handle = _raw_stream(index) if stream is None else _given(where, index, stream, x, codes, scales, ts, out)
     L = lib()
-    n = L.moe_linear_fp4_workspace(fmt, T, N, K) if T * N * K >> 28 else 0       # a smaller product never wants one
+    n = L.moe_linear_fp4_workspace_for(fmt, code, T, N, K) if T * N * K >> 28 else 0       # a smaller product never wants one
     call = L.moe_linear_fp4
     if _devices != 1 and _elsewhere(index):
         call = _there(index, call)

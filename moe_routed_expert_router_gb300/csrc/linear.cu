@@ -399,9 +399,15 @@ moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_E
 
 extern "C" {
 
-size_t moe_linear_fp4_workspace(int32_t weight_format, int32_t T, int32_t N, int32_t K) {
+size_t moe_linear_fp4_workspace_for(int32_t weight_format, int32_t dtype, int32_t T, int32_t N, int32_t K) {
     if (T < 1 || T > kMaxTokens || N < 1 || N > INT32_MAX - 1024 || K < 128 || K > kMaxK || K % 128) return 0;
-    return linear_tc_workspace(weight_format == MOE_WEIGHTS_MXFP4, T, N, K);
+    if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F16) return 0;
+    return linear_tc_workspace(weight_format == MOE_WEIGHTS_MXFP4, dtype == MOE_DTYPE_F16, T, N, K);
+}
+
+size_t moe_linear_fp4_workspace(int32_t weight_format, int32_t T, int32_t N, int32_t K) {
+    return std::max(moe_linear_fp4_workspace_for(weight_format, MOE_DTYPE_BF16, T, N, K),
+                    moe_linear_fp4_workspace_for(weight_format, MOE_DTYPE_F16, T, N, K));
 }
 
 moe_status moe_linear_fp4(const void *x, int64_t x_stride, const moe_nvfp4 *weight, int32_t weight_format, int32_t T,
@@ -414,7 +420,7 @@ moe_status moe_linear_fp4(const void *x, int64_t x_stride, const moe_nvfp4 *weig
         return MOE_ERR_UNSUPPORTED_SHAPE;
     if (T == 0) return MOE_OK;
     const bool mx = weight_format == MOE_WEIGHTS_MXFP4;
-    const size_t ws = linear_tc_workspace(mx, T, N, K);
+    const size_t ws = linear_tc_workspace(mx, dtype == MOE_DTYPE_F16, T, N, K);
     if (!x || !out || !weight->codes || !weight->scales || (!mx && !weight->tensor_scale) || (ws && !workspace) || workspace_bytes < ws)
         return MOE_ERR_INVALID_ARG;
     if (!aligned_to(x, 16) || !aligned_to(weight->codes, 16) || !aligned_to(weight->scales, 16) ||

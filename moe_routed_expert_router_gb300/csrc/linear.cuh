@@ -42,7 +42,7 @@ struct LinearCall {
 };
 
 // Bytes of workspace of the block-scaled tensor-core kernel; 0: the call is not for it.
-size_t linear_tc_workspace(bool mx, int T, int N, int K);
+size_t linear_tc_workspace(bool mx, bool f16, int T, int N, int K);
 cudaError_t launch_linear_tc(const LinearCall &c, cudaStream_t st);
 
 }  // namespace moe

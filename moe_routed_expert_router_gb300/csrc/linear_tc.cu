@@ -648,16 +648,32 @@ template <bool MX> cudaError_t launch_chunk(const LinearCall &c, cudaStream_t st
 
 namespace moe {
 
-size_t linear_tc_workspace(bool mx, int T, int N, int K) {
+size_t linear_tc_workspace(bool mx, bool f16, int T, int N, int K) {
     // a stage is 256 values, and TMA wants rows of scales in whole 16 bytes
     if (T < 1 || N < 1 || K < 1 || K % (mx ? 512 : 256)) return 0;
-    // What the two launches, the filling and the joining cost, 8 us, has to come back from the products.  Graphs, NVFP4 bf16,
-    // here against the warp MMAs: 1 token 8192 x 4096 10.0 us against 7.7, 38912 x 7168 33.3 against 33.9, 100000 x 4096 42.7
-    // against 48.5; 16 tokens 4096 x 4096 11.6 against 9.1, 8192 x 4096 12.0 against 12.6, 100000 x 4096 45 against 80; 32
-    // tokens 2048 x 2048 12.5 against 7.7, 7168 x 2048 11.2 against 11.2, 16384 x 7168 25.7 against 42; 64 tokens 2048 x
-    // 2048 10.8 against 9.3, 7168 x 2048 11.2 against 16.8, 100000 x 4096 103 against 259.
-    const int64_t values = (int64_t)N * K;
-    if (T <= 8 ? values < (int64_t)1 << 28 : T <= 16 ? values < 1 << 25 : values * blocks_of(T, 32) < 1 << 24) return 0;
+    // What the two launches, the filling and the joining cost, 8 us, has to come back from the products.  The warp MMAs take
+    // f16 rows as they are and bf16 ones behind a pass over them, so f16 rows want more work.  In graphs, us, warp MMAs against
+    // here (which is the same for both types, and 0 to 3 % faster for MXFP4):
+    //   tokens, weight        NVFP4 bf16   f16          MXFP4 bf16   f16
+    //   1   16384 x 8192      20.3 22.8    18.7 22.8    18.4 22.3    16.8 22.3
+    //   1   32768 x 8192      33.4 32.5    32.0 32.7    29.8 32.0    28.2 31.8
+    //   1   100003 x 4096     49.5 42.4    48.8 42.3    43.6 40.5    42.9 40.5
+    //   8   32768 x 8192      35.2 33.6    34.4 33.4    31.8 32.1    30.3 32.1
+    //   16  4096 x 4096       9.8  12.7    7.8  12.7    9.6  12.7    7.5  12.7
+    //   16  8192 x 4096       13.8 13.8    11.8 13.9    13.5 13.8    11.6 13.8
+    //   16  8192 x 8192       20.8 18.1    17.7 18.1    20.8 17.8    18.0 17.8
+    //   16  16384 x 7168      27.7 22.4    25.0 22.4    27.7 21.9    25.7 21.8
+    //   17  4096 x 4096       13.6 13.0    9.1  13.0    14.2 13.0    9.7  13.0
+    //   32  8192 x 4096       20.7 15.1    16.8 15.1    21.5 15.1    18.1 15.0
+    //   32  11000 x 4096      23.7 15.3    19.8 15.3    24.8 15.3    21.4 15.2
+    //   64  2048 x 4096       14.0 15.5    9.7  15.6    14.7 15.5    10.3 15.5
+    //   64  7168 x 2048       17.1 11.7    14.8 11.7    18.3 11.7    16.1 11.7
+    //   64  5800 x 4096       23.2 15.8    19.2 15.8    24.4 15.7    20.8 15.8
+    // A call that no graph holds takes the host 4 us more than the other form's (two launches, three tensor maps, the
+    // workspace): where the GPU is faster than the host, bf16 rows between the rule's borders and about twice the work lose them.
+    const int64_t work = (int64_t)N * K * (T <= 16 ? 1 : blocks_of(T, 32));
+    const int64_t least = T <= 8 ? (f16 && mx ? (int64_t)3 << 27 : (int64_t)1 << 28) : T <= 16 ? (f16 ? 3 << 25 : 1 << 25) : (f16 ? 5 << 23 : 1 << 24);
+    if (work < least) return 0;
     size_t n = layout_of(mx, std::min(T, kChunkTokens), N, K).bytes;
     if (T % kChunkTokens) n = std::max(n, layout_of(mx, T % kChunkTokens, N, K).bytes);   // may have more parts
     return n;
