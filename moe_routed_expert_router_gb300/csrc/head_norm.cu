@@ -254,17 +254,18 @@ __global__ void __launch_bounds__(kThreads) k_head_norm(HeadArgs a) {
     // a' = rstd (a (cos wa) - b (sin wb)),  b' = rstd (b (cos wb) + a (sin wa))
     float wa[8], wb[8], ca[8], cb[8], sa[8], sb[8];
     {
-        to_planes<DT, kPairs>(wr, wa, wb);
         const Angles r = angles_of<DT, kPairs>(a, l, cs, n);
+        to_planes<DT, kPairs>(wr, wa, wb);
         mul8(ca, wa, r.c);
         mul8(cb, wb, r.c);
-        mul8(sa, wa, r.s);
-        mul8(sb, wb, r.s);
-        scale8(sb, -1.0f);
-        if (kRest && !l.turned) {          // whatever the weight is
+        if (!kRest || l.turned) {          // else nothing of the other value, whatever the weight is
+            mul8(sa, wa, r.s);
+            mul8(sb, wb, r.s);
+        } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) sa[i] = sb[i] = 0.0f;
         }
+        scale8(sb, -1.0f);
     }
     for (int base = 0; base < h.heads; base += U * l.heads) {
         if (base > 0) fetch();
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(kThreads) k_head_norm(HeadArgs a) {
         }
         // A row with an infinity has an rstd of 0.  Where values are not rotated, 0 (a sine) times the infinity has reached
         // its place's other value above; they are written again, each by itself: 0, the infinity's own NaN.  (4096 x 40 heads
-        // of 128, 64 turned: 16.9 us, without this 16.5; with a branch around the sines' products instead 18.8.  Rows that are
+        // of 128, 64 turned: 16.8 us, without this 16.5; with a branch around the sines' products instead 18.8.  Rows that are
         // rotated whole have no such values.)
         if (kRest && least == 0.0f && !l.turned) {
 #pragma unroll
