@@ -456,7 +456,7 @@ template <bool MX> __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(co
             const int n0 = it.group * 256 + quad * 32 + lane;
             int2 info = make_int2(0, 0);                           // lane j: token j's
             if (lane < tokens) info = a.info[t0 + lane];
-            const float own_first = first_factor(info.x + power), own_second = second_factor(info.x + power);
+            const float own_first = first_factor(info.x + power), own_second = second_factor(info.x + power);   // MXFP4: one is enough
             if (ok) ok = mbar_wait(acc_full, aph, err);
             aph ^= 1;
             tc_fence_after();
@@ -484,7 +484,7 @@ template <bool MX> __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(co
             if (lane == 0) mbar_arrive(acc_empty);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float first = __shfl_sync(0xffffffffu, own_first, j), second = __shfl_sync(0xffffffffu, own_second, j);
+                const float first = __shfl_sync(0xffffffffu, own_first, j), second = MX ? 1.0f : __shfl_sync(0xffffffffu, own_second, j);
                 const bool bad = __shfl_sync(0xffffffffu, info.y, j) != 0;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
