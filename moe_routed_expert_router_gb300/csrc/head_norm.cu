@@ -23,11 +23,11 @@
 // a place in the row give (sines, cosines, weights, and in the forward pass their
 // products) is in registers and a row costs its own arithmetic only, in packed fp32.
 //
-// Bound by HBM, reading and writing every row once: bf16 4096 x 72 heads of 128 26.1
-// us (5.8 TB/s, 87 % of the copy bandwidth; with four rows a thread at once 30), fp32
-// 8192 x 40 53 us (94 %); backward 8192 x 36 42.3 us (80 %), fp32 8192 x 40 83 us (90
+// Bound by HBM, reading and writing every row once: bf16 4096 x 72 heads of 128 26.2
+// us (5.8 TB/s, 86 % of the copy bandwidth; with four rows a thread at once 30), fp32
+// 8192 x 40 53 us (94 %); backward 8192 x 36 42.8 us (79 %), fp32 8192 x 40 82 us (91
 // %).  Rows whose values are not a power of two leave lanes idle (28 + 4 heads of 80:
-// 59 and 52 %).
+// 58 and 52 %).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

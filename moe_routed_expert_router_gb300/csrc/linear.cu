@@ -24,14 +24,16 @@
 // a time, with a cp.async ring of its own, so that neither tokens nor weights pass
 // between warps and no barrier stops the stream.  The warps' sums of a pass over
 // the rows are joined in shared memory in a fixed order.  (Tokens in shared memory,
-// whole or in chunks with a barrier each: 16 x 16384 x 7168 31 to 41 us against 27.)
+// whole or in chunks with a barrier each: 31 to 41 us against 27 at 16 x 16384 x 7168,
+// before linear_tc.cu had that size.)
 //
-// Measured: 1 x 38912 x 7168 NVFP4 33.9 us (0.69 of the copy bandwidth), 1 x 16384 x 7168 18.8, 4 x 4096 x 4096 5.5.  With
-// all data in shared memory a sub-partition needs 39 cycles for 16 rows x 32 values and eight tokens (the eight code
-// conversions 23 of them, the two MMAs 21 beside them; codes widened by shifts and masks instead 44), 27 us of the 48 that
-// 1 x 100000 x 4096 takes; 65 are spent: four warps do not hide each other's chains of load, conversion, product and MMA.
-// Each eight tokens more add two MMAs, so from 16 tokens on the warp MMAs are the limit, not the bytes: large products go
-// to linear_tc.cu.
+// Measured in graphs, us (share of the copy bandwidth): 4 x 4096 x 4096 NVFP4 bf16 6.3, f16 5.6, MXFP4 bf16 6.2, f16 5.3; 1 x
+// 16384 x 7168 18.9 (0.52), 17.3, 17.1 (0.55), 15.6; 1 x 32760 x 8192 33.4 (0.67), 32.0, 29.8 (0.71), 28.3; 16 x 4096 x 4096
+// 9.8, 7.8, 9.6, 7.5.  With all data in shared memory a sub-partition needs 39 cycles for 16 rows x 32 values and eight tokens
+// (the eight code conversions 23 of them, the two MMAs 21 beside them; codes widened by shifts and masks instead 44), 16 us of
+// the 33 that 1 x 32760 x 8192 takes: four warps do not hide each other's chains of load, conversion, product and MMA.  Each
+// eight tokens more add two MMAs, so from 16 tokens on the warp MMAs are the limit, not the bytes: large products go to
+// linear_tc.cu.
 #include "linear.cuh"
 #include "linear_split.cuh"
 

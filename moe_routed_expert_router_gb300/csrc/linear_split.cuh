@@ -22,7 +22,7 @@ constexpr int linear_tokens(int T) { return T <= 8 ? 1 : T <= 16 ? 2 : 4; }
 constexpr int linear_stage_k(int nt) { return nt >= 4 ? 128 : 256; }
 // Warps of a block: what the tokens' registers leave room for.
 constexpr int linear_warps(int nt) { return nt == 1 ? 16 : 12; }
-constexpr int kLinearRows = 16;            // rows a tile (32: 53.1 us for 1 x 100003 x 4096 against 47.1, the sums' place taken from the ring)
+constexpr int kLinearRows = 16;            // rows a tile (32 took the sums' place from the ring: 53 us against 47 at 1 x 100003 x 4096, before linear_tc.cu had that size)
 constexpr int kScaleBytes = 16;            // a row's place for a stage's scales (MXFP4 uses half)
 constexpr int kCodePad = 16;               // behind a row's codes: eight rows' equal words lie in different banks
 constexpr int kLeastLinearRing = 2, kMostLinearRing = 6;

@@ -20,11 +20,12 @@
 // weights while the digits are still being written.  An item is 256 weight rows (the M side, two accumulators of 128) x 16
 // tokens x a part of K; the parts of an item are a cluster's blocks, each of which adds a share of the rows, in order.
 //
-// Bound by the weight's bytes where there are enough of them: 1 x 100003 x 4096 NVFP4 42.8 us (0.80 of the copy bandwidth),
-// 16 x 100000 x 4096 45.5 (0.77), 16 x 38912 x 7168 38 (0.62), 16 x 16384 x 7168 MXFP4 21.6 (0.44; the warp MMAs of linear.cu
-// 27.4).  The stream itself runs at 5 to 6 TB/s; about 8 us are outside it: digits, the first token tile, joining and
-// storing.  Every 16 tokens more read weights and digits from L2, 54 KB a stage in 0.53 us, near what an SM takes from it:
-// 64 x 38912 x 7168 67 us (197).
+// Bound by the weight's bytes where there are enough of them: 1 x 100003 x 4096 NVFP4 42.9 us (0.80 of the copy bandwidth),
+// 16 x 100000 x 4096 45.5 (0.76), 16 x 38912 x 7168 37.9 (0.62), 16 x 16384 x 7168 MXFP4 21.9 (0.43; the warp MMAs of linear.cu
+// 27.7).  About 8 us are outside the stream (digits, the first token tile, joining and storing), which itself runs at 4.5 TB/s
+// (16 x 16384 x 7168) to 6.6 (1 x 100003 x 4096).  Every 16 tokens more read weights and digits from L2, 54 KB a stage in 0.53
+// us, near what an SM takes from it: 64 x 38912 x 7168 67 us.  Tokens go in pieces of 256 (256 x 16384 x 7168 111 us, 1024 x
+// 16384 x 7168 443), so this is not made for prompts.
 // Tried, 16 x 16384 x 7168: digits made in the multiplying blocks by the warps of the epilogue 30 us (each block makes all of
 // them again, 1.5 us a stage); rings of their own for weights, five stages, and digits, two, 22.2; groups of 216 rows that
 // fill all SMs instead of 128 of them 25.0 (the next launch's blocks find no room beside the last ones).
